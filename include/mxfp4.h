@@ -64,7 +64,8 @@ typedef enum {
     MXFP4_ERR_UNSUPPORTED_DEVICE = 3, /* current device is not compute capability 10.3    */
     MXFP4_ERR_CUDA = 4,               /* a CUDA runtime/driver call or a launch failed    */
     MXFP4_ERR_TIMEOUT = 5,            /* a kernel's bounded wait ran out (device word)    */
-    MXFP4_ERR_NONFINITE = 6           /* a tensorwise FP8 amax was NaN or inf (device word) */
+    MXFP4_ERR_NONFINITE = 6,          /* a tensorwise FP8 amax was NaN or inf (device word) */
+    MXFP4_ERR_GROUPS = 7              /* group offsets or a row index out of range (device word) */
 } mxfp4_status;
 
 typedef enum { MXFP4_SCALE_PLAIN = 0, MXFP4_SCALE_TC = 1 } mxfp4_scale_layout;
@@ -405,6 +406,65 @@ typedef struct {
 mxfp4_status mxfp4_fp8_gemm_batch(int32_t count, const mxfp4_fp8_gemm_task* tasks,
                                   mxfp4_stream_t stream);
 
+/* ---- linears grouped by expert ---------------------------------------------------------
+ * The MXFP4 linear of a mixture-of-experts layer: E experts with weights W_e[N, K], and rows
+ * of X that the routing sent to them.  The rows of G (the gathered X, `rows` of them) are
+ * ordered by expert; group e is rows offsets[e] .. offsets[e+1] of G, may be of any size, and
+ * only the device knows the sizes: no call reads them on the host.
+ *
+ *   Y_e = X_e . W_e^T        mxfp4_quantize_grouped of X and of W, mxfp4_gemm_grouped FWD
+ *   dX_e = dY_e . W_e        mxfp4_quantize_grouped of dY, DGRAD
+ *   dW_e = dY_e^T . X_e      WGRAD
+ *
+ * offsets: int32[groups + 1] in device memory, nondecreasing within [0, rows]; rows outside
+ * offsets[0] .. offsets[groups] belong to no group.  offsets == NULL: `groups` equal groups of
+ * rows / groups rows (the weights: groups of N rows).  Offsets or a row index that break their
+ * range are clamped (a bad index reads as a zero row), so nothing outside the buffers is
+ * touched, and mxfp4_last_device_error reports MXFP4_ERR_GROUPS.
+ *
+ * Grouped blobs.  P_e = 128 * sum over f < e of ceil(m_f / 128) is the padded row at which
+ * group e starts, m_e its size; capacity = the most padded rows that `rows` rows in `groups`
+ * groups can need: 128 * floor((rows + 127 min(groups, rows)) / 128), or, for equal groups,
+ * groups * ceil(rows / groups / 128) * 128.
+ *   row blob   q_row[rows, Kp/2]: row i of G, blocks of 32 along K, no padding between groups;
+ *              s_row: MXFP4_SCALE_TC for (capacity, K), row i of group e at P_e + i - offsets[e];
+ *              what it holds at padding rows is unspecified and never used.
+ *   col blob   q_col[K, capacity/2], s_col: MXFP4_SCALE_TC for (K, capacity): the col blob of
+ *              the matrix whose rows P_e .. P_e + m_e are group e and whose other rows are +0.
+ *              Written (padding included) up to the last group's end, P_E. */
+#define MXFP4_MAX_GROUPS 1024
+
+typedef enum { MXFP4_GROUPED_FWD = 0, MXFP4_GROUPED_DGRAD = 1, MXFP4_GROUPED_WGRAD = 2 } mxfp4_grouped_form;
+
+/* Bytes of the four buffers of the grouped blobs of G[rows, k], and the capacity in rows;
+ * `equal` nonzero: for offsets == NULL.  Any output pointer may be NULL.  rows >= 0 (a multiple
+ * of groups when equal), k >= 1, groups in 1..MXFP4_MAX_GROUPS, else MXFP4_ERR_INVALID_ARG. */
+mxfp4_status mxfp4_grouped_sizes(int64_t rows, int64_t k, int64_t groups, int32_t equal, size_t* q_row,
+                                 size_t* s_row, size_t* q_col, size_t* s_col, int64_t* capacity);
+
+/* Grouped quantizer: the blobs of G, G[i] = X[row_index[i]], or X[i] when row_index is NULL
+ * (then x_rows >= rows), by the rules of mxfp4_quantize / mxfp4_quantize_dual.
+ *   x          bf16 X[x_rows, K], row pitch ldx elements (ldx >= K, ldx % 8 == 0), 16-byte aligned
+ *   row_index  int32[rows] in device memory (4-byte aligned), each in [0, x_rows), or NULL
+ *   q_col, s_col   both NULL: the row blob only
+ * rows == 0 does nothing. */
+mxfp4_status mxfp4_quantize_grouped(const void* x, int64_t x_rows, int64_t K, int64_t ldx, const int32_t* row_index,
+                                    const int32_t* offsets, int64_t groups, int64_t rows, void* q_row, void* s_row,
+                                    void* q_col, void* s_col, mxfp4_stream_t stream);
+
+/* The products of all groups in one launch, over blobs of mxfp4_quantize_grouped (those of X
+ * and dY with `offsets`, those of W with offsets NULL and groups * N rows):
+ *   FWD    a: row blob of X [rows, K], b: row blob of W; c[rows, N], ldc >= N
+ *   DGRAD  a: row blob of dY [rows, N], b: col blob of W; c[rows, K], ldc >= K
+ *   WGRAD  a: col blob of dY, b: col blob of X; c[groups * N, K], ldc >= K: a group without rows
+ *          gets zeros
+ * Rows of c outside every group are not written.  Accumulation, rounding and alignment as for
+ * mxfp4_gemm.  rows == 0: FWD and DGRAD do nothing, WGRAD writes zeros (a and b are not read
+ * and may be NULL). */
+mxfp4_status mxfp4_gemm_grouped(mxfp4_grouped_form form, const void* a_q, const void* a_s, const void* b_q,
+                                const void* b_s, const int32_t* offsets, int64_t groups, int64_t rows, int64_t N,
+                                int64_t K, void* c, int64_t ldc, mxfp4_out_dtype out_dtype, mxfp4_stream_t stream);
+
 /* ---- a step from host memory to host memory -------------------------------------------
  * The data path of `MXFP4LinearFunction` (primus_turbo_mxfp4_local.py) for linears whose
  * bf16 inputs and results live in host memory: per linear, forward = dual (train) or
@@ -477,8 +537,8 @@ mxfp4_status mxfp4_linear_host_wait(mxfp4_stream_t stream);
 
 /* Synchronizes `stream`, then reads and clears the device error word of the current
  * device: MXFP4_ERR_TIMEOUT if a bounded wait in any kernel of this library ran out
- * since the last call, else MXFP4_ERR_NONFINITE if a tensorwise FP8 quantization met a
- * non-finite amax; MXFP4_ERR_CUDA if the synchronization itself failed; else OK. */
+ * since the last call, else MXFP4_ERR_GROUPS if a grouped call met offsets or a row index out
+ * of range, else MXFP4_ERR_NONFINITE if a tensorwise FP8 quantization met a non-finite amax; MXFP4_ERR_CUDA if the synchronization itself failed; else OK. */
 mxfp4_status mxfp4_last_device_error(mxfp4_stream_t stream);
 
 /* Diagnostic for the bounded-wait machinery: launches one warp that waits on a barrier

@@ -19,6 +19,7 @@ MXFP4_ERR_UNSUPPORTED_DEVICE = 3
 MXFP4_ERR_CUDA = 4
 MXFP4_ERR_TIMEOUT = 5
 MXFP4_ERR_NONFINITE = 6
+MXFP4_ERR_GROUPS = 7
 
 MXFP4_SCALE_PLAIN = 0
 MXFP4_SCALE_TC = 1
@@ -31,6 +32,11 @@ MXFP4_MAX_BATCH = 4
 MXFP4_TILES_AUTO = 0
 MXFP4_TILES_NARROW = 1
 MXFP4_TILES_WIDE = 2
+
+MXFP4_MAX_GROUPS = 1024
+MXFP4_GROUPED_FWD = 0
+MXFP4_GROUPED_DGRAD = 1
+MXFP4_GROUPED_WGRAD = 2
 
 
 class GemmTask(ctypes.Structure):
@@ -94,6 +100,9 @@ EXPORTED = (
     "mxfp4_fp8_quantize_tw_batch",
     "mxfp4_fp8_gemm",
     "mxfp4_fp8_gemm_batch",
+    "mxfp4_grouped_sizes",
+    "mxfp4_quantize_grouped",
+    "mxfp4_gemm_grouped",
     "mxfp4_linear_workspace_bytes",
     "mxfp4_linear_step_host",
     "mxfp4_linear_pipelined_workspace_bytes",
@@ -146,6 +155,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_fp8_quantize_tw_batch.argtypes = [i32, ctypes.POINTER(Fp8QuantizeTask), vp]
     lib.mxfp4_fp8_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i64, i32, vp]
     lib.mxfp4_fp8_gemm_batch.argtypes = [i32, ctypes.POINTER(Fp8GemmTask), vp]
+    szp = ctypes.POINTER(ctypes.c_size_t)
+    lib.mxfp4_grouped_sizes.argtypes = [i64, i64, i64, i32, szp, szp, szp, szp, ctypes.POINTER(i64)]
+    lib.mxfp4_quantize_grouped.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp]
+    lib.mxfp4_gemm_grouped.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, i32, vp]
     lib.mxfp4_linear_workspace_bytes.argtypes = [i32, ctypes.POINTER(LinearHostTask),
                                                  ctypes.POINTER(ctypes.c_size_t)]
     lib.mxfp4_linear_step_host.argtypes = [i32, ctypes.POINTER(LinearHostTask), vp, ctypes.c_size_t, vp]
@@ -358,6 +371,29 @@ def mxfp4_fp8_gemm_batch(tasks, stream=None) -> None:
     _check(load().mxfp4_fp8_gemm_batch(len(tasks), arr, _stream(stream)), "mxfp4_fp8_gemm_batch")
 
 
+def mxfp4_grouped_sizes(rows: int, k: int, groups: int, equal: bool = False) -> Tuple[int, int, int, int, int]:
+    """Bytes of q_row, s_row, q_col, s_col of the grouped blobs of G[rows, k], and the capacity in
+    padded rows; equal: groups of rows / groups rows (offsets None)."""
+    out = [ctypes.c_size_t() for _ in range(4)]
+    cap = ctypes.c_int64()
+    _check(load().mxfp4_grouped_sizes(rows, k, groups, int(bool(equal)), *[ctypes.byref(o) for o in out],
+                                      ctypes.byref(cap)), "mxfp4_grouped_sizes")
+    return (*[o.value for o in out], cap.value)
+
+
+def mxfp4_quantize_grouped(x, x_rows, K, ldx, row_index, offsets, groups, rows, q_row, s_row, q_col=None,
+                           s_col=None, stream=None) -> None:
+    _check(load().mxfp4_quantize_grouped(_ptr(x), x_rows, K, ldx, _ptr(row_index), _ptr(offsets), groups, rows,
+                                         _ptr(q_row), _ptr(s_row), _ptr(q_col), _ptr(s_col), _stream(stream)),
+           "mxfp4_quantize_grouped")
+
+
+def mxfp4_gemm_grouped(form, a_q, a_s, b_q, b_s, offsets, groups, rows, N, K, c, ldc, out_dtype=MXFP4_OUT_BF16,
+                       stream=None) -> None:
+    _check(load().mxfp4_gemm_grouped(form, _ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), groups, rows,
+                                     N, K, _ptr(c), ldc, out_dtype, _stream(stream)), "mxfp4_gemm_grouped")
+
+
 def _host_tasks(tasks):
     """tasks: sequence of (x, w, dy, y, dx, dw, M, N, K, train, out_dtype) with host
     buffers (tensors or addresses; dy, dx, dw may be None when train is 0)."""
@@ -483,6 +519,35 @@ def gemm(a_q, a_s, b_q, b_s, M, N, K, out_dtype=None, out=None, stream=None, bia
         assert bias.dtype == torch.bfloat16 and bias.is_contiguous() and bias.numel() == N
         mxfp4_gemm_bias(a_q, a_s, b_q, b_s, M, N, K, bias, out, out.stride(0), code, stream)
     return out
+
+
+def alloc_grouped_blobs(rows: int, k: int, groups: int, equal: bool = False, dual: bool = True, device="cuda"):
+    """Uninitialised (q_row, s_row[, q_col, s_col]) uint8 buffers of the grouped blobs of G[rows, k]."""
+    import torch
+    qr, sr, qc, sc, cap = mxfp4_grouped_sizes(rows, k, groups, equal)
+
+    def buf(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+
+    row = (buf(rows, qr // max(rows, 1)), buf(sr))
+    return row + (buf(k, cap // 2), buf(sc)) if dual else row
+
+
+def quantize_grouped(x, offsets=None, row_index=None, groups=None, rows=None, dual: bool = True, stream=None):
+    """Grouped blobs (row_q, row_s[, col_q, col_s]) of the rows of bf16 X[T, K] (CUDA, row pitch a
+    multiple of 8) that row_index (int32) gathers, or of X's own rows, in groups by the int32 CUDA
+    `offsets` (groups + 1 of them), or in `groups` equal groups when offsets is None."""
+    import torch
+    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
+    for t in (offsets, row_index):
+        assert t is None or (t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.is_cuda)
+    groups = groups if offsets is None else offsets.numel() - 1
+    rows = rows if rows is not None else (x.shape[0] if row_index is None else row_index.numel())
+    assert row_index is None or row_index.numel() >= rows
+    blobs = alloc_grouped_blobs(rows, x.shape[1], groups, offsets is None, dual, x.device)
+    mxfp4_quantize_grouped(x, x.shape[0], x.shape[1], x.stride(0), row_index, offsets, groups, rows,
+                           *(blobs if dual else blobs + (None, None)), stream)
+    return blobs
 
 
 def fp8_pitch(n: int) -> int:

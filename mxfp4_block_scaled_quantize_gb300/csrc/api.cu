@@ -387,6 +387,20 @@ mxfp4_status fp8_gemm_fill(const mxfp4_fp8_gemm_task& t, DeviceState* dev, mxfp4
 }  // namespace
 
 namespace mxfp4 {
+int device_info(int* sms, uint32_t** err) {
+    DeviceState* dev = nullptr;
+    const mxfp4_status st = device_ready(&dev);
+    if (st != MXFP4_OK) return st;
+    *sms = dev->sms;
+    *err = dev->err;
+    return MXFP4_OK;
+}
+
+bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+    return encode_2d(map, type, base, inner, outer, row_bytes, box_inner, box_outer, swizzle);
+}
+
 cudaError_t launch_selftest_wait(uint32_t* err, uint64_t timeout_ns, cudaStream_t stream) {
     selftest_wait_kernel<<<1, 32, 0, stream>>>(err, timeout_ns);
     return cudaGetLastError();
@@ -728,7 +742,8 @@ mxfp4_status mxfp4_last_device_error(mxfp4_stream_t stream) {
     if (word != 0) {
         const uint32_t zero = 0;
         if (cudaMemcpy(dev->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return MXFP4_ERR_CUDA;
-        return (word & mxfp4::kErrWaitBits) ? MXFP4_ERR_TIMEOUT : MXFP4_ERR_NONFINITE;
+        if (word & mxfp4::kErrWaitBits) return MXFP4_ERR_TIMEOUT;
+        return (word & mxfp4::kErrGroups) ? MXFP4_ERR_GROUPS : MXFP4_ERR_NONFINITE;
     }
     return MXFP4_OK;
 }
@@ -755,6 +770,8 @@ const char* mxfp4_status_string(mxfp4_status status) {
         case MXFP4_ERR_TIMEOUT: return "MXFP4_ERR_TIMEOUT: a kernel's bounded wait ran out";
         case MXFP4_ERR_NONFINITE:
             return "MXFP4_ERR_NONFINITE: a tensorwise FP8 quantization met a NaN or infinite input";
+        case MXFP4_ERR_GROUPS:
+            return "MXFP4_ERR_GROUPS: group offsets decrease or leave the rows, or a row index lies outside X";
     }
     return "MXFP4: unknown status";
 }

@@ -33,6 +33,7 @@
 #include "epilogue.cuh"
 #include "launch.h"
 #include "mx_encode.cuh"
+#include "pair_common.cuh"
 #include "ptx.cuh"
 
 namespace mxfp4 {
@@ -46,8 +47,6 @@ constexpr uint32_t kBarHandoff = 1;
 constexpr uint32_t kBarEpilogue = 2;
 constexpr uint32_t kBarStore0 = 3;        // wide: + column group h, the group's four warps
 constexpr uint32_t kTmemCols = 512;
-constexpr int kOutRowBytes = 64;
-constexpr int kOutBytes = 32 * kOutRowBytes;
 
 // Tile shapes.  Narrow: 256 x 256 tiles, one N 256 MMA per K slice, five stages.  Wide:
 // 256 x 384 tiles, per K slice an N 256 MMA (tile columns 0..255, accumulator columns
@@ -98,32 +97,6 @@ struct PairSmem {
     uint32_t tmem_base;
     int abort;
 };
-
-// tcgen05.mma kind::mxf4 instruction descriptor, M = 256 (the pair), N = n.
-__device__ __forceinline__ uint32_t pair_idesc(uint32_t sf_id, uint32_t n) {
-    uint32_t d = 0;
-    d |= sf_id << 4;
-    d |= 1u << 7;
-    d |= 1u << 10;
-    d |= (n >> 3) << 17;
-    d |= 1u << 23;
-    d |= static_cast<uint32_t>(256 >> 4) << 24;
-    d |= sf_id << 29;
-    return d;
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ uint32_t swz64(uint32_t r, uint32_t j) {
-    return r * kOutRowBytes + ((j ^ ((r >> 1) & 3u)) << 4);
-}
 
 // Four 8 x 8 bf16 matrices from shared memory, transposed: lanes 8j .. 8j + 7 give the
 // addresses of the 8 rows (16 bytes each) of matrix j, and lane t receives in d[j] the

@@ -146,6 +146,60 @@ int gemm_pair_max_clusters(bool wide);   // co-resident clusters of the pair ker
 // wide: 256 x 384 tiles; every problem bf16 out through TMA stores (c_tma).
 cudaError_t launch_gemm_pair(const GemmPairBatch& b, int clusters, cudaStream_t stream, bool quant, bool wide);
 
+// ---- linears grouped by expert -----------------------------------------------------------
+constexpr int kMaxGroups = 1024;   // MXFP4_MAX_GROUPS
+
+struct GroupedQuantArgs {
+    const uint16_t* x;          // bf16 X[x_rows, K], row pitch ldx
+    int64_t ldx;
+    int64_t K;
+    int32_t x_rows;
+    int32_t rows;               // rows of G
+    const int32_t* row_index;   // X's row of each row of G, or null: the same row
+    const int32_t* offsets;     // groups + 1 offsets into G, or null: equal groups
+    int32_t groups;
+    int32_t tiles_k;            // Kp / 128
+    int32_t tiles_r;            // capacity of group-padded rows / 128: pitch of the col blob
+    uint8_t* q_row;
+    uint8_t* s_row;
+    uint8_t* q_col;             // null: row blob only
+    uint8_t* s_col;
+    int64_t ldq_row;            // Kp / 2
+    int64_t ldq_col;            // capacity / 2
+    uint32_t* err;
+};
+cudaError_t launch_quantize_grouped(const GroupedQuantArgs& a, int sms, cudaStream_t stream);
+
+// Operand maps as for the narrow pair kernel, over all groups' rows or padded rows at once;
+// cmap: C, box {64 bytes of columns, 32 rows}, 64-byte swizzle, read when c_tma.
+struct GroupedGemmArgs {
+    CUtensorMap amap, bmap, sfamap, sfbmap, cmap;
+    const int32_t* offsets;
+    int32_t groups;
+    int32_t rows;               // rows of G
+    int32_t atoms;              // forward, dgrad: Kp / 128
+    int32_t tiles_m;            // wgrad: ceil(m_rows / 256)
+    int32_t tiles_n;            // ceil(n_cols / 256)
+    int32_t b_step_rows;        // from one group's B to the next: rows of the elements,
+    int32_t b_step_groups;      // 128-row scale groups (forward),
+    int32_t b_step_atoms;       // atoms along the packed axis (dgrad)
+    int64_t m_rows;             // wgrad: rows of a group's output
+    int64_t n_cols;             // output columns
+    void* c;
+    int64_t ldc;
+    int32_t out_f32;
+    int32_t c_tma;
+    uint32_t* err;
+};
+int gemm_grouped_max_clusters();   // co-resident clusters, 0 if none
+cudaError_t launch_gemm_grouped(const GroupedGemmArgs& a, bool wgrad, int clusters, cudaStream_t stream);
+
+// ---- host helpers of the C ABI (api.cu) ----------------------------------------------------
+// The current device's SM count and error word; an mxfp4_status.
+int device_info(int* sms, uint32_t** err);
+bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
 // ---- diagnostics -----------------------------------------------------------------------
 cudaError_t launch_selftest_wait(uint32_t* err, uint64_t timeout_ns, cudaStream_t stream);
 

@@ -22,6 +22,7 @@ enum : uint32_t {
     kErrGemmDrain = 1u << 5,
     kErrSelftest = 1u << 6,
     kErrNonFinite = 1u << 7,   // not a wait: a tensorwise FP8 amax was NaN or inf
+    kErrGroups = 1u << 8,      // not a wait: group offsets or a row index out of range
 };
 constexpr uint32_t kErrWaitBits = kErrNonFinite - 1;
 

@@ -1,0 +1,129 @@
+"""Host-side checks of the grouped linear that need no GPU: sizes, refusals, and the group
+table's arithmetic restated in Python."""
+import ctypes
+
+import pytest
+
+from mxfp4_block_scaled_quantize_gb300 import abi
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    return abi.load()
+
+
+def test_capacity_holds_every_split(lib):
+    import itertools
+    for rows, groups in ((1, 1), (3, 2), (129, 2), (130, 3), (256, 3), (5, 4)):
+        cap = abi.mxfp4_grouped_sizes(rows, 32, groups)[4]
+        most = 0
+        for cuts in itertools.combinations_with_replacement(range(rows + 1), groups - 1):
+            edges = (0, *cuts, rows)
+            most = max(most, sum((b - a + 127) // 128 * 128 for a, b in zip(edges, edges[1:])))
+        assert most == cap, (rows, groups)   # enough for any split, and some split needs it
+
+
+def test_sizes(lib):
+    # 300 rows in 4 ragged groups: floor((300 + 127 * 4) / 128) = 6 tiles
+    assert abi.mxfp4_grouped_sizes(300, 100, 4) == (300 * 64, 768 * 4, 100 * 384, 128 * 24, 768)
+    # equal groups of 75 rows: one tile each
+    assert abi.mxfp4_grouped_sizes(300, 100, 4, True)[4] == 512
+    assert abi.mxfp4_grouped_sizes(0, 100, 4) == (0, 0, 0, 0, 0)
+    for bad in ((-1, 8, 1, 0), (4, 0, 1, 0), (4, 8, 0, 0), (4, 8, 1025, 0), (5, 8, 2, 1), (2**31, 8, 1, 0)):
+        with pytest.raises(abi.Mxfp4Error) as e:
+            abi.mxfp4_grouped_sizes(*bad)
+        assert e.value.status == abi.MXFP4_ERR_INVALID_ARG
+
+
+def test_quantize_refusals(lib):
+    bad, mis = abi.MXFP4_ERR_INVALID_ARG, abi.MXFP4_ERR_MISALIGNED
+    # x, x_rows, K, ldx, row_index, offsets, groups, rows, q_row, s_row, q_col, s_col, stream
+    ok = [16, 8, 8, 8, 32, 64, 2, 8, 48, 80, 96, 112, None]
+
+    def call(**change):
+        names = ["x", "x_rows", "K", "ldx", "row_index", "offsets", "groups", "rows", "q_row", "s_row", "q_col", "s_col"]
+        a = list(ok)
+        for k, v in change.items():
+            a[names.index(k)] = v
+        return lib.mxfp4_quantize_grouped(*a)
+
+    assert call(x=None) == bad and call(q_row=None) == bad and call(s_row=None) == bad
+    assert call(q_col=None) == bad and call(s_col=None) == bad          # both or neither
+    assert call(K=0) == bad and call(ldx=0) == bad and call(rows=-1) == bad and call(x_rows=-1) == bad
+    assert call(groups=0) == bad and call(groups=1025) == bad
+    assert call(row_index=None, x_rows=7) == bad                         # fewer rows than G without an index
+    assert call(offsets=None, rows=7) == bad                             # equal groups of 3.5 rows
+    assert call(x=24) == mis and call(ldx=12) == mis and call(q_row=40) == mis and call(s_row=88) == mis
+    assert call(q_col=100) == mis and call(s_col=104) == mis and call(row_index=34) == mis and call(offsets=66) == mis
+
+
+def test_gemm_refusals(lib):
+    bad, mis = abi.MXFP4_ERR_INVALID_ARG, abi.MXFP4_ERR_MISALIGNED
+    names = ["form", "a_q", "a_s", "b_q", "b_s", "offsets", "groups", "rows", "N", "K", "c", "ldc", "out_dtype"]
+    ok = [0, 16, 32, 48, 64, 80, 2, 8, 8, 24, 96, 24, 0, None]
+
+    def call(**change):
+        a = list(ok)
+        for k, v in change.items():
+            a[names.index(k)] = v
+        return lib.mxfp4_gemm_grouped(*a)
+
+    assert call(form=3) == bad and call(form=-1) == bad
+    for p in ("a_q", "a_s", "b_q", "b_s", "c"):
+        assert call(**{p: None}) == bad and call(**{p: 24}) == mis
+    assert call(groups=0) == bad and call(rows=-1) == bad and call(N=0) == bad and call(K=0) == bad
+    assert call(ldc=7) == bad                        # forward: at least N
+    assert call(form=1, ldc=23) == bad and call(form=2, ldc=23) == bad   # gradients: at least K
+    assert call(out_dtype=2) == bad and call(offsets=82) == mis
+    assert call(offsets=None, rows=7) == bad
+    assert call(groups=1024, N=2**22) == bad         # more weight rows than coordinates
+    assert call(form=2, rows=0, a_q=None, a_s=None, b_q=None, b_s=None, c=None) == bad
+
+
+def test_no_usable_device_fails_loudly(lib):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a CUDA device is present")
+    gone = (abi.MXFP4_ERR_CUDA, abi.MXFP4_ERR_UNSUPPORTED_DEVICE)
+    assert lib.mxfp4_quantize_grouped(0x10000, 8, 8, 8, None, 0x20000, 2, 8, 0x30000, 0x40000, None, None, None) in gone
+    assert lib.mxfp4_gemm_grouped(0, 0x10000, 0x20000, 0x30000, 0x40000, 0x50000, 2, 8, 8, 24, 0x60000, 24, 0,
+                                  None) in gone
+    assert abi.status_string(abi.MXFP4_ERR_GROUPS).startswith("MXFP4_ERR_GROUPS")
+
+
+def group_table(offsets, groups, rows):
+    """csrc/group_table.cuh, lane by lane."""
+    per = (groups + 1 + 31) // 32
+    start, tops = [None] * (groups + 1), []
+    for lane in range(32):
+        top = 0
+        for e in range(lane * per, min(lane * per + per, groups + 1)):
+            top = max(top, min(max(offsets[e], 0), rows))
+            start[e] = top
+        tops.append(top)
+    carry = 0
+    for lane in range(32):
+        for e in range(lane * per, min(lane * per + per, groups + 1)):
+            if start[e] >= carry:
+                break
+            start[e] = carry
+        carry = max(carry, tops[lane])
+    tiles = [0]
+    for e in range(groups):
+        tiles.append(tiles[-1] + (start[e + 1] - start[e] + 127) // 128)
+    return start, tiles
+
+
+def test_group_table_stays_inside_the_buffers(lib):
+    import random
+    rng = random.Random(1)
+    for _ in range(400):
+        groups, rows = rng.choice([1, 2, 31, 32, 33, 64, 1024]), rng.choice([0, 1, 127, 128, 1000, 70000])
+        o = [rng.randint(-2 * rows - 3, 3 * rows + 3) for _ in range(groups + 1)]
+        if rng.random() < 0.5:
+            o.sort()
+        start, tiles = group_table(o, groups, rows)
+        assert all(0 <= s <= rows for s in start) and start == sorted(start)
+        assert 128 * tiles[-1] <= abi.mxfp4_grouped_sizes(rows, 8, groups)[4]
