@@ -465,6 +465,56 @@ mxfp4_status mxfp4_gemm_grouped(mxfp4_grouped_form form, const void* a_q, const 
                                 const void* b_s, const int32_t* offsets, int64_t groups, int64_t rows, int64_t N,
                                 int64_t K, void* c, int64_t ldc, mxfp4_out_dtype out_dtype, mxfp4_stream_t stream);
 
+/* ---- optimizer step ----------------------------------------------------------------------
+ * One AdamW step (decoupled weight decay) over any number of tensors, in one launch per 320 of
+ * them.  Per element, g the gradient times grad_scale:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p - lr (m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay p),
+ * computed in fp32 (1 - beta and 1 - beta^step in fp64 first); p is `master` where given (the bf16 parameter becomes its rounding, to
+ * nearest even), else the parameter, rounded once to its type.
+ * Moments are fp32, or (MXFP4_ADAMW_STATE_E4M3) 8-bit: per block of MXFP4_ADAMW_BLOCK
+ * consecutive elements of a tensor an fp32 scale max(amax / 448, 2^-126), amax the largest finite
+ * magnitude of the block, and E4M3 codes of the elements over the scale, to nearest even; the
+ * first moment itself, and the square root of the second, where a value above zero never
+ * encodes to zero (it takes at least the code of 2^-9).  A value that is not finite encodes to
+ * NaN.  All-zero codes with any finite scale are zero moments. */
+#define MXFP4_ADAMW_P_F32 1          /* parameters fp32 (else bf16)                            */
+#define MXFP4_ADAMW_G_F32 2          /* gradients fp32 (else bf16)                             */
+#define MXFP4_ADAMW_STATE_E4M3 4     /* moments in 8 bits (else fp32)                          */
+#define MXFP4_ADAMW_BLOCK 128
+
+/* One tensor of n elements (n == 0: skipped), dense, every buffer aligned to its element; all
+ * of them on 16 bytes (codes: 8) is fastest.  master: fp32 copy of a bf16 parameter, or NULL;
+ * m_scale, v_scale: ceil(n / MXFP4_ADAMW_BLOCK) fp32 each, read for 8-bit moments only.
+ * p, master, m, v and the scales are updated in place; g is read.  Buffers must not overlap. */
+typedef struct {
+    void* p;
+    float* master;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    int64_t n;
+} mxfp4_adamw_tensor;
+
+/* beta1, beta2 in [0, 1), eps >= 0, step >= 1 (the number of this step).  dynamic: NULL, or
+ * four fp32 in device memory read instead of the host's values, so that a captured graph can
+ * go on: lr, 1 - beta1^step, 1 - beta2^step, grad_scale. */
+typedef struct {
+    double lr;
+    double beta1;
+    double beta2;
+    double eps;
+    double weight_decay;
+    double grad_scale;
+    int64_t step;
+    const float* dynamic;
+} mxfp4_adamw_params;
+
+mxfp4_status mxfp4_adamw(int32_t count, const mxfp4_adamw_tensor* tensors, int32_t flags,
+                         const mxfp4_adamw_params* params, mxfp4_stream_t stream);
+
 /* ---- a step from host memory to host memory -------------------------------------------
  * The data path of `MXFP4LinearFunction` (primus_turbo_mxfp4_local.py) for linears whose
  * bf16 inputs and results live in host memory: per linear, forward = dual (train) or

@@ -38,6 +38,11 @@ MXFP4_GROUPED_FWD = 0
 MXFP4_GROUPED_DGRAD = 1
 MXFP4_GROUPED_WGRAD = 2
 
+MXFP4_ADAMW_P_F32 = 1
+MXFP4_ADAMW_G_F32 = 2
+MXFP4_ADAMW_STATE_E4M3 = 4
+MXFP4_ADAMW_BLOCK = 128
+
 
 class GemmTask(ctypes.Structure):
     """mxfp4_gemm_task of include/mxfp4.h."""
@@ -73,6 +78,18 @@ class Fp8GemmTask(ctypes.Structure):
                 ("out_dtype", ctypes.c_int)]
 
 
+class AdamwTensor(ctypes.Structure):
+    """mxfp4_adamw_tensor of include/mxfp4.h."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] + \
+        [("n", ctypes.c_int64)]
+
+
+class AdamwParams(ctypes.Structure):
+    """mxfp4_adamw_params of include/mxfp4.h."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + \
+        [("step", ctypes.c_int64), ("dynamic", ctypes.c_void_p)]
+
+
 class LinearHostTask(ctypes.Structure):
     """mxfp4_linear_host_task of include/mxfp4.h."""
     _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("dy", ctypes.c_void_p),
@@ -103,6 +120,7 @@ EXPORTED = (
     "mxfp4_grouped_sizes",
     "mxfp4_quantize_grouped",
     "mxfp4_gemm_grouped",
+    "mxfp4_adamw",
     "mxfp4_linear_workspace_bytes",
     "mxfp4_linear_step_host",
     "mxfp4_linear_pipelined_workspace_bytes",
@@ -159,6 +177,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_grouped_sizes.argtypes = [i64, i64, i64, i32, szp, szp, szp, szp, ctypes.POINTER(i64)]
     lib.mxfp4_quantize_grouped.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp]
     lib.mxfp4_gemm_grouped.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, i32, vp]
+    lib.mxfp4_adamw.argtypes = [i32, vp, i32, ctypes.POINTER(AdamwParams), vp]
     lib.mxfp4_linear_workspace_bytes.argtypes = [i32, ctypes.POINTER(LinearHostTask),
                                                  ctypes.POINTER(ctypes.c_size_t)]
     lib.mxfp4_linear_step_host.argtypes = [i32, ctypes.POINTER(LinearHostTask), vp, ctypes.c_size_t, vp]
@@ -392,6 +411,12 @@ def mxfp4_gemm_grouped(form, a_q, a_s, b_q, b_s, offsets, groups, rows, N, K, c,
                        stream=None) -> None:
     _check(load().mxfp4_gemm_grouped(form, _ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), groups, rows,
                                      N, K, _ptr(c), ldc, out_dtype, _stream(stream)), "mxfp4_gemm_grouped")
+
+
+def mxfp4_adamw(count, tensors, flags, params, stream=None) -> None:
+    """tensors: a ctypes array of AdamwTensor, or the address of such a table; params: AdamwParams."""
+    address = tensors if isinstance(tensors, int) or tensors is None else ctypes.addressof(tensors)
+    _check(load().mxfp4_adamw(count, address, flags, ctypes.byref(params), _stream(stream)), "mxfp4_adamw")
 
 
 def _host_tasks(tasks):

@@ -16,7 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4_gb300.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "gemm_pair.cu", "quantize_fp8.cu", "gemm_fp8.cu",
-           "host_step.cu", "grouped.cu", "quantize_grouped.cu", "gemm_grouped.cu"]
+           "host_step.cu", "grouped.cu", "quantize_grouped.cu", "gemm_grouped.cu",
+           "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

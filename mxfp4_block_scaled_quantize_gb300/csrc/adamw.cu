@@ -1,0 +1,363 @@
+// adamw.cu -- one AdamW step (decoupled weight decay) over many tensors in one launch, with
+// moments in fp32 or in 8 bits.
+//
+// Per element, with g the gradient times grad_scale and c = 1 - beta^step:
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,
+//   p = p - lr (m / c1 / (sqrt(v / c2) + eps) + wd p),
+// all in fp32; p is the fp32 master where there is one (the bf16 parameter is then its rounding),
+// else the parameter itself, rounded once to its type.
+//
+// 8-bit moments.  A block of 128 consecutive elements shares an fp32 scale, amax / 448 (at least
+// 2^-126), and an element is the E4M3 value nearest to it over the scale.  The second moment
+// enters p through its square root, and its square spans twice the binades, so what is stored is
+// r = sqrt(v): E4M3's 18 binades then hold 36 binades of v.  An r above zero never becomes zero
+// (it takes the smallest code): m / sqrt(v) of a small element beside a large one would otherwise
+// divide by eps.  An element that is not finite becomes NaN and leaves its block's scale alone.
+//
+// Bound by memory: bf16 parameters with masters and bf16 gradients move 28 bytes an element with
+// fp32 moments and 16.1 with 8-bit ones.  A thread takes 8 consecutive elements, all of whose
+// loads are in flight together; 16 lanes hold a block, so its maxima are four shuffles.  The
+// tensor table travels as a kernel parameter: no copy, no allocation, and a graph captures it.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "launch.h"
+#include "launch_adamw.h"
+#include "ptx.cuh"
+
+namespace mxfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinScale = 1.17549435e-38f;   // 2^-126
+constexpr float kMinCode = 0.001953125f;       // 2^-9, the smallest E4M3 value above zero
+
+__device__ __forceinline__ void unpack_bf16(const uint4& u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight elements at i: with wide loads where they are whole and aligned, else one by one, zero past n.
+template <bool kF32>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, bool wide, float* f) {
+    if (wide) {
+        if (kF32) {
+            const float4* const s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+            const float4 a = s[0], b = s[1];
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        } else {
+            unpack_bf16(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), f);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        f[k] = 0.0f;
+        if (i + k < n)
+            f[k] = kF32 ? static_cast<const float*>(p)[i + k]
+                        : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i + k]) << 16);
+    }
+}
+
+template <bool kF32>
+__device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, bool wide, const float* f) {
+    if (wide) {
+        if (kF32) {
+            float4* const d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+            d[0] = make_float4(f[0], f[1], f[2], f[3]);
+            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (i + k >= n) break;
+        if (kF32)
+            static_cast<float*>(p)[i + k] = f[k];
+        else
+            static_cast<__nv_bfloat16*>(p)[i + k] = __float2bfloat16_rn(f[k]);
+    }
+}
+
+__device__ __forceinline__ uint2 load_codes(const void* p, int64_t i, int64_t n, bool wide) {
+    const uint8_t* const s = static_cast<const uint8_t*>(p) + i;
+    if (wide) return *reinterpret_cast<const uint2*>(s);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (i + k < n) w[k >> 2] |= static_cast<uint32_t>(s[k]) << (8 * (k & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t n, bool wide, uint2 q) {
+    uint8_t* const d = static_cast<uint8_t*>(p) + i;
+    if (wide) {
+        *reinterpret_cast<uint2*>(d) = q;
+        return;
+    }
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (i + k < n) d[k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
+}
+
+__device__ __forceinline__ void decode_e4m3(uint2 q, float scale, float* f) {
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t h;
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+            : "=r"(h)
+            : "r"(w[k >> 1] >> (16 * (k & 1))));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        f[2 * k] = v.x * scale;
+        f[2 * k + 1] = v.y * scale;
+    }
+}
+
+__device__ __forceinline__ uint2 encode_e4m3(const float* f) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+            "mov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(w[k])
+            : "f"(f[4 * k]), "f"(f[4 * k + 1]), "f"(f[4 * k + 2]), "f"(f[4 * k + 3]));
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// This lane's block (16 lanes) of x: its scale, and the eight codes.  kRoot: values >= 0, of
+// which those above zero stay there.  The quotients x / scale are those of IEEE division, by
+// Markstein's theorem (IBM J. Res. Dev. 34, 1990): from the correctly rounded reciprocal y,
+// q = x y and the exact residual x - q scale give the correctly rounded quotient as
+// q + residual y.  Three operations an element in place of a division; a code is the nearest to
+// the rounded quotient in either case.
+template <bool kRoot>
+__device__ __forceinline__ uint2 encode_block(const float* x, float* scale) {
+    const float inf = __int_as_float(0x7F800000);
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(x[k]));
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const bool odd = !(top < inf);   // the block holds a value that is not finite: rare
+    if (__any_sync(0xFFFFFFFFu, odd)) {
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t = fmaxf(t, fabsf(x[k]) < inf ? fabsf(x[k]) : 0.0f);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, d));
+        top = t;
+    }
+    const float s = fmaxf(__fmul_rn(top, 1.0f / kE4m3Max), kMinScale);
+    const float inv = __frcp_rn(s);
+    *scale = s;
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float q = __fmul_rn(x[k], inv);
+        y[k] = __fmaf_rn(__fmaf_rn(-q, s, x[k]), inv, q);
+        if (kRoot) y[k] = x[k] > 0.0f ? fmaxf(y[k], kMinCode) : 0.0f;
+    }
+    if (odd) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (!(fabsf(x[k]) < inf)) y[k] = __int_as_float(0x7FC00000);
+    }
+    return encode_e4m3(y);
+}
+
+template <bool kPF32, bool kGF32, bool kState8, int kCap>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs<kCap> a) {
+    grid_wait_prerequisites();
+    grid_launch_dependents();
+    const int unit = static_cast<int>(blockIdx.x);
+    int lo = 0, hi = a.count - 1;   // the tensor of this unit: the first with end > unit
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.end[mid] > unit) hi = mid;
+        else lo = mid + 1;
+    }
+    const mxfp4_adamw_tensor& t = a.t[lo];
+    const int64_t n = t.n;
+    const int64_t base = static_cast<int64_t>(unit - (lo > 0 ? a.end[lo - 1] : 0)) * kAdamwUnit;
+    const bool dyn = a.dynamic != nullptr;
+    const float lr = dyn ? __ldg(a.dynamic) : a.lr;
+    const float c1 = dyn ? __ldg(a.dynamic + 1) : a.c1, c2 = dyn ? __ldg(a.dynamic + 2) : a.c2;
+    const float gs = dyn ? __ldg(a.dynamic + 3) : a.grad_scale;
+    const float step_c1 = lr / c1, inv_root_c2 = 1.0f / sqrtf(c2), decay = lr * a.weight_decay;
+    // every pointer where an 8-element access may start: 16 bytes apart (codes: 8)
+    const uintptr_t all = reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
+                          reinterpret_cast<uintptr_t>(t.master) |
+                          (kState8 ? (reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) << 1
+                                   : reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v));
+    const bool aligned = (all & 15u) == 0;
+#pragma unroll 1
+    for (int64_t i = base + 8 * threadIdx.x; i < base + kAdamwUnit; i += 8 * kThreads) {
+        // past the end a lane still takes part in its block's maximum, with zeros
+        const bool wide = aligned && i + 8 <= n;
+        float g[8], p[8], m[8], v[8];
+        load8<kGF32>(t.g, i, n, wide, g);
+        if (t.master != nullptr)
+            load8<true>(t.master, i, n, wide, p);
+        else
+            load8<kPF32>(t.p, i, n, wide, p);
+        if (kState8) {
+            const int64_t block = min(i, n - 1) / kAdamwBlock;
+            decode_e4m3(load_codes(t.m, i, n, wide), t.m_scale[block], m);
+            decode_e4m3(load_codes(t.v, i, n, wide), t.v_scale[block], v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= v[k];
+        } else {
+            load8<true>(t.m, i, n, wide, m);
+            load8<true>(t.v, i, n, wide, v);
+        }
+        // The moments in single roundings, in the order the formula has them: an 8-bit code jumps
+        // by a sixteenth where its value crosses a midpoint, so a value that another evaluation in
+        // fp32 reproduces is worth more than the fused product that is nearer.  The parameter
+        // has no such borders.
+        float r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float gk = __fmul_rn(g[k], gs);
+            m[k] = __fadd_rn(__fmul_rn(a.beta1, m[k]), __fmul_rn(a.one_beta1, gk));
+            v[k] = __fadd_rn(__fmul_rn(a.beta2, v[k]), __fmul_rn(__fmul_rn(a.one_beta2, gk), gk));
+            r[k] = __fsqrt_rn(v[k]);
+            p[k] -= __fdividef(step_c1 * m[k], fmaf(r[k], inv_root_c2, a.eps)) + decay * p[k];
+        }
+        if (t.master != nullptr) store8<true>(t.master, i, n, wide, p);
+        store8<kPF32>(t.p, i, n, wide, p);
+        if (kState8) {
+            float ms, vs;
+            const uint2 mq = encode_block<false>(m, &ms), vq = encode_block<true>(r, &vs);
+            store_codes(t.m, i, n, wide, mq);
+            store_codes(t.v, i, n, wide, vq);
+            if ((threadIdx.x & 15) == 0 && i < n) {
+                t.m_scale[i / kAdamwBlock] = ms;
+                t.v_scale[i / kAdamwBlock] = vs;
+            }
+        } else {
+            store8<true>(t.m, i, n, wide, m);
+            store8<true>(t.v, i, n, wide, v);
+        }
+    }
+}
+
+template <int kCap>
+cudaError_t launch(const AdamwArgs<kCap>& a, int flags, cudaStream_t stream) {
+    using K = void (*)(AdamwArgs<kCap>);
+    static const K kernels[8] = {
+        adamw_kernel<false, false, false, kCap>, adamw_kernel<true, false, false, kCap>,
+        adamw_kernel<false, true, false, kCap>,  adamw_kernel<true, true, false, kCap>,
+        adamw_kernel<false, false, true, kCap>,  adamw_kernel<true, false, true, kCap>,
+        adamw_kernel<false, true, true, kCap>,   adamw_kernel<true, true, true, kCap>};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.end[a.count - 1]), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernels[flags], a);
+}
+
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+mxfp4_status check(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, const mxfp4_adamw_params* h) {
+    if (count < 0 || (count > 0 && t == nullptr) || h == nullptr || (flags & ~7)) return MXFP4_ERR_INVALID_ARG;
+    // the fp32 values that the kernel uses have to lie in the ranges too
+    const float b1 = static_cast<float>(h->beta1), b2 = static_cast<float>(h->beta2), eps = static_cast<float>(h->eps);
+    if (!(h->beta1 >= 0.0 && b1 < 1.0f) || !(h->beta2 >= 0.0 && b2 < 1.0f) || !(h->eps >= 0.0) || h->step < 1 ||
+        !std::isfinite(eps) || !std::isfinite(h->lr) || !std::isfinite(h->weight_decay))
+        return MXFP4_ERR_INVALID_ARG;
+    if (!aligned_to(h->dynamic, 4)) return MXFP4_ERR_MISALIGNED;
+    const bool p_f32 = flags & MXFP4_ADAMW_P_F32, g_f32 = flags & MXFP4_ADAMW_G_F32, s8 = flags & MXFP4_ADAMW_STATE_E4M3;
+    for (int32_t j = 0; j < count; ++j) {
+        const mxfp4_adamw_tensor& x = t[j];
+        if (x.n < 0 || x.n > (int64_t{1} << 40)) return MXFP4_ERR_INVALID_ARG;
+        if (p_f32 && x.master != nullptr) return MXFP4_ERR_INVALID_ARG;
+        if (x.n > 0 && (!x.p || !x.g || !x.m || !x.v || (s8 && (!x.m_scale || !x.v_scale)))) return MXFP4_ERR_INVALID_ARG;
+        if (!aligned_to(x.p, p_f32 ? 4 : 2) || !aligned_to(x.g, g_f32 ? 4 : 2) || !aligned_to(x.master, 4) ||
+            !aligned_to(x.m, s8 ? 1 : 4) || !aligned_to(x.v, s8 ? 1 : 4) ||
+            (s8 && (!aligned_to(x.m_scale, 4) || !aligned_to(x.v_scale, 4))))
+            return MXFP4_ERR_MISALIGNED;
+    }
+    return MXFP4_OK;
+}
+
+template <int kCap>
+mxfp4_status step(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, const mxfp4_adamw_params& h,
+                  cudaStream_t stream) {
+    AdamwArgs<kCap> a;
+    a.beta1 = static_cast<float>(h.beta1);
+    a.one_beta1 = static_cast<float>(1.0 - h.beta1);
+    a.beta2 = static_cast<float>(h.beta2);
+    a.one_beta2 = static_cast<float>(1.0 - h.beta2);
+    a.eps = static_cast<float>(h.eps);
+    a.weight_decay = static_cast<float>(h.weight_decay);
+    a.lr = static_cast<float>(h.lr);
+    a.c1 = static_cast<float>(1.0 - std::pow(h.beta1, static_cast<double>(h.step)));
+    a.c2 = static_cast<float>(1.0 - std::pow(h.beta2, static_cast<double>(h.step)));
+    a.grad_scale = static_cast<float>(h.grad_scale);
+    a.dynamic = h.dynamic;
+    int32_t j = 0;
+    while (j < count) {
+        int64_t units = 0;
+        a.count = 0;
+        while (j < count && a.count < kCap) {
+            if (t[j].n == 0) {
+                ++j;
+                continue;
+            }
+            const int64_t more = (t[j].n + kAdamwUnit - 1) / kAdamwUnit;
+            if (units + more > 0x7FFFFFFF) break;
+            units += more;
+            a.t[a.count] = t[j++];
+            a.end[a.count++] = static_cast<int32_t>(units);
+        }
+        if (a.count > 0 && launch<kCap>(a, flags, stream) != cudaSuccess) return MXFP4_ERR_CUDA;
+    }
+    return MXFP4_OK;
+}
+
+}  // namespace
+}  // namespace mxfp4
+
+extern "C" mxfp4_status mxfp4_adamw(int32_t count, const mxfp4_adamw_tensor* tensors, int32_t flags,
+                                    const mxfp4_adamw_params* params, mxfp4_stream_t stream) {
+    const mxfp4_status ok = mxfp4::check(count, tensors, flags, params);
+    if (ok != MXFP4_OK) return ok;
+    int sms = 0;
+    uint32_t* err = nullptr;
+    const int st = mxfp4::device_info(&sms, &err);
+    if (st != MXFP4_OK) return static_cast<mxfp4_status>(st);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return count <= mxfp4::kAdamwFew ? mxfp4::step<mxfp4::kAdamwFew>(count, tensors, flags, *params, s)
+                                     : mxfp4::step<mxfp4::kAdamwMany>(count, tensors, flags, *params, s);
+}

@@ -1,0 +1,96 @@
+"""AdamW over the tensors of a model in one launch, with moments in fp32 or in 8 bits.
+
+The weight update next to the MXFP4 layers: it takes their dW (bf16 or fp32) and writes the bf16
+W that the next step quantizes, from fp32 master copies where they are kept.
+"""
+import numpy as np
+import torch
+
+from . import abi
+
+_TABLE = np.dtype([(name, np.uint64) for name in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] +
+                  [("n", np.int64)])
+
+
+class AdamW:
+    """params: contiguous CUDA tensors, all fp32 or all bf16; masters: fp32 copies of bf16
+    parameters (or None: the parameters themselves are updated).  Moments: `state_bits` 32 or 8
+    allocates zeros; or exp_avg / exp_avg_sq give them, per tensor an fp32 tensor, or for 8 bits
+    a pair (E4M3 codes, fp32 scale per 128 elements), exp_avg_sq then holding the square root of
+    the second moment.  All tensors are updated in place and must stay where they are."""
+
+    def __init__(self, params, masters=None, state_bits=32, exp_avg=None, exp_avg_sq=None, lr=1e-3,
+                 betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        self.dtype = self.params[0].dtype
+        if self.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"parameters in fp32 or bf16, not {self.dtype}")
+        self.masters = None if masters is None else list(masters)
+        if self.masters is not None and self.dtype == torch.float32:
+            raise ValueError("fp32 parameters need no masters")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits: 32 or 8")
+        if exp_avg is None:
+            exp_avg = [self._zeros(p, state_bits) for p in self.params]
+            exp_avg_sq = [self._zeros(p, state_bits) for p in self.params]
+        self.exp_avg, self.exp_avg_sq = list(exp_avg), list(exp_avg_sq)
+        self.state_bits = 32 if isinstance(self.exp_avg[0], torch.Tensor) else 8
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.steps = 0
+        self._numel = [p.numel() for p in self.params]
+        self._table = np.zeros(len(self.params), dtype=_TABLE)
+        self._fill()
+
+    @staticmethod
+    def _zeros(p, bits):
+        if bits == 32:
+            return torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
+        blocks = -(-p.numel() // abi.MXFP4_ADAMW_BLOCK)
+        return (torch.zeros(p.numel(), dtype=torch.float8_e4m3fn, device=p.device),
+                torch.zeros(blocks, dtype=torch.float32, device=p.device))
+
+    def _fill(self):
+        """Checks every tensor and writes the table that each step hands to the library."""
+        def put(name, tensors, dtype, counts):
+            if len(tensors) != len(self.params):
+                raise ValueError(f"{len(tensors)} tensors of {name} for {len(self.params)} parameters")
+            for t, n in zip(tensors, counts):
+                if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != self.params[0].device:
+                    raise ValueError(f"{name}: contiguous {dtype} tensors of the parameters' sizes, on their device")
+            self._table[name] = [t.data_ptr() for t in tensors]
+
+        put("p", self.params, self.dtype, self._numel)
+        if self.masters is not None:
+            put("master", self.masters, torch.float32, self._numel)
+        for name, moments in (("m", self.exp_avg), ("v", self.exp_avg_sq)):
+            if self.state_bits == 32:
+                put(name, moments, torch.float32, self._numel)
+            else:
+                put(name, [c for c, _ in moments], torch.float8_e4m3fn, self._numel)
+                put(name + "_scale", [s for _, s in moments], torch.float32,
+                    [-(-n // abi.MXFP4_ADAMW_BLOCK) for n in self._numel])
+        self._table["n"] = self._numel
+
+    def step(self, grads, step=None, lr=None, grad_scale=1.0, dynamic=None, stream=None):
+        """One update with the gradients (contiguous, all fp32 or all bf16, in the order of the
+        parameters).  step: this step's number (default: counted from 1); grad_scale: a factor on
+        every gradient; dynamic: a CUDA fp32 tensor [lr, 1 - beta1^step, 1 - beta2^step, grad_scale]
+        that takes their place, for steps captured in a graph."""
+        dtype = grads[0].dtype
+        if dtype not in (torch.float32, torch.bfloat16) or len(grads) != len(self.params):
+            raise ValueError("one fp32 or bf16 gradient for each parameter")
+        for g, n in zip(grads, self._numel):
+            if g.dtype != dtype or g.numel() != n or not g.is_contiguous():
+                raise ValueError("gradients: contiguous, of one type and the parameters' sizes")
+        if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != 4 or not dynamic.is_cuda):
+            raise ValueError("dynamic: four fp32 on the device")
+        self.steps = self.steps + 1 if step is None else step
+        self._table["g"] = [g.data_ptr() for g in grads]
+        flags = (abi.MXFP4_ADAMW_P_F32 if self.dtype == torch.float32 else 0) | \
+                (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0) | \
+                (abi.MXFP4_ADAMW_STATE_E4M3 if self.state_bits == 8 else 0)
+        h = abi.AdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                            grad_scale, self.steps, None if dynamic is None else dynamic.data_ptr())
+        abi.mxfp4_adamw(len(self.params), self._table.ctypes.data, flags, h, stream)
