@@ -498,7 +498,7 @@ typedef struct {
     int64_t n;
 } mxfp4_adamw_tensor;
 
-/* beta1, beta2 in [0, 1), eps >= 0, step >= 1 (the number of this step).  dynamic: NULL, or
+/* beta1, beta2 in [0, 1), eps 0 or a normal fp32 above it, step >= 1 (the number of this step).  dynamic: NULL, or
  * four fp32 in device memory read instead of the host's values, so that a captured graph can
  * go on: lr, 1 - beta1^step, 1 - beta2^step, grad_scale. */
 typedef struct {

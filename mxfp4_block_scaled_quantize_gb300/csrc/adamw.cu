@@ -31,7 +31,12 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a CTA.  With 8-bit moments the arithmetic (some 65 instructions an element) nearly
+// fills the time of the memory, and many small CTAs keep both busy: 288 M elements took 877 us
+// with 256 threads a CTA, 830 with 128, 750 with 64, 725 (6.4 TB/s, 0.96 of the measured copy) with
+// one warp.  With fp32 moments 128 threads were fastest (7.1 TB/s on 72 M elements).
+constexpr int kThreads32 = 128;   // fp32 moments
+constexpr int kThreads8 = 32;     // 8-bit moments
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126
 constexpr float kMinCode = 0.001953125f;       // 2^-9, the smallest E4M3 value above zero
@@ -191,8 +196,98 @@ __device__ __forceinline__ uint2 encode_block(const float* x, float* scale) {
     return encode_e4m3(y);
 }
 
+// Square roots of eight values >= 0: y = 1 / sqrt(v) approximately, s = v y, and one correction
+// by the exact residual, s + (v - s^2) y / 2 (Markstein, as above); equal to __fsqrt_rn for
+// every mantissa of both exponent parities (checked over [1, 4)), without its branch an element.
+// Values outside [2^-100, 2^126), where a residual could lose bits, zero among them, take
+// __fsqrt_rn.
+__device__ __forceinline__ void sqrt8(const float* v, float* r) {
+    float lo = v[0], hi = v[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) {
+        lo = fminf(lo, v[k]);
+        hi = max_nan(hi, v[k]);
+    }
+    if (lo >= 7.8886091e-31f && hi < 8.5070592e37f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float y;
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v[k]));
+            const float s = __fmul_rn(v[k], y);
+            r[k] = __fmaf_rn(__fmaf_rn(-s, s, v[k]), 0.5f * y, s);
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(v[k]);
+    }
+}
+
+struct Hyper {
+    float beta1, one_beta1, beta2, one_beta2, eps, step_c1, inv_root_c2, decay, grad_scale;
+};
+
+// Eight elements of t at i.  kWhole: all eight exist and every access is aligned.
+template <bool kPF32, bool kGF32, bool kState8, bool kWhole>
+__device__ __forceinline__ void update8(const mxfp4_adamw_tensor& t, const Hyper& h, int64_t i, int64_t n, bool aligned) {
+    // past the end a lane still takes part in its block's maximum, with zeros
+    const bool wide = kWhole || (aligned && i + 8 <= n);
+    float g[8], p[8], m[8], v[8], r[8];
+    load8<kGF32>(t.g, i, n, wide, g);
+    if (t.master != nullptr)
+        load8<true>(t.master, i, n, wide, p);
+    else
+        load8<kPF32>(t.p, i, n, wide, p);
+    if (kState8) {
+        const int64_t block = (kWhole ? i : min(i, n - 1)) / kAdamwBlock;
+        decode_e4m3(load_codes(t.m, i, n, wide), t.m_scale[block], m);
+        decode_e4m3(load_codes(t.v, i, n, wide), t.v_scale[block], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= v[k];
+    } else {
+        load8<true>(t.m, i, n, wide, m);
+        load8<true>(t.v, i, n, wide, v);
+    }
+    // The moments in single roundings, in the order the formula has them: an 8-bit code jumps by a
+    // sixteenth where its value crosses a midpoint, so a value that another evaluation in fp32
+    // reproduces is worth more than the fused product that is nearer.  The parameter has no such
+    // borders.
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float gk = __fmul_rn(g[k], h.grad_scale);
+        m[k] = __fadd_rn(__fmul_rn(h.beta1, m[k]), __fmul_rn(h.one_beta1, gk));
+        v[k] = __fadd_rn(__fmul_rn(h.beta2, v[k]), __fmul_rn(__fmul_rn(h.one_beta2, gk), gk));
+    }
+    if (kState8) {
+        sqrt8(v, r);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r[k], h.inv_root_c2, h.eps)));
+        p[k] -= h.step_c1 * m[k] * inv + h.decay * p[k];
+    }
+    if (t.master != nullptr) store8<true>(t.master, i, n, wide, p);
+    store8<kPF32>(t.p, i, n, wide, p);
+    if (kState8) {
+        float ms, vs;
+        const uint2 mq = encode_block<false>(m, &ms), vq = encode_block<true>(r, &vs);
+        store_codes(t.m, i, n, wide, mq);
+        store_codes(t.v, i, n, wide, vq);
+        if ((threadIdx.x & 15) == 0 && (kWhole || i < n)) {
+            t.m_scale[i / kAdamwBlock] = ms;
+            t.v_scale[i / kAdamwBlock] = vs;
+        }
+    } else {
+        store8<true>(t.m, i, n, wide, m);
+        store8<true>(t.v, i, n, wide, v);
+    }
+}
+
 template <bool kPF32, bool kGF32, bool kState8, int kCap>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs<kCap> a) {
+__global__ void __launch_bounds__(kState8 ? kThreads8 : kThreads32, kState8 ? 32 : 8) adamw_kernel(const __grid_constant__ AdamwArgs<kCap> a) {
     grid_wait_prerequisites();
     grid_launch_dependents();
     const int unit = static_cast<int>(blockIdx.x);
@@ -208,62 +303,22 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const bool dyn = a.dynamic != nullptr;
     const float lr = dyn ? __ldg(a.dynamic) : a.lr;
     const float c1 = dyn ? __ldg(a.dynamic + 1) : a.c1, c2 = dyn ? __ldg(a.dynamic + 2) : a.c2;
-    const float gs = dyn ? __ldg(a.dynamic + 3) : a.grad_scale;
-    const float step_c1 = lr / c1, inv_root_c2 = 1.0f / sqrtf(c2), decay = lr * a.weight_decay;
+    Hyper h{a.beta1, a.one_beta1, a.beta2, a.one_beta2, a.eps, lr / c1, 1.0f / sqrtf(c2), lr * a.weight_decay,
+            dyn ? __ldg(a.dynamic + 3) : a.grad_scale};
     // every pointer where an 8-element access may start: 16 bytes apart (codes: 8)
     const uintptr_t all = reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
                           reinterpret_cast<uintptr_t>(t.master) |
                           (kState8 ? (reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) << 1
                                    : reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v));
     const bool aligned = (all & 15u) == 0;
+    const int64_t i0 = base + 8 * threadIdx.x;
+    constexpr int kPass = 8 * (kState8 ? kThreads8 : kThreads32);
+    if (aligned && base + kAdamwUnit <= n) {
 #pragma unroll 1
-    for (int64_t i = base + 8 * threadIdx.x; i < base + kAdamwUnit; i += 8 * kThreads) {
-        // past the end a lane still takes part in its block's maximum, with zeros
-        const bool wide = aligned && i + 8 <= n;
-        float g[8], p[8], m[8], v[8];
-        load8<kGF32>(t.g, i, n, wide, g);
-        if (t.master != nullptr)
-            load8<true>(t.master, i, n, wide, p);
-        else
-            load8<kPF32>(t.p, i, n, wide, p);
-        if (kState8) {
-            const int64_t block = min(i, n - 1) / kAdamwBlock;
-            decode_e4m3(load_codes(t.m, i, n, wide), t.m_scale[block], m);
-            decode_e4m3(load_codes(t.v, i, n, wide), t.v_scale[block], v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= v[k];
-        } else {
-            load8<true>(t.m, i, n, wide, m);
-            load8<true>(t.v, i, n, wide, v);
-        }
-        // The moments in single roundings, in the order the formula has them: an 8-bit code jumps
-        // by a sixteenth where its value crosses a midpoint, so a value that another evaluation in
-        // fp32 reproduces is worth more than the fused product that is nearer.  The parameter
-        // has no such borders.
-        float r[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float gk = __fmul_rn(g[k], gs);
-            m[k] = __fadd_rn(__fmul_rn(a.beta1, m[k]), __fmul_rn(a.one_beta1, gk));
-            v[k] = __fadd_rn(__fmul_rn(a.beta2, v[k]), __fmul_rn(__fmul_rn(a.one_beta2, gk), gk));
-            r[k] = __fsqrt_rn(v[k]);
-            p[k] -= __fdividef(step_c1 * m[k], fmaf(r[k], inv_root_c2, a.eps)) + decay * p[k];
-        }
-        if (t.master != nullptr) store8<true>(t.master, i, n, wide, p);
-        store8<kPF32>(t.p, i, n, wide, p);
-        if (kState8) {
-            float ms, vs;
-            const uint2 mq = encode_block<false>(m, &ms), vq = encode_block<true>(r, &vs);
-            store_codes(t.m, i, n, wide, mq);
-            store_codes(t.v, i, n, wide, vq);
-            if ((threadIdx.x & 15) == 0 && i < n) {
-                t.m_scale[i / kAdamwBlock] = ms;
-                t.v_scale[i / kAdamwBlock] = vs;
-            }
-        } else {
-            store8<true>(t.m, i, n, wide, m);
-            store8<true>(t.v, i, n, wide, v);
-        }
+        for (int k = 0; k < kAdamwUnit; k += kPass) update8<kPF32, kGF32, kState8, true>(t, h, i0 + k, n, true);
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < kAdamwUnit; k += kPass) update8<kPF32, kGF32, kState8, false>(t, h, i0 + k, n, aligned);
     }
 }
 
@@ -280,7 +335,7 @@ cudaError_t launch(const AdamwArgs<kCap>& a, int flags, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.end[a.count - 1]), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(flags & MXFP4_ADAMW_STATE_E4M3 ? kThreads8 : kThreads32, 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -294,7 +349,7 @@ mxfp4_status check(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, co
     // the fp32 values that the kernel uses have to lie in the ranges too
     const float b1 = static_cast<float>(h->beta1), b2 = static_cast<float>(h->beta2), eps = static_cast<float>(h->eps);
     if (!(h->beta1 >= 0.0 && b1 < 1.0f) || !(h->beta2 >= 0.0 && b2 < 1.0f) || !(h->eps >= 0.0) || h->step < 1 ||
-        !std::isfinite(eps) || !std::isfinite(h->lr) || !std::isfinite(h->weight_decay))
+        !std::isfinite(eps) || (h->eps > 0.0 && eps < kMinScale) || !std::isfinite(h->lr) || !std::isfinite(h->weight_decay))
         return MXFP4_ERR_INVALID_ARG;
     if (!aligned_to(h->dynamic, 4)) return MXFP4_ERR_MISALIGNED;
     const bool p_f32 = flags & MXFP4_ADAMW_P_F32, g_f32 = flags & MXFP4_ADAMW_G_F32, s8 = flags & MXFP4_ADAMW_STATE_E4M3;

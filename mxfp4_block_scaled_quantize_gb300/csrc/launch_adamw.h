@@ -10,7 +10,7 @@
 namespace mxfp4 {
 
 constexpr int kAdamwBlock = 128;     // elements that share the scale of an 8-bit moment
-constexpr int kAdamwUnit = 4096;     // elements of a CTA's unit of work
+constexpr int kAdamwUnit = 1024;     // elements of a CTA's unit of work
 constexpr int kAdamwFew = 40;        // tensors of the small launch's table,
 constexpr int kAdamwMany = 320;      // and of the large one's (a kernel parameter: 22 of 32 KB)
 

@@ -33,6 +33,7 @@ def test_refusals(lib):
     assert call(lib, flags=abi.MXFP4_ADAMW_P_F32, master=80) == bad          # fp32 parameters have no master
     assert call(lib, flags=abi.MXFP4_ADAMW_STATE_E4M3) == bad                # 8-bit moments need scales
     for h in ({"beta1": 1.0}, {"beta2": -0.1}, {"beta1": float("nan")}, {"eps": -1.0}, {"eps": float("inf")},
+              {"eps": 1e-40},
               {"step": 0}, {"lr": float("nan")}, {"weight_decay": float("inf")}):
         assert call(lib, params=h) == bad, h
     assert call(lib, p=17) == mis and call(lib, flags=abi.MXFP4_ADAMW_P_F32, p=18) == mis
