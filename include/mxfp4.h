@@ -465,6 +465,38 @@ mxfp4_status mxfp4_gemm_grouped(mxfp4_grouped_form form, const void* a_q, const 
                                 const void* b_s, const int32_t* offsets, int64_t groups, int64_t rows, int64_t N,
                                 int64_t K, void* c, int64_t ldc, mxfp4_out_dtype out_dtype, mxfp4_stream_t stream);
 
+/* The layer's data path in one call each, from the entry points above (quantization of X and,
+ * where its bf16 form is given, W, then FWD; quantization of dY, then DGRAD and WGRAD), over
+ * buffers that the caller keeps from the forward to the backward:
+ *   x_blobs, w_blobs, dy_blobs   grouped blobs (q_row, s_row, q_col, s_col) of X and dY for up to
+ *             the rows of a call, and of W (equal groups of N rows).  Serving: x_blobs with q_col
+ *             and s_col NULL; a w that is never quantized here needs no col blob either.
+ *   y, dx, dw outputs, dense: [rows, N], [rows, K], [groups * N, K] in out_dtype
+ *   forward:  w = bf16 W[groups * N, K], dense (K % 8 == 0), whose blobs are written; or NULL: the
+ *             row blob in w_blobs is used as it is.  x, x_rows, ldx, row_index, offsets (not
+ *             NULL), rows as for mxfp4_quantize_grouped.
+ *   backward: dy = bf16 [rows, N] with pitch lddy; needs the blobs of the forward with the same
+ *             offsets and rows.
+ * Errors as for the entry points; nothing is enqueued when an argument is refused. */
+typedef struct {
+    int64_t groups;
+    int64_t N;
+    int64_t K;
+    void* x_blobs[4];
+    void* w_blobs[4];
+    void* dy_blobs[4];
+    void* y;
+    void* dx;
+    void* dw;
+    int32_t out_dtype;   /* mxfp4_out_dtype */
+} mxfp4_grouped_linear;
+
+mxfp4_status mxfp4_grouped_forward(const mxfp4_grouped_linear* layer, const void* x, int64_t x_rows, int64_t ldx,
+                                   const int32_t* row_index, const int32_t* offsets, int64_t rows, const void* w,
+                                   mxfp4_stream_t stream);
+mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const void* dy, int64_t lddy,
+                                    const int32_t* offsets, int64_t rows, mxfp4_stream_t stream);
+
 /* ---- optimizer step ----------------------------------------------------------------------
  * One AdamW step (decoupled weight decay) over any number of tensors, in one launch per 320 of
  * them.  Per element, g the gradient times grad_scale:

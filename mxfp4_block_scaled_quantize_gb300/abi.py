@@ -78,6 +78,13 @@ class Fp8GemmTask(ctypes.Structure):
                 ("out_dtype", ctypes.c_int)]
 
 
+class GroupedLinear(ctypes.Structure):
+    """mxfp4_grouped_linear of include/mxfp4.h."""
+    _fields_ = [(name, ctypes.c_int64) for name in ("groups", "N", "K")] + \
+        [(name, ctypes.c_void_p * 4) for name in ("x_blobs", "w_blobs", "dy_blobs")] + \
+        [(name, ctypes.c_void_p) for name in ("y", "dx", "dw")] + [("out_dtype", ctypes.c_int32)]
+
+
 class AdamwTensor(ctypes.Structure):
     """mxfp4_adamw_tensor of include/mxfp4.h."""
     _fields_ = [(name, ctypes.c_void_p) for name in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] + \
@@ -120,6 +127,8 @@ EXPORTED = (
     "mxfp4_grouped_sizes",
     "mxfp4_quantize_grouped",
     "mxfp4_gemm_grouped",
+    "mxfp4_grouped_forward",
+    "mxfp4_grouped_backward",
     "mxfp4_adamw",
     "mxfp4_linear_workspace_bytes",
     "mxfp4_linear_step_host",
@@ -177,6 +186,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_grouped_sizes.argtypes = [i64, i64, i64, i32, szp, szp, szp, szp, ctypes.POINTER(i64)]
     lib.mxfp4_quantize_grouped.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp]
     lib.mxfp4_gemm_grouped.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, i32, vp]
+    lib.mxfp4_grouped_forward.argtypes = [ctypes.POINTER(GroupedLinear), vp, i64, i64, vp, vp, i64, vp, vp]
+    lib.mxfp4_grouped_backward.argtypes = [ctypes.POINTER(GroupedLinear), vp, i64, vp, i64, vp]
     lib.mxfp4_adamw.argtypes = [i32, vp, i32, ctypes.POINTER(AdamwParams), vp]
     lib.mxfp4_linear_workspace_bytes.argtypes = [i32, ctypes.POINTER(LinearHostTask),
                                                  ctypes.POINTER(ctypes.c_size_t)]
@@ -205,8 +216,9 @@ def _ptr(buf) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        # the handle alone: building torch's stream object around it takes 3 us
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -411,6 +423,17 @@ def mxfp4_gemm_grouped(form, a_q, a_s, b_q, b_s, offsets, groups, rows, N, K, c,
                        stream=None) -> None:
     _check(load().mxfp4_gemm_grouped(form, _ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), groups, rows,
                                      N, K, _ptr(c), ldc, out_dtype, _stream(stream)), "mxfp4_gemm_grouped")
+
+
+def mxfp4_grouped_forward(layer, x, x_rows, ldx, row_index, offsets, rows, w=None, stream=None) -> None:
+    """layer: a GroupedLinear."""
+    _check(load().mxfp4_grouped_forward(layer, _ptr(x), x_rows, ldx, _ptr(row_index), _ptr(offsets), rows, _ptr(w),
+                                        _stream(stream)), "mxfp4_grouped_forward")
+
+
+def mxfp4_grouped_backward(layer, dy, lddy, offsets, rows, stream=None) -> None:
+    _check(load().mxfp4_grouped_backward(layer, _ptr(dy), lddy, _ptr(offsets), rows, _stream(stream)),
+           "mxfp4_grouped_backward")
 
 
 def mxfp4_adamw(count, tensors, flags, params, stream=None) -> None:

@@ -41,6 +41,8 @@ class AdamW:
         self.steps = 0
         self._numel = [p.numel() for p in self.params]
         self._table = np.zeros(len(self.params), dtype=_TABLE)
+        self._grads = self._table["g"]   # views and addresses that every step uses
+        self._address = self._table.ctypes.data
         self._fill()
 
     @staticmethod
@@ -81,16 +83,17 @@ class AdamW:
         dtype = grads[0].dtype
         if dtype not in (torch.float32, torch.bfloat16) or len(grads) != len(self.params):
             raise ValueError("one fp32 or bf16 gradient for each parameter")
-        for g, n in zip(grads, self._numel):
-            if g.dtype != dtype or g.numel() != n or not g.is_contiguous():
-                raise ValueError("gradients: contiguous, of one type and the parameters' sizes")
+        addresses = [g.data_ptr() for g, n in zip(grads, self._numel)
+                     if g.dtype is dtype and g.numel() == n and g.is_contiguous()]
+        if len(addresses) != len(self.params):
+            raise ValueError("gradients: contiguous, of one type and the parameters' sizes")
         if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != 4 or not dynamic.is_cuda):
             raise ValueError("dynamic: four fp32 on the device")
         self.steps = self.steps + 1 if step is None else step
-        self._table["g"] = [g.data_ptr() for g in grads]
+        self._grads[:] = addresses
         flags = (abi.MXFP4_ADAMW_P_F32 if self.dtype == torch.float32 else 0) | \
                 (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0) | \
                 (abi.MXFP4_ADAMW_STATE_E4M3 if self.state_bits == 8 else 0)
         h = abi.AdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                             grad_scale, self.steps, None if dynamic is None else dynamic.data_ptr())
-        abi.mxfp4_adamw(len(self.params), self._table.ctypes.data, flags, h, stream)
+        abi.mxfp4_adamw(len(self.params), self._address, flags, h, stream)

@@ -82,6 +82,57 @@ def test_gemm_refusals(lib):
     assert call(form=2, rows=0, a_q=None, a_s=None, b_q=None, b_s=None, c=None) == bad
 
 
+def layer_struct(**change):
+    f = dict(groups=2, N=8, K=24, y=0x1000, dx=0x2000, dw=0x3000, out_dtype=0,
+             x_blobs=(16, 32, 48, 64), w_blobs=(80, 96, 112, 128), dy_blobs=(144, 160, 176, 192))
+    f.update(change)
+    c = abi.GroupedLinear(**{k: v for k, v in f.items() if not k.endswith("blobs")})
+    for name in ("x_blobs", "w_blobs", "dy_blobs"):
+        getattr(c, name)[:] = f[name]
+    return c
+
+
+def test_layer_call_refusals(lib):
+    bad, mis = abi.MXFP4_ERR_INVALID_ARG, abi.MXFP4_ERR_MISALIGNED
+
+    def fwd(x=16, x_rows=8, ldx=24, row_index=None, offsets=64, rows=8, w=32, **change):
+        return lib.mxfp4_grouped_forward(layer_struct(**change), x, x_rows, ldx, row_index, offsets, rows, w, None)
+
+    def bwd(dy=16, lddy=8, offsets=64, rows=8, **change):
+        return lib.mxfp4_grouped_backward(layer_struct(**change), dy, lddy, offsets, rows, None)
+
+    assert lib.mxfp4_grouped_forward(None, 16, 8, 24, None, 64, 8, None, None) == bad
+    assert fwd(offsets=None) == bad and fwd(x=None) == bad and fwd(rows=-1) == bad and fwd(rows=9) == bad
+    assert fwd(groups=0) == bad and fwd(groups=2**40) == bad and fwd(N=2**31) == bad and fwd(y=None) == bad
+    assert fwd(x_blobs=(None, 32, None, None)) == bad and fwd(x_blobs=(16, 32, 48, None)) == bad
+    assert fwd(w_blobs=(None, 96, None, None), w=None) == bad
+    assert fwd(ldx=28) == mis and fwd(w=40) == mis and fwd(x=20) == mis and fwd(y=0x1008) == mis
+    assert fwd(K=20, ldx=24) == mis                  # W's rows of 20 elements are not 16 bytes apart
+    assert lib.mxfp4_grouped_backward(None, 16, 8, 64, 8, None) == bad
+    assert bwd(offsets=None) == bad and bwd(dy=None) == bad and bwd(lddy=7) == bad
+    assert bwd(dx=None) == bad and bwd(dw=None) == bad
+    for name in ("x_blobs", "w_blobs", "dy_blobs"):  # the col blobs of a training layer
+        assert bwd(**{name: (16, 32, None, None)}) == bad
+    assert bwd(dy=24) == mis and bwd(lddy=12) == mis and bwd(dw=0x3004) == mis
+
+
+def test_layer_refusals():
+    import torch
+    from mxfp4_block_scaled_quantize_gb300.grouped import MXFP4GroupedLinear
+    L = MXFP4GroupedLinear(2, 8, 24, 10, train=False, device="cpu")
+    x, o = torch.zeros(4, 24, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    w = torch.zeros(2, 8, 24, dtype=torch.bfloat16)
+    for args in ((x, None, o), (x, w.float(), o), (x, w[:, :, :16], o), (x.float(), w, o), (x[:, :16], w, o),
+                 (x, w, o[:2]), (x, w, o.long()), (torch.zeros(11, 24, dtype=torch.bfloat16), w, o),
+                 (x, w, o, torch.zeros(11, dtype=torch.int32)), (x, w, o, torch.zeros(4))):
+        with pytest.raises(ValueError):
+            L.forward(*args)
+    with pytest.raises(ValueError):
+        L.backward(x[:, :8].contiguous(), o)
+    with pytest.raises(ValueError):
+        MXFP4GroupedLinear(2, 8, 24, 10, device="cpu", out_dtype=torch.float16)
+
+
 def test_no_usable_device_fails_loudly(lib):
     import torch
     if torch.cuda.is_available():
