@@ -58,11 +58,14 @@ mxfp4_status check(const Quantize& t) {
     if (t.x_rows < 0 || t.x_rows > kMaxDim || t.ldx < t.K || t.ldx > kMaxDim) return MXFP4_ERR_INVALID_ARG;
     if (t.row_index == nullptr && t.x_rows < t.rows) return MXFP4_ERR_INVALID_ARG;
     if ((t.blob[2] == nullptr) != (t.blob[3] == nullptr)) return MXFP4_ERR_INVALID_ARG;
-    if (t.rows > 0 && (!t.blob[0] || !t.blob[1] || (!t.x && t.x_rows > 0))) return MXFP4_ERR_INVALID_ARG;
+    if (t.rows > 0 && (!t.blob[0] || !t.blob[1] || !t.x || t.x_rows < 1)) return MXFP4_ERR_INVALID_ARG;
     if (!aligned16(t.x) || t.ldx % 8 != 0 || !aligned(t.row_index, 4) || !aligned(t.offsets, 4))
         return MXFP4_ERR_MISALIGNED;
     for (const void* p : t.blob)
         if (!aligned16(p)) return MXFP4_ERR_MISALIGNED;
+    // two tensors' tiles are counted in 32 bits
+    if (most_tiles(t.rows, t.groups, t.offsets == nullptr, 128) * (pad128(t.K) / 128) > (int64_t{1} << 30) - 1)
+        return MXFP4_ERR_INVALID_ARG;
     return MXFP4_OK;
 }
 
@@ -98,9 +101,9 @@ bool blob_maps(CUtensorMap* q, CUtensorMap* s, const void* qp, const void* sp, i
                                 groups, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-mxfp4_status launch(const Quantize& t, const Device& dev, cudaStream_t stream) {
-    mxfp4::GroupedQuantArgs a;
-    std::memset(&a, 0, sizeof(a));
+// Appends a checked tensor with rows to the batch.
+mxfp4_status append(const Quantize& t, const Device& dev, mxfp4::GroupedQuantBatch* b) {
+    mxfp4::GroupedQuantArgs& a = b->task[b->count];
     a.x = static_cast<const uint16_t*>(t.x);
     a.ldx = t.ldx;
     a.K = t.K;
@@ -118,7 +121,25 @@ mxfp4_status launch(const Quantize& t, const Device& dev, cudaStream_t stream) {
     a.ldq_row = pad128(t.K) / 2;
     a.ldq_col = static_cast<int64_t>(a.tiles_r) * 64;
     a.err = dev.err;
-    return mxfp4::launch_quantize_grouped(a, dev.sms, stream) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+    if (t.row_index == nullptr &&
+        !mxfp4::encode_map_2d(&b->map[b->count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t.x, static_cast<uint64_t>(t.K),
+                              static_cast<uint64_t>(t.x_rows), static_cast<uint64_t>(t.ldx) * 2, 64, 128,
+                              CU_TENSOR_MAP_SWIZZLE_128B))
+        return MXFP4_ERR_CUDA;
+    ++b->count;
+    return MXFP4_OK;
+}
+
+// t, and then `also` where it is given and both write both blobs, in one launch; else in two.
+mxfp4_status launch(const Quantize& t, const Quantize* also, const Device& dev, cudaStream_t stream) {
+    mxfp4::GroupedQuantBatch b;
+    std::memset(&b, 0, sizeof(b));
+    const bool together = also != nullptr && t.blob[2] != nullptr && also->blob[2] != nullptr;
+    mxfp4_status st = append(t, dev, &b);
+    if (st == MXFP4_OK && together) st = append(*also, dev, &b);
+    if (st != MXFP4_OK) return st;
+    if (mxfp4::launch_quantize_grouped(b, dev.sms, stream) != cudaSuccess) return MXFP4_ERR_CUDA;
+    return also != nullptr && !together ? launch(*also, nullptr, dev, stream) : MXFP4_OK;
 }
 
 mxfp4_status launch(const Product& t, const Device& dev, cudaStream_t stream) {
@@ -205,7 +226,7 @@ mxfp4_status mxfp4_quantize_grouped(const void* x, int64_t x_rows, int64_t K, in
     Device dev;
     st = device(&dev);
     if (st != MXFP4_OK || rows == 0) return st;
-    return launch(t, dev, reinterpret_cast<cudaStream_t>(stream));
+    return launch(t, nullptr, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 mxfp4_status mxfp4_gemm_grouped(mxfp4_grouped_form form, const void* a_q, const void* a_s, const void* b_q,
@@ -239,8 +260,10 @@ mxfp4_status mxfp4_grouped_forward(const mxfp4_grouped_linear* l, const void* x,
     st = device(&dev);
     if (st != MXFP4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (w != nullptr) st = launch(qw, dev, s);
-    if (st == MXFP4_OK && rows > 0) st = launch(qx, dev, s);
+    if (rows > 0)
+        st = launch(qx, w != nullptr ? &qw : nullptr, dev, s);
+    else if (w != nullptr)
+        st = launch(qw, nullptr, dev, s);
     return st == MXFP4_OK ? launch(y, dev, s) : st;
 }
 
@@ -264,7 +287,7 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* l, const void* d
     st = device(&dev);
     if (st != MXFP4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (rows > 0) st = launch(q, dev, s);
+    if (rows > 0) st = launch(q, nullptr, dev, s);
     if (st == MXFP4_OK) st = launch(dx, dev, s);
     return st == MXFP4_OK ? launch(dw, dev, s) : st;
 }

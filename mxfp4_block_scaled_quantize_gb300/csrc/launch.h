@@ -159,7 +159,7 @@ struct GroupedQuantArgs {
     const int32_t* offsets;     // groups + 1 offsets into G, or null: equal groups
     int32_t groups;
     int32_t tiles_k;            // Kp / 128
-    int32_t tiles_r;            // capacity of group-padded rows / 128: pitch of the col blob
+    int32_t tiles_r;            // capacity of group-padded rows / 128 (equal groups: their tiles)
     uint8_t* q_row;
     uint8_t* s_row;
     uint8_t* q_col;             // null: row blob only
@@ -168,7 +168,16 @@ struct GroupedQuantArgs {
     int64_t ldq_col;            // capacity / 2
     uint32_t* err;
 };
-cudaError_t launch_quantize_grouped(const GroupedQuantArgs& a, int sms, cudaStream_t stream);
+// Up to two tensors of one launch, both with or both without col blobs, at most one of them with
+// offsets.  map[j]: task j's bf16 X as {K, x_rows}, box {64, 128}, 128-byte swizzle, zero fill;
+// read where its row_index is null.
+constexpr int kGroupedQuantTasks = 2;
+struct GroupedQuantBatch {
+    CUtensorMap map[kGroupedQuantTasks];
+    GroupedQuantArgs task[kGroupedQuantTasks];
+    int32_t count;
+};
+cudaError_t launch_quantize_grouped(const GroupedQuantBatch& b, int sms, cudaStream_t stream);
 
 // Operand maps as for the narrow pair kernel, over all groups' rows or padded rows at once;
 // cmap: C, box {64 bytes of columns, 32 rows}, 64-byte swizzle, read when c_tma.

@@ -53,6 +53,7 @@ def test_quantize_refusals(lib):
     assert call(q_col=None) == bad and call(s_col=None) == bad          # both or neither
     assert call(K=0) == bad and call(ldx=0) == bad and call(rows=-1) == bad and call(x_rows=-1) == bad
     assert call(groups=0) == bad and call(groups=1025) == bad
+    assert call(x_rows=0) == bad                                         # rows from nowhere
     assert call(row_index=None, x_rows=7) == bad                         # fewer rows than G without an index
     assert call(offsets=None, rows=7) == bad                             # equal groups of 3.5 rows
     assert call(x=24) == mis and call(ldx=12) == mis and call(q_row=40) == mis and call(s_row=88) == mis
