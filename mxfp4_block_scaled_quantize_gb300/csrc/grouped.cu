@@ -8,6 +8,10 @@
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 512;
+constexpr int64_t kTileConstant = 320; // of the cost of a tile, in columns
+// Tokens a group, on average, up to which the few-token products run (8 groups, 4096 x 4096: 26.6 us
+// against 30.6 at 96 tokens, 34.8 against 32.7 at 192).
+constexpr int64_t kFewTokens = 96;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t pad128(int64_t n) { return cdiv(n, 128) * 128; }
@@ -83,22 +87,36 @@ mxfp4_status check(const Product& t) {
     if (!aligned16(t.a_q) || !aligned16(t.a_s) || !aligned16(t.b_q) || !aligned16(t.b_s) || !aligned16(t.c) ||
         !aligned(t.offsets, 4))
         return MXFP4_ERR_MISALIGNED;
-    const int64_t tiles = wgrad ? t.groups * cdiv(t.N, 256) * cdiv(t.K, 256)
-                                : most_tiles(t.rows, t.groups, t.offsets == nullptr, 256) * cdiv(cols, 256);
+    const int64_t tiles = wgrad ? t.groups * cdiv(t.N, 256) * cdiv(t.K, 128)
+                                : most_tiles(t.rows, t.groups, t.offsets == nullptr, 128) * cdiv(cols, 256);
     if (tiles > (int64_t{1} << 31) - 1) return MXFP4_ERR_INVALID_ARG;
     return MXFP4_OK;
 }
 
-// The elements [rows, packed / 2] of a blob, boxes of 128 rows x 128 bytes, and its scales as
-// rows of 128-row atom groups in 8-byte units, boxes of `groups` x 2 atoms.
-bool blob_maps(CUtensorMap* q, CUtensorMap* s, const void* qp, const void* sp, int64_t rows, int64_t packed,
-               int64_t scale_rows, uint32_t groups) {
-    return mxfp4::encode_map_2d(q, CU_TENSOR_MAP_DATA_TYPE_UINT8, qp, static_cast<uint64_t>(packed / 2),
-                                static_cast<uint64_t>(rows), static_cast<uint64_t>(packed / 2), 128, 128,
-                                CU_TENSOR_MAP_SWIZZLE_128B) &&
-           mxfp4::encode_map_2d(s, CU_TENSOR_MAP_DATA_TYPE_UINT64, sp, static_cast<uint64_t>(packed / 128) * 64,
-                                static_cast<uint64_t>(scale_rows / 128), static_cast<uint64_t>(packed / 128) * 512, 128,
-                                groups, CU_TENSOR_MAP_SWIZZLE_NONE);
+// The elements [rows, packed / 2] of a blob, boxes of box_rows rows x 128 bytes.
+bool element_map(CUtensorMap* m, const void* q, int64_t rows, int64_t packed, uint32_t box_rows) {
+    return mxfp4::encode_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, static_cast<uint64_t>(packed / 2),
+                                static_cast<uint64_t>(rows), static_cast<uint64_t>(packed / 2), 128, box_rows,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Its scales as rows of 128-row atom groups in 8-byte units, boxes of box_groups x 2 atoms.
+bool scale_map(CUtensorMap* m, const void* s, int64_t rows, int64_t packed, uint32_t box_groups) {
+    return mxfp4::encode_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, s, static_cast<uint64_t>(packed / 128) * 64,
+                                static_cast<uint64_t>(rows / 128), static_cast<uint64_t>(packed / 128) * 512, 128,
+                                box_groups, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// The operand whose rows are the MMA's M, and the one whose rows are its N.
+bool m_maps(mxfp4::GroupedGemmArgs* g, const void* q, const void* s, int64_t rows, int64_t packed, int64_t scale_rows) {
+    return element_map(&g->amap, q, rows, packed, 128) && scale_map(&g->sfamap, s, scale_rows, packed, 1);
+}
+
+bool n_maps(mxfp4::GroupedGemmArgs* g, const void* q, const void* s, int64_t rows, int64_t packed, int64_t scale_rows,
+            bool few) {
+    for (int i = 0; i < 4; ++i)
+        if (!element_map(&g->bmap[i], q, rows, packed, 16u << i)) return false;
+    return scale_map(&g->sfbmap, s, scale_rows, packed, few ? 1 : 3);
 }
 
 // Appends a checked tensor with rows to the batch.
@@ -142,9 +160,34 @@ mxfp4_status launch(const Quantize& t, const Quantize* also, const Device& dev, 
     return also != nullptr && !together ? launch(*also, nullptr, dev, stream) : MXFP4_OK;
 }
 
-mxfp4_status launch(const Product& t, const Device& dev, cudaStream_t stream) {
+// What a product's kernel may rely on before the launch ahead of it is done: nothing, or that what
+// came before that launch is complete, offsets with it, or W's blob too.
+enum Ready { kNothing, kOffsets, kOffsetsAndW };
+
+// Columns of the tiles of `strips` strips of `cols` columns each (forward, dgrad: a group's tokens on
+// average, all that the host knows of them): the width whose modelled time is least.  The
+// tiles go round the clusters in waves, and a tile costs its columns and a constant.  Wide
+// tiles win as soon as they fill the clusters (wgrad of 64 groups, 1408 x 2048: 94 us, 123 at 128
+// columns); below that narrow ones spread over more of them (5 groups of 222 tokens:
+// 14.0 -> 12.6 us).
+int32_t tile_width(int64_t strips, int64_t cols, int64_t clusters) {
+    int32_t best = 384;
+    int64_t least = INT64_MAX;
+    for (int32_t width = 384; width >= 128; width -= 128) {
+        const int64_t tiles = cdiv(cols, width);
+        const int64_t time = cdiv(strips * tiles, clusters) * (cdiv(cols, tiles) + kTileConstant);
+        if (time < least) {
+            least = time;
+            best = width;
+        }
+    }
+    return best;
+}
+
+mxfp4_status launch(const Product& t, const Device& dev, cudaStream_t stream, Ready ready = kNothing) {
     const bool wgrad = t.form == MXFP4_GROUPED_WGRAD;
-    const int64_t esize = t.out == MXFP4_OUT_F32 ? 4 : 2;
+    const bool f32 = t.out == MXFP4_OUT_F32;
+    const int64_t esize = f32 ? 4 : 2;
     if (t.rows == 0) {
         if (!wgrad) return MXFP4_OK;
         return cudaMemset2DAsync(t.c, static_cast<size_t>(t.ldc * esize), 0, static_cast<size_t>(t.K * esize),
@@ -157,35 +200,30 @@ mxfp4_status launch(const Product& t, const Device& dev, cudaStream_t stream) {
     const bool equal = t.offsets == nullptr;
     const int64_t cap = 128 * most_tiles(t.rows, t.groups, equal, 128);
     const int64_t kp = pad128(t.K), np = pad128(t.N);
+    const bool few = !wgrad && t.rows <= t.groups * kFewTokens;
     bool maps;
     if (t.form == MXFP4_GROUPED_FWD) {
-        maps = blob_maps(&g.amap, &g.sfamap, t.a_q, t.a_s, t.rows, kp, cap, 1) &&
-               blob_maps(&g.bmap, &g.sfbmap, t.b_q, t.b_s, t.groups * t.N, kp, t.groups * np, 2);
+        maps = m_maps(&g, t.b_q, t.b_s, t.groups * t.N, kp, t.groups * np) && n_maps(&g, t.a_q, t.a_s, t.rows, kp, cap, few);
         g.atoms = static_cast<int32_t>(kp / 128);
-        g.b_step_rows = static_cast<int32_t>(t.N);
-        g.b_step_groups = static_cast<int32_t>(np / 128);
-        g.n_cols = t.N;
+        g.a_step_rows = static_cast<int32_t>(t.N);
+        g.a_step_groups = static_cast<int32_t>(np / 128);
+        g.m_rows = static_cast<int32_t>(t.N);
     } else if (t.form == MXFP4_GROUPED_DGRAD) {
-        maps = blob_maps(&g.amap, &g.sfamap, t.a_q, t.a_s, t.rows, np, cap, 1) &&
-               blob_maps(&g.bmap, &g.sfbmap, t.b_q, t.b_s, t.K, t.groups * np, kp, 2);
+        maps = m_maps(&g, t.b_q, t.b_s, t.K, t.groups * np, kp) && n_maps(&g, t.a_q, t.a_s, t.rows, np, cap, few);
         g.atoms = static_cast<int32_t>(np / 128);
-        g.b_step_atoms = static_cast<int32_t>(np / 128);
-        g.n_cols = t.K;
+        g.a_step_atoms = static_cast<int32_t>(np / 128);
+        g.m_rows = static_cast<int32_t>(t.K);
     } else {
-        maps = blob_maps(&g.amap, &g.sfamap, t.a_q, t.a_s, t.N, cap, np, 1) &&
-               blob_maps(&g.bmap, &g.sfbmap, t.b_q, t.b_s, t.K, cap, kp, 2);
-        g.tiles_m = static_cast<int32_t>(cdiv(t.N, 256));
-        g.m_rows = t.N;
-        g.n_cols = t.K;
+        maps = m_maps(&g, t.a_q, t.a_s, t.N, cap, np) && n_maps(&g, t.b_q, t.b_s, t.K, cap, kp, false);
+        g.m_rows = static_cast<int32_t>(t.N);
+        g.n_cols = static_cast<int32_t>(t.K);
     }
     if (!maps) return MXFP4_ERR_CUDA;
-    g.tiles_n = static_cast<int32_t>(cdiv(g.n_cols, 256));
-    const int64_t tiles = wgrad ? t.groups * g.tiles_m * g.tiles_n : most_tiles(t.rows, t.groups, equal, 256) * g.tiles_n;
+    g.tiles_m = static_cast<int32_t>(cdiv(g.m_rows, 256));
+    const int64_t cols = wgrad ? t.K : g.m_rows;
     g.c_tma = (t.ldc * esize) % 16 == 0 &&
-              mxfp4::encode_map_2d(&g.cmap, t.out == MXFP4_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                   t.c, static_cast<uint64_t>(g.n_cols),
-                                   static_cast<uint64_t>(wgrad ? t.groups * t.N : t.rows),
+              mxfp4::encode_map_2d(&g.cmap, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t.c,
+                                   static_cast<uint64_t>(cols), static_cast<uint64_t>(wgrad ? t.groups * t.N : t.rows),
                                    static_cast<uint64_t>(t.ldc * esize), static_cast<uint32_t>(64 / esize), 32,
                                    CU_TENSOR_MAP_SWIZZLE_64B);
     g.offsets = t.offsets;
@@ -193,12 +231,16 @@ mxfp4_status launch(const Product& t, const Device& dev, cudaStream_t stream) {
     g.rows = static_cast<int32_t>(t.rows);
     g.c = t.c;
     g.ldc = t.ldc;
-    g.out_f32 = t.out == MXFP4_OUT_F32 ? 1 : 0;
+    g.out_f32 = f32 ? 1 : 0;
+    g.early_offsets = ready != kNothing;
+    g.early_m = ready == kOffsetsAndW;
     g.err = dev.err;
     const int most = mxfp4::gemm_grouped_max_clusters();
     if (most <= 0) return MXFP4_ERR_CUDA;
+    g.width = few ? 128 : tile_width(t.groups * g.tiles_m, wgrad ? t.K : cdiv(t.rows, t.groups), most);
+    const int64_t tiles = g.tiles_m * (wgrad ? t.groups * cdiv(t.K, g.width) : most_tiles(t.rows, t.groups, equal, 128));
     const int clusters = static_cast<int>(tiles < most ? tiles : most);
-    return mxfp4::launch_gemm_grouped(g, wgrad, clusters, stream) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+    return mxfp4::launch_gemm_grouped(g, wgrad, few, clusters, stream) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
 }
 
 }  // namespace
@@ -264,7 +306,8 @@ mxfp4_status mxfp4_grouped_forward(const mxfp4_grouped_linear* l, const void* x,
         st = launch(qx, w != nullptr ? &qw : nullptr, dev, s);
     else if (w != nullptr)
         st = launch(qw, nullptr, dev, s);
-    return st == MXFP4_OK ? launch(y, dev, s) : st;
+    // the quantizers let a launch start only when all before them is complete
+    return st == MXFP4_OK ? launch(y, dev, s, rows == 0 ? kNothing : w == nullptr ? kOffsetsAndW : kOffsets) : st;
 }
 
 mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* l, const void* dy, int64_t lddy, const int32_t* offsets,
@@ -288,8 +331,8 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* l, const void* d
     if (st != MXFP4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows > 0) st = launch(q, nullptr, dev, s);
-    if (st == MXFP4_OK) st = launch(dx, dev, s);
-    return st == MXFP4_OK ? launch(dw, dev, s) : st;
+    if (st == MXFP4_OK) st = launch(dx, dev, s, rows > 0 ? kOffsetsAndW : kNothing);
+    return st == MXFP4_OK ? launch(dw, dev, s, rows > 0 ? kOffsets : kNothing) : st;
 }
 
 }  // extern "C"

@@ -179,29 +179,35 @@ struct GroupedQuantBatch {
 };
 cudaError_t launch_quantize_grouped(const GroupedQuantBatch& b, int sms, cudaStream_t stream);
 
-// Operand maps as for the narrow pair kernel, over all groups' rows or padded rows at once;
-// cmap: C, box {64 bytes of columns, 32 rows}, 64-byte swizzle, read when c_tma.
+// The operand whose rows are the MMA's M (forward, dgrad: W; wgrad: dY): amap, box 128 rows,
+// sfamap, box one 128-row scale group; the one whose rows are its N (tokens; wgrad: X): bmap[i],
+// box 16 << i rows, sfbmap, box three scale groups (few: one).  All over all groups' rows or
+// padded rows at once, element boxes 128 bytes wide, 128-byte swizzle.  cmap (read when c_tma): C,
+// box 32 rows x 64 bytes of columns, 64-byte swizzle.
 struct GroupedGemmArgs {
-    CUtensorMap amap, bmap, sfamap, sfbmap, cmap;
+    CUtensorMap amap, bmap[4], sfamap, sfbmap, cmap;
     const int32_t* offsets;
     int32_t groups;
     int32_t rows;               // rows of G
-    int32_t atoms;              // forward, dgrad: Kp / 128
-    int32_t tiles_m;            // wgrad: ceil(m_rows / 256)
-    int32_t tiles_n;            // ceil(n_cols / 256)
-    int32_t b_step_rows;        // from one group's B to the next: rows of the elements,
-    int32_t b_step_groups;      // 128-row scale groups (forward),
-    int32_t b_step_atoms;       // atoms along the packed axis (dgrad)
-    int64_t m_rows;             // wgrad: rows of a group's output
-    int64_t n_cols;             // output columns
+    int32_t atoms;              // forward, dgrad: Kp / 128 of the reduction
+    int32_t tiles_m;            // 256-row tiles of the M operand in a group
+    int32_t a_step_rows;        // forward, dgrad: from one group's W to the next: rows of the elements,
+    int32_t a_step_groups;      // 128-row scale groups (forward),
+    int32_t a_step_atoms;       // atoms along the packed axis (dgrad)
+    int32_t m_rows;             // rows of the M operand in a group (forward, dgrad: columns of C)
+    int32_t n_cols;             // wgrad: columns of C
     void* c;
     int64_t ldc;
     int32_t out_f32;
     int32_t c_tma;
+    int32_t width;              // most columns of a tile: 128 (few), 256 or 384
+    int32_t early_offsets;      // offsets are complete, and C free, before the launch ahead of this one starts
+    int32_t early_m;            // and so is the M operand (with early_offsets)
     uint32_t* err;
 };
 int gemm_grouped_max_clusters();   // co-resident clusters, 0 if none
-cudaError_t launch_gemm_grouped(const GroupedGemmArgs& a, bool wgrad, int clusters, cudaStream_t stream);
+// few (forward, dgrad): the instance for few tokens a group.
+cudaError_t launch_gemm_grouped(const GroupedGemmArgs& a, bool wgrad, bool few, int clusters, cudaStream_t stream);
 
 // ---- host helpers of the C ABI (api.cu) ----------------------------------------------------
 // The current device's SM count and error word; an mxfp4_status.

@@ -147,6 +147,20 @@ __device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t count, b
     return r != 0;
 }
 
+// Named barrier over `count` threads (whole warps) that also returns how many participants
+// brought a true `v`: a hand-over that carries a small number.
+__device__ __forceinline__ uint32_t named_barrier_count(uint32_t id, uint32_t count, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.popc.u32 %0, %2, %3, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(count)
+        : "memory");
+    return r;
+}
+
 // Whole (converged) warp: true in exactly one lane.  Tensor-core work issued from a lane
 // chosen this way keeps the warp converged; issuing it from `lane == 0` branches instead
 // makes every scale copy wait on the MMAs queued before it.
@@ -170,6 +184,12 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last() {
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 

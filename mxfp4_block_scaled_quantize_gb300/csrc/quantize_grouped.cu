@@ -76,8 +76,8 @@ __device__ __forceinline__ int source_row(const GroupedQuantArgs& p, int i) {
 // Padded row tile gt of a task: its group by the table, or by division for equal groups.
 __device__ __forceinline__ void place_rows(const GroupedQuantArgs& p, const GroupTable& table, int gt, int* row0, int* live) {
     if (p.offsets == nullptr) {
-        const int m = p.rows / p.groups, per = (m + kQT - 1) / kQT;
-        const int e = gt / per, j = gt - e * per;
+        int j;
+        const int m = p.rows / p.groups, e = small_div(gt, (m + kQT - 1) / kQT, &j);
         *row0 = e * m + j * kQT;
         *live = min(m - j * kQT, kQT);
     } else {
@@ -169,12 +169,13 @@ __device__ __forceinline__ void quantize_tile(const GroupedQuantArgs& p, const T
 __device__ __forceinline__ bool locate(const GroupedQuantBatch& P, const GroupTable& table, int end0, int t, Tile& at) {
     const int j = t < end0 ? 0 : 1;
     const GroupedQuantArgs& p = P.task[j];
-    const int in = t - (j > 0 ? end0 : 0), gt = in / p.tiles_k;
+    int tk;
+    const int gt = small_div(t - (j > 0 ? end0 : 0), p.tiles_k, &tk);
     const bool same = at.task == j && at.gt == gt;
     if (!same) place_rows(p, table, gt, &at.row0, &at.live);
     at.task = j;
     at.gt = gt;
-    at.tk = in - gt * p.tiles_k;
+    at.tk = tk;
     return same;
 }
 

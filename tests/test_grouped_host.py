@@ -146,26 +146,29 @@ def test_no_usable_device_fails_loudly(lib):
 
 
 def group_table(offsets, groups, rows):
-    """csrc/group_table.cuh, lane by lane."""
-    per = (groups + 1 + 31) // 32
-    start, tops = [None] * (groups + 1), []
-    for lane in range(32):
-        top = 0
-        for e in range(lane * per, min(lane * per + per, groups + 1)):
-            top = max(top, min(max(offsets[e], 0), rows))
-            start[e] = top
-        tops.append(top)
-    carry = 0
-    for lane in range(32):
-        for e in range(lane * per, min(lane * per + per, groups + 1)):
-            if start[e] >= carry:
-                break
-            start[e] = carry
-        carry = max(carry, tops[lane])
-    tiles = [0]
-    for e in range(groups):
-        tiles.append(tiles[-1] + (start[e + 1] - start[e] + 127) // 128)
-    return start, tiles
+    """csrc/group_table.cuh, chunk by chunk and lane by lane: starts, 128-row tiles before, refused."""
+    start, tiles, bad = [0] * (groups + 1), [0] * (groups + 1), False
+    top = total = 0
+    for base in range(0, groups + 1, 32):
+        cur = [offsets[min(base + lane, groups)] for lane in range(32)]
+        last = offsets[min(base + 32, groups)]
+        nxt = cur[1:] + [last]
+        if any(c < top or c > rows or n < c or n > rows for c, n in zip(cur, nxt)):
+            bad = True
+            cur = [max(min(c, rows), top) for c in cur]
+            nxt = [max(min(n, rows), top) for n in nxt]
+            for lane in range(1, 32):
+                cur[lane] = max(cur[lane], cur[lane - 1])
+            nxt = [max(n, c) for n, c in zip(nxt, cur)]
+            nxt = cur[1:] + [nxt[31]]
+        for lane in range(32):
+            e = base + lane
+            if e <= groups:
+                start[e], tiles[e] = cur[lane], total
+            if e < groups:
+                total += (nxt[lane] - cur[lane] + 127) // 128
+        top = nxt[31]
+    return start, tiles, bad
 
 
 def test_group_table_stays_inside_the_buffers(lib):
@@ -176,6 +179,26 @@ def test_group_table_stays_inside_the_buffers(lib):
         o = [rng.randint(-2 * rows - 3, 3 * rows + 3) for _ in range(groups + 1)]
         if rng.random() < 0.5:
             o.sort()
-        start, tiles = group_table(o, groups, rows)
+        start, tiles, bad = group_table(o, groups, rows)
         assert all(0 <= s <= rows for s in start) and start == sorted(start)
+        assert tiles == [sum((b - a + 127) // 128 for a, b in zip(start[:e], start[1:e + 1])) for e in range(groups + 1)]
         assert 128 * tiles[-1] <= abi.mxfp4_grouped_sizes(rows, 8, groups)[4]
+        want, top = [], 0
+        for x in o:
+            top = max(top, min(max(x, 0), rows))
+            want.append(top)
+        assert start == want and bad == (want != o)
+
+
+
+def test_waves_deal_every_tile_once(lib):
+    # csrc/gemm_grouped.cu: cluster c takes tile w n + (c + w) % n of wave w
+    for n in (1, 2, 5, 76):
+        for total in (0, 1, n - 1, n, n + 1, 3 * n + 2, 500):
+            got = []
+            for c in range(n):
+                w = 0
+                while (i := w * n + (c + w) % n) < total:
+                    got.append(i)
+                    w += 1
+            assert sorted(got) == list(range(total))
