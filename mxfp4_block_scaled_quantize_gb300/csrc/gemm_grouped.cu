@@ -14,9 +14,10 @@
 // In forward and dgrad the rows of W are the MMA's M and the tokens its N: W's tiles of 256 rows
 // are always whole, and the tokens of a group, of which there may be one or ten thousand, are
 // cut into tiles of 384 and a last one of any multiple of 32, which takes that much less of the
-// tensor pipe and of the operand bytes, the scarcest thing here.  (With the tokens as M, 256 rows a
-// tile, and single accumulators: 64 experts of 384 tokens on average 54 us forward, 50 here; 8 experts
-// of 2048 tokens 122 and 110; 4 tokens an expert 31 and 26.)  The accumulator then
+// tensor pipe and of the operand bytes, the scarcest thing here.  (With the tokens as M, in tiles of
+// 256 rows, forward took, in us: 64 groups of 384 tokens on average, 1408 x 2048, 57.4, and 55.3 here;
+// 8 groups of 2048, 8192 x 2048, 133.1 and 112.6; 64 groups of 4, 2048 x 2048, 38.9 and 32.8; 8 single
+// tokens 14.3 both.)  The accumulator then
 // holds C transposed, and the epilogue turns 32 x 32 pieces round in shared memory.  What a tile
 // holds past its group are the next group's rows: their products are never stored, and an
 // FP4 product has no NaN to spread.  A group without rows has no tile in forward and dgrad,
@@ -29,13 +30,14 @@
 //
 // The few-token instances (launches whose groups have some 96 tokens or fewer on average) have
 // tiles of up to 128 tokens and seven stages in place of four: they are bound by the stream of
-// W, which needs the more bytes in flight.
+// W, which needs the more bytes in flight.  (64 groups of 8 tokens, 2048 x 2048: 38.9 us, 45.1 by the
+// other instance; of 96 tokens 41.0 and 47.1; of 192, two tiles, 55.3 and 49.2.)
 //
 // Roles as in the pair kernel (gemm_pair.cu).  The clusters take the tiles round-robin (the token
 // tiles of one W tile in turn, then the next W tile), each wave rotated by one cluster, or clusters
 // would keep meeting tiles of one size: neighbours then read the same W tile, or the same
-// tokens, at the same time.  (A contiguous run of tiles for each cluster, balanced by cost, lost
-// 40 %.)  The MMA warp must not touch shared memory with MMAs in flight, so the
+// tokens, at the same time.  (A contiguous run of tiles for each cluster, balanced by cost, took 178 us
+// where this took 125: forward of 32 groups of 512 tokens on average, 4096 x 4096.)  The MMA warp must not touch shared memory with MMAs in flight, so the
 // waiter hands it what it has to know of a tile with every stage, as the count of a barrier
 // reduction.
 #include <cuda_bf16.h>

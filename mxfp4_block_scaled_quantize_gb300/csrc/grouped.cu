@@ -166,10 +166,11 @@ enum Ready { kNothing, kOffsets, kOffsetsAndW };
 
 // Columns of the tiles of `strips` strips of `cols` columns each (forward, dgrad: a group's tokens on
 // average, all that the host knows of them): the width whose modelled time is least.  The
-// tiles go round the clusters in waves, and a tile costs its columns and a constant.  Wide
-// tiles win as soon as they fill the clusters (wgrad of 64 groups, 1408 x 2048: 94 us, 123 at 128
-// columns); below that narrow ones spread over more of them (5 groups of 222 tokens:
-// 14.0 -> 12.6 us).
+// tiles go round the clusters in waves, and a tile costs its columns and a constant.  A whole training
+// step at 384, 256 and 128 columns throughout, in us: 64 groups of 384 tokens, 1408 x 2048, 349, 357,
+// 425; 8 of 2048, 8192 x 2048, 485, 533, 736; 5 of 222 in fp32 with few tiles to go round 56.0, 53.7,
+// 53.9, where the rule's own mixture takes 53.1.  The constant came from the first two: at 256 the
+// rule took 256 columns for the second one's dgrad, and that step 502 us; it now takes 481.
 int32_t tile_width(int64_t strips, int64_t cols, int64_t clusters) {
     int32_t best = 384;
     int64_t least = INT64_MAX;
