@@ -32,9 +32,10 @@ namespace mxfp4 {
 namespace {
 
 // Threads of a CTA.  With 8-bit moments the arithmetic (some 65 instructions an element) nearly
-// fills the time of the memory, and many small CTAs keep both busy: 288 M elements took 877 us
-// with 256 threads a CTA, 830 with 128, 750 with 64, 725 (6.4 TB/s, 0.96 of the measured copy) with
-// one warp.  With fp32 moments 128 threads were fastest (7.1 TB/s on 72 M elements).
+// fills the time of the memory, and many small CTAs keep both busy: one warp takes 717 us for 288 M
+// elements (6.5 TB/s, 0.97 of the measured copy), four warps 754; for 140 M in tensors of odd sizes
+// with fp32 gradients 473 and 455.  With fp32 moments, 72 M elements in 48 tensors, 128 threads take
+// 320 us (6.3 TB/s), 64 322 and one warp 326.
 constexpr int kThreads32 = 128;   // fp32 moments
 constexpr int kThreads8 = 32;     // 8-bit moments
 constexpr float kE4m3Max = 448.0f;

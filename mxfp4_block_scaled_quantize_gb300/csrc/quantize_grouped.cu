@@ -16,7 +16,7 @@
 //                measured copy rate).  Gathered rows come from anywhere in X: every thread
 //                fetches its share of a tile two ahead with 16-byte cp.async.  (50 M elements
 //                gathered from 4096 rows: gathering tensor copies, four rows each, took 71 us, cp.async
-//                from two producer warps 92 us, this 42.)
+//                from two producer warps 92 us, this 43.)
 //   row blob     no shared memory: a warp takes a 1024-element piece of one row, so that a
 //                single token's row is spread over as many warps as it has pieces; its loads and
 //                stores are whole lines (a lane holding a whole block read 16 bytes of each of 32
@@ -39,7 +39,7 @@ constexpr int kWarps = 8;                         // that quantize
 constexpr int kThreads = (kWarps + 1) * 32;       // + the producer
 constexpr int kGatherThreads = kWarps * 32;       // no producer: each thread fetches its share
 constexpr int kRowThreads = 128;
-constexpr int kSharedTilesPerCta = 2;             // most tiles a CTA of a launch that two tensors share
+constexpr int kSharedTilesPerCta = 12;            // most tiles a CTA of a launch that two tensors share
 
 // A 128 x 128 tile of a task.
 struct Tile {
@@ -474,8 +474,11 @@ cudaError_t launch_quantize_grouped(const GroupedQuantBatch& b, int sms, cudaStr
     const bool gather = b.task[0].row_index != nullptr || (b.count > 1 && b.task[1].row_index != nullptr);
     const int64_t tiles = tiles_of(b.task[0]) + (b.count > 1 ? tiles_of(b.task[1]) : 0);
     if (b.count > 1 && gather && tiles > static_cast<int64_t>(sms) * 2 * kSharedTilesPerCta) {
-        // Two small tensors share the gathering kernel's launch (8 experts of 512 x 512 and 1024
-        // rows: 13 us against 7 + 8 in two, and one launch less); larger ones each take the kernel that they need.
+        // Two small tensors share the gathering kernel's launch, larger ones each take the kernel
+        // that they need.  A training step, shared and apart, in us: 8 groups of 512 x 512 and 1024
+        // rows 29.5 and 33.9; 8 of 1536 x 1536, 2048 rows, 60.3 and 64.8; 8 of 2048 x 2048, 8192
+        // rows (10 tiles a CTA), 124 and 128; 16 of them, 4096 rows (16 a CTA), 130.7 and 129.8;
+        // 64 of 1408 x 2048, 24576 rows, 357 and 348.
         for (int j = 0; j < b.count; ++j) {
             GroupedQuantBatch one = b;
             one.task[0] = b.task[j];
