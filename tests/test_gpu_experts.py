@@ -7,9 +7,19 @@ import torch
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 import experts  # noqa: E402
+from mxfp4_block_scaled_quantize_gb300 import abi  # noqa: E402
 from mxfp4_block_scaled_quantize_gb300.grouped import MXFP4GroupedLinear  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    yield
+    assert abi.mxfp4_last_device_error() == abi.MXFP4_OK
 
 
 def test_experts_learn_and_serve():
