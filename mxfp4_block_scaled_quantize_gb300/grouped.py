@@ -36,6 +36,7 @@ class MXFP4GroupedLinear:
         self.x_blobs = abi.alloc_grouped_blobs(max_rows, K, groups, dual=train, device=device)
         self.y = torch.empty((max_rows, N), dtype=out_dtype, device=device)
         self.w_blobs = None
+        self._has_w = False   # w_blobs hold the blobs of some W
         self._c = abi.GroupedLinear(groups, N, K, out_dtype=code, y=self.y.data_ptr())
         self._c.x_blobs[:] = _addresses(self.x_blobs)
         if train:
@@ -73,6 +74,7 @@ class MXFP4GroupedLinear:
         blobs = self.w_blobs if self.train else self.w_blobs + (None, None)
         abi.mxfp4_quantize_grouped(w, self.groups * self.N, self.K, self.K, None, None, self.groups,
                                    self.groups * self.N, *blobs, stream)
+        self._has_w = True
 
     def _forward(self, x, w, offsets, rows, stream):
         ldx = self._pitch(x, self.K)
@@ -87,13 +89,15 @@ class MXFP4GroupedLinear:
         return self.y if R == self.max_rows else self.y[:R]
 
     def forward(self, x, w, offsets, rows=None, stream=None):
-        """Y [R, N] in the grouped order; w None: the weights of the last quantize_w."""
+        """Y [R, N] in the grouped order; w None: the weights of the last quantize_w or forward."""
         if w is not None:
             self._check_w(w)
-        elif self.w_blobs is None:
+        elif not self._has_w:
             raise ValueError("no weights quantized yet")
         self._c.w_blobs[0], self._c.w_blobs[1] = self.w_blobs[0].data_ptr(), self.w_blobs[1].data_ptr()
-        return self._forward(x, w, offsets, rows, stream)
+        y = self._forward(x, w, offsets, rows, stream)
+        self._has_w = True
+        return y
 
     def forward_packed(self, x, w_q, w_s, offsets, rows=None, stream=None):
         """Y [R, N] with the row blob of the weights (codes [E * N, Kp / 2], scales in the tensor-core

@@ -1,0 +1,47 @@
+"""Refusals of the grouped layer that need no GPU: the order of its calls and what it is handed."""
+import pytest
+import torch
+
+from mxfp4_block_scaled_quantize_gb300 import abi
+from mxfp4_block_scaled_quantize_gb300.grouped import MXFP4GroupedLinear
+
+E, N, K, R = 2, 8, 24, 10
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls, noted instead of made."""
+    made = []
+    for name in ("mxfp4_quantize_grouped", "mxfp4_grouped_forward", "mxfp4_grouped_backward"):
+        monkeypatch.setattr(abi, name, lambda *a, _name=name, **k: made.append((_name, a)))
+    return made
+
+
+def layer(train=True):
+    return MXFP4GroupedLinear(E, N, K, R, train=train, device="cpu")
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+OFFSETS = torch.zeros(E + 1, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("train", [True, False])
+def test_products_need_weights_that_were_quantized(train, calls):
+    ours = layer(train)
+    with pytest.raises(ValueError, match="no weights quantized"):
+        ours.forward(bf16(4, K), None, OFFSETS)
+    assert not calls
+    ours.quantize_w(bf16(E, N, K))
+    ours.forward(bf16(4, K), None, OFFSETS)
+    ours = layer(train)
+    ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)   # quantizes them too
+    ours.forward(bf16(4, K), None, OFFSETS)
