@@ -37,6 +37,7 @@ class MXFP4GroupedLinear:
         self.y = torch.empty((max_rows, N), dtype=out_dtype, device=device)
         self.w_blobs = None
         self._has_w = False   # w_blobs hold the blobs of some W
+        self._packed = False  # the last forward took its weights from elsewhere
         self._c = abi.GroupedLinear(groups, N, K, out_dtype=code, y=self.y.data_ptr())
         self._c.x_blobs[:] = _addresses(self.x_blobs)
         if train:
@@ -96,20 +97,24 @@ class MXFP4GroupedLinear:
             raise ValueError("no weights quantized yet")
         self._c.w_blobs[0], self._c.w_blobs[1] = self.w_blobs[0].data_ptr(), self.w_blobs[1].data_ptr()
         y = self._forward(x, w, offsets, rows, stream)
-        self._has_w = True
+        self._has_w, self._packed = True, False
         return y
 
     def forward_packed(self, x, w_q, w_s, offsets, rows=None, stream=None):
         """Y [R, N] with the row blob of the weights (codes [E * N, Kp / 2], scales in the tensor-core
-        layout with each expert's rows padded to 128)."""
+        layout with each expert's rows padded to 128).  No backward follows it."""
         self._c.w_blobs[0], self._c.w_blobs[1] = w_q.data_ptr(), w_s.data_ptr()
-        return self._forward(x, None, offsets, rows, stream)
+        y = self._forward(x, None, offsets, rows, stream)
+        self._packed = True
+        return y
 
     def backward(self, dy, offsets, stream=None):
         """dX [R, K] in the grouped order (a token's rows are for the caller to add up) and
         dW [E, N, K], for the X, W and offsets of the last forward."""
         if not self.train:
             raise ValueError("backward needs the column blobs of a training layer")
+        if self._packed:
+            raise ValueError("the last forward took packed weights, which have no column blob")
         lddy, R = self._pitch(dy, self.N), dy.size(0)
         self._check_rows(R, offsets)
         abi.mxfp4_grouped_backward(self._c, dy, lddy, offsets, R, stream)

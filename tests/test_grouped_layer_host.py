@@ -45,3 +45,16 @@ def test_products_need_weights_that_were_quantized(train, calls):
     ours = layer(train)
     ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)   # quantizes them too
     ours.forward(bf16(4, K), None, OFFSETS)
+
+
+def test_packed_weights_have_no_gradient(calls):
+    # dX comes from the col blob of W, which packed weights do not have
+    ours = layer()
+    w_q, w_s = abi.alloc_grouped_blobs(E * N, K, E, equal=True, dual=False, device="cpu")
+    ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)
+    ours.forward_packed(bf16(4, K), w_q, w_s, OFFSETS)
+    with pytest.raises(ValueError, match="packed"):
+        ours.backward(bf16(4, N), OFFSETS)
+    assert "mxfp4_grouped_backward" not in [name for name, _ in calls]
+    ours.forward(bf16(4, K), None, OFFSETS)
+    ours.backward(bf16(4, N), OFFSETS)
