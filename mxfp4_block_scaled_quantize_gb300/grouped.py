@@ -38,6 +38,7 @@ class MXFP4GroupedLinear:
         self.w_blobs = None
         self._has_w = False   # w_blobs hold the blobs of some W
         self._packed = False  # the last forward took its weights from elsewhere
+        self._rows = None     # its rows
         self._c = abi.GroupedLinear(groups, N, K, out_dtype=code, y=self.y.data_ptr())
         self._c.x_blobs[:] = _addresses(self.x_blobs)
         if train:
@@ -87,6 +88,7 @@ class MXFP4GroupedLinear:
                 raise ValueError("rows: contiguous int32 values")
         self._check_rows(R, offsets)
         abi.mxfp4_grouped_forward(self._c, x, x.size(0), ldx, rows, offsets, R, w, stream)
+        self._rows = R
         return self.y if R == self.max_rows else self.y[:R]
 
     def forward(self, x, w, offsets, rows=None, stream=None):
@@ -117,6 +119,9 @@ class MXFP4GroupedLinear:
             raise ValueError("the last forward took packed weights, which have no column blob")
         lddy, R = self._pitch(dy, self.N), dy.size(0)
         self._check_rows(R, offsets)
+        if R != self._rows:   # X's column blob is laid out for that forward's rows
+            raise ValueError(f"{R} rows after " + ("no forward" if self._rows is None else
+                                                   f"a forward of {self._rows} rows"))
         abi.mxfp4_grouped_backward(self._c, dy, lddy, offsets, R, stream)
         return self.dx if R == self.max_rows else self.dx[:R], self.dw
 

@@ -58,3 +58,20 @@ def test_packed_weights_have_no_gradient(calls):
     assert "mxfp4_grouped_backward" not in [name for name, _ in calls]
     ours.forward(bf16(4, K), None, OFFSETS)
     ours.backward(bf16(4, N), OFFSETS)
+
+
+def test_backward_takes_the_rows_of_its_forward(calls):
+    # the row count sets the pitch of X's col blob
+    ours = layer()
+    with pytest.raises(ValueError, match="forward"):
+        ours.backward(bf16(4, N), OFFSETS)
+    ours.forward(bf16(6, K), bf16(E, N, K), OFFSETS)
+    for rows in (5, 7, 0):
+        with pytest.raises(ValueError, match="6 rows"):
+            ours.backward(bf16(rows, N), OFFSETS)
+    assert "mxfp4_grouped_backward" not in [name for name, _ in calls]
+    ours.backward(bf16(6, N), OFFSETS)
+    ours.forward(bf16(3, K), None, OFFSETS, torch.zeros(7, dtype=torch.int32))   # gathered: 7 rows
+    with pytest.raises(ValueError, match="7 rows"):
+        ours.backward(bf16(6, N), OFFSETS)
+    ours.backward(bf16(7, N), OFFSETS)
