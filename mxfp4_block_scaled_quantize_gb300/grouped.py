@@ -35,6 +35,7 @@ class MXFP4GroupedLinear:
         code = abi.MXFP4_OUT_F32 if out_dtype == torch.float32 else abi.MXFP4_OUT_BF16
         self.x_blobs = abi.alloc_grouped_blobs(max_rows, K, groups, dual=train, device=device)
         self.y = torch.empty((max_rows, N), dtype=out_dtype, device=device)
+        self._packed_bytes = abi.mxfp4_grouped_sizes(groups * N, K, groups, equal=True)[:2]
         self.w_blobs = None
         self._has_w = False   # w_blobs hold the blobs of some W
         self._packed = False  # the last forward took its weights from elsewhere
@@ -69,6 +70,11 @@ class MXFP4GroupedLinear:
             self.w_blobs = abi.alloc_grouped_blobs(self.groups * self.N, self.K, self.groups, equal=True, dual=False,
                                                    device=w.device)
             self._c.w_blobs[:] = _addresses(self.w_blobs)
+
+    def _check_packed(self, w_q, w_s):
+        for t, n in zip((w_q, w_s), self._packed_bytes):
+            if not isinstance(t, torch.Tensor) or t.element_size() != 1 or t.numel() < n or not t.is_contiguous():
+                raise ValueError("packed weights: contiguous bytes, {} of codes and {} of scales".format(*self._packed_bytes))
 
     def quantize_w(self, w, stream=None):
         """The blobs of W[E, N, K], kept for the products that follow."""
@@ -105,6 +111,7 @@ class MXFP4GroupedLinear:
     def forward_packed(self, x, w_q, w_s, offsets, rows=None, stream=None):
         """Y [R, N] with the row blob of the weights (codes [E * N, Kp / 2], scales in the tensor-core
         layout with each expert's rows padded to 128).  No backward follows it."""
+        self._check_packed(w_q, w_s)
         self._c.w_blobs[0], self._c.w_blobs[1] = w_q.data_ptr(), w_s.data_ptr()
         y = self._forward(x, None, offsets, rows, stream)
         self._packed = True

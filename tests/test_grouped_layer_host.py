@@ -75,3 +75,19 @@ def test_backward_takes_the_rows_of_its_forward(calls):
     with pytest.raises(ValueError, match="7 rows"):
         ours.backward(bf16(6, N), OFFSETS)
     ours.backward(bf16(7, N), OFFSETS)
+
+
+@pytest.mark.parametrize("train", [True, False])
+def test_packed_weights_of_another_layout_are_refused(train, calls):
+    # the blob's extents come from E, N and K alone: a shorter one would be read past its end
+    ours = layer(train)
+    w_q, w_s = abi.alloc_grouped_blobs(E * N, K, E, equal=True, dual=False, device="cpu")
+    strided_q, strided_s = w_q.repeat(1, 2)[:, ::2], w_s.repeat(2)[::2]
+    for q, s in ((w_q[:-1], w_s), (w_q[:, :K // 2].contiguous(), w_s), (w_q, w_s[:-1]), (strided_q, w_s),
+                 (w_q, strided_s), (w_q.float(), w_s), (w_q, w_s.short()), (None, w_s), (w_q, None),
+                 (w_q.data_ptr(), w_s)):
+        with pytest.raises(ValueError, match="packed weights"):
+            ours.forward_packed(bf16(4, K), q, s, OFFSETS)
+    assert not calls
+    ours.forward_packed(bf16(4, K), w_q, w_s, OFFSETS)
+    ours.forward_packed(bf16(4, K), w_q.view(E, N, -1), w_s.view(torch.int8), OFFSETS)   # any view of the same bytes
