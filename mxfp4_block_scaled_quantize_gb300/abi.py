@@ -586,9 +586,12 @@ def quantize_grouped(x, offsets=None, row_index=None, groups=None, rows=None, du
     multiple of 8) that row_index (int32) gathers, or of X's own rows, in groups by the int32 CUDA
     `offsets` (groups + 1 of them), or in `groups` equal groups when offsets is None."""
     import torch
+    for t in (x, offsets, row_index):
+        if t is not None and not (t.is_cuda and t.device == x.device):
+            raise ValueError(f"a tensor on {t.device}: X, offsets and row_index are on one GPU")
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     for t in (offsets, row_index):
-        assert t is None or (t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.is_cuda)
+        assert t is None or (t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous())
     groups = groups if offsets is None else offsets.numel() - 1
     rows = rows if rows is not None else (x.shape[0] if row_index is None else row_index.numel())
     assert row_index is None or row_index.numel() >= rows

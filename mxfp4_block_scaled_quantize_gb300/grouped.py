@@ -35,6 +35,7 @@ class MXFP4GroupedLinear:
         code = abi.MXFP4_OUT_F32 if out_dtype == torch.float32 else abi.MXFP4_OUT_BF16
         self.x_blobs = abi.alloc_grouped_blobs(max_rows, K, groups, dual=train, device=device)
         self.y = torch.empty((max_rows, N), dtype=out_dtype, device=device)
+        self._gpu = self._here(self.y)
         self._packed_bytes = abi.mxfp4_grouped_sizes(groups * N, K, groups, equal=True)[:2]
         self.w_blobs = None
         self._has_w = False   # w_blobs hold the blobs of some W
@@ -51,21 +52,33 @@ class MXFP4GroupedLinear:
             self._c.dy_blobs[:] = _addresses(self.dy_blobs)
             self._c.dx, self._c.dw = self.dx.data_ptr(), self.dw.data_ptr()
 
+    @staticmethod
+    def _here(t):
+        """Index of t's GPU; None elsewhere, which no tensor's get_device() is."""
+        return t.get_device() if t.is_cuda else None
+
+    def _check_gpu(self, *tensors):
+        for t in tensors:
+            if t.get_device() != self._gpu:
+                raise ValueError(f"a tensor on {t.device}: the layer's tensors are on its GPU")
+
     def _check_rows(self, R, offsets):
+        self._check_gpu(offsets)
         if R > self.max_rows:
             raise ValueError(f"{R} rows for a layer of at most {self.max_rows}")
         if offsets.dtype != torch.int32 or offsets.numel() != self.groups + 1 or not offsets.is_contiguous():
             raise ValueError(f"offsets: {self.groups + 1} contiguous int32 values")
 
-    @staticmethod
-    def _pitch(x, k):
+    def _pitch(self, x, k):
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.size(1) != k or x.stride(1) != 1:
             raise ValueError(f"bf16 rows of {k} contiguous elements")
+        self._check_gpu(x)
         return x.stride(0)
 
     def _check_w(self, w):
         if w.dtype != torch.bfloat16 or w.shape != (self.groups, self.N, self.K) or not w.is_contiguous():
             raise ValueError(f"W: contiguous bf16 [{self.groups}, {self.N}, {self.K}]")
+        self._check_gpu(w)
         if self.w_blobs is None:
             self.w_blobs = abi.alloc_grouped_blobs(self.groups * self.N, self.K, self.groups, equal=True, dual=False,
                                                    device=w.device)
@@ -75,6 +88,7 @@ class MXFP4GroupedLinear:
         for t, n in zip((w_q, w_s), self._packed_bytes):
             if not isinstance(t, torch.Tensor) or t.element_size() != 1 or t.numel() < n or not t.is_contiguous():
                 raise ValueError("packed weights: contiguous bytes, {} of codes and {} of scales".format(*self._packed_bytes))
+        self._check_gpu(w_q, w_s)
 
     def quantize_w(self, w, stream=None):
         """The blobs of W[E, N, K], kept for the products that follow."""
@@ -92,6 +106,7 @@ class MXFP4GroupedLinear:
             R = rows.numel()
             if rows.dtype != torch.int32 or not rows.is_contiguous():
                 raise ValueError("rows: contiguous int32 values")
+            self._check_gpu(rows)
         self._check_rows(R, offsets)
         abi.mxfp4_grouped_forward(self._c, x, x.size(0), ldx, rows, offsets, R, w, stream)
         self._rows = R

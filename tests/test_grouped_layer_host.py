@@ -16,8 +16,9 @@ def _lib():
 
 @pytest.fixture
 def calls(monkeypatch):
-    """The library's calls, noted instead of made."""
+    """The library's calls, noted instead of made; the host stands in for the layer's GPU."""
     made = []
+    monkeypatch.setattr(MXFP4GroupedLinear, "_here", staticmethod(lambda t: t.get_device()))
     for name in ("mxfp4_quantize_grouped", "mxfp4_grouped_forward", "mxfp4_grouped_backward"):
         monkeypatch.setattr(abi, name, lambda *a, _name=name, **k: made.append((_name, a)))
     return made
@@ -91,3 +92,52 @@ def test_packed_weights_of_another_layout_are_refused(train, calls):
     assert not calls
     ours.forward_packed(bf16(4, K), w_q, w_s, OFFSETS)
     ours.forward_packed(bf16(4, K), w_q.view(E, N, -1), w_s.view(torch.int8), OFFSETS)   # any view of the same bytes
+
+
+def test_tensors_elsewhere_are_refused():
+    # a host address would be dereferenced on the GPU
+    for ours in (layer(True), layer(False)):
+        w_q, w_s = abi.alloc_grouped_blobs(E * N, K, E, equal=True, dual=False, device="cpu")
+        with pytest.raises(ValueError, match="GPU"):
+            ours.quantize_w(bf16(E, N, K))
+        with pytest.raises(ValueError, match="GPU"):
+            ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)
+        with pytest.raises(ValueError, match="GPU"):
+            ours.forward_packed(bf16(4, K), w_q, w_s, OFFSETS)
+
+
+@pytest.mark.parametrize("which", ["x", "w", "offsets", "rows", "dy", "backward's offsets", "w_q", "w_s"])
+def test_each_tensor_is_on_the_layers_device(which, calls):
+    class OnAnotherGpu(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    ours = layer()
+    t = {"x": bf16(4, K), "w": bf16(E, N, K), "offsets": OFFSETS, "rows": torch.zeros(4, dtype=torch.int32),
+         "dy": bf16(4, N), "backward's offsets": OFFSETS}
+    t["w_q"], t["w_s"] = abi.alloc_grouped_blobs(E * N, K, E, equal=True, dual=False, device="cpu")
+    ok = dict(t)
+    t[which] = t[which].as_subclass(OnAnotherGpu)
+    if which in ("dy", "backward's offsets"):
+        ours.forward(ok["x"], ok["w"], ok["offsets"], ok["rows"])
+        call = lambda t: ours.backward(t["dy"], t["backward's offsets"])
+    elif which in ("w_q", "w_s"):
+        call = lambda t: ours.forward_packed(t["x"], t["w_q"], t["w_s"], t["offsets"], t["rows"])
+    else:
+        call = lambda t: ours.forward(t["x"], t["w"], t["offsets"], t["rows"])
+    made = len(calls)
+    with pytest.raises(ValueError, match="GPU"):
+        call(t)
+    assert len(calls) == made
+    call(ok)
+    if which == "w":
+        with pytest.raises(ValueError, match="GPU"):
+            ours.quantize_w(t["w"])
+
+
+def test_grouped_quantizer_takes_gpu_tensors_only(calls):
+    x = bf16(4, K)
+    for args in ((x, OFFSETS), (x, None, None, 2)):
+        with pytest.raises(ValueError, match="GPU"):
+            abi.quantize_grouped(*args)
+    assert not calls
