@@ -40,7 +40,7 @@ class MXFP4GroupedLinear:
         self.w_blobs = None
         self._has_w = False   # w_blobs hold the blobs of some W
         self._packed = False  # the last forward took its weights from elsewhere
-        self._rows = None     # its rows
+        self._rows = None     # its rows; None: no backward can follow
         self._c = abi.GroupedLinear(groups, N, K, out_dtype=code, y=self.y.data_ptr())
         self._c.x_blobs[:] = _addresses(self.x_blobs)
         if train:
@@ -91,12 +91,13 @@ class MXFP4GroupedLinear:
         self._check_gpu(w_q, w_s)
 
     def quantize_w(self, w, stream=None):
-        """The blobs of W[E, N, K], kept for the products that follow."""
+        """The blobs of W[E, N, K], kept for the products that follow (a forward and its backward use
+        the same)."""
         self._check_w(w)
         blobs = self.w_blobs if self.train else self.w_blobs + (None, None)
         abi.mxfp4_quantize_grouped(w, self.groups * self.N, self.K, self.K, None, None, self.groups,
                                    self.groups * self.N, *blobs, stream)
-        self._has_w = True
+        self._has_w, self._rows = True, None
 
     def _forward(self, x, w, offsets, rows, stream):
         ldx = self._pitch(x, self.K)

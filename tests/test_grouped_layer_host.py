@@ -141,3 +141,14 @@ def test_grouped_quantizer_takes_gpu_tensors_only(calls):
         with pytest.raises(ValueError, match="GPU"):
             abi.quantize_grouped(*args)
     assert not calls
+
+
+def test_weights_quantized_after_the_forward_are_not_its_weights(calls):
+    # they replace the blobs that the forward used, so dX would be another W's
+    ours = layer()
+    ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)
+    ours.quantize_w(bf16(E, N, K))
+    with pytest.raises(ValueError, match="no forward"):
+        ours.backward(bf16(4, N), OFFSETS)
+    ours.forward(bf16(4, K), None, OFFSETS)
+    ours.backward(bf16(4, N), OFFSETS)
