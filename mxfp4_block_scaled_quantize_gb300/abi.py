@@ -581,6 +581,11 @@ def alloc_grouped_blobs(rows: int, k: int, groups: int, equal: bool = False, dua
     return row + (buf(k, cap // 2), buf(sc)) if dual else row
 
 
+def row_pitch(x) -> int:
+    """Elements from one row of X to the next; one row alone, whose stride says nothing: its length, rounded up to 8."""
+    return x.stride(0) if x.size(0) > 1 else (x.size(1) + 7) // 8 * 8
+
+
 def quantize_grouped(x, offsets=None, row_index=None, groups=None, rows=None, dual: bool = True, stream=None):
     """Grouped blobs (row_q, row_s[, col_q, col_s]) of the rows of bf16 X[T, K] (CUDA, row pitch a
     multiple of 8) that row_index (int32) gathers, or of X's own rows, in groups by the int32 CUDA
@@ -596,7 +601,7 @@ def quantize_grouped(x, offsets=None, row_index=None, groups=None, rows=None, du
     rows = rows if rows is not None else (x.shape[0] if row_index is None else row_index.numel())
     assert row_index is None or row_index.numel() >= rows
     blobs = alloc_grouped_blobs(rows, x.shape[1], groups, offsets is None, dual, x.device)
-    mxfp4_quantize_grouped(x, x.shape[0], x.shape[1], x.stride(0), row_index, offsets, groups, rows,
+    mxfp4_quantize_grouped(x, x.shape[0], x.shape[1], row_pitch(x), row_index, offsets, groups, rows,
                            *(blobs if dual else blobs + (None, None)), stream)
     return blobs
 

@@ -73,7 +73,7 @@ class MXFP4GroupedLinear:
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.size(1) != k or x.stride(1) != 1:
             raise ValueError(f"bf16 rows of {k} contiguous elements")
         self._check_gpu(x)
-        return x.stride(0)
+        return abi.row_pitch(x)
 
     def _check_w(self, w):
         if w.dtype != torch.bfloat16 or w.shape != (self.groups, self.N, self.K) or not w.is_contiguous():

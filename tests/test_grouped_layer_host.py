@@ -152,3 +152,25 @@ def test_weights_quantized_after_the_forward_are_not_its_weights(calls):
         ours.backward(bf16(4, N), OFFSETS)
     ours.forward(bf16(4, K), None, OFFSETS)
     ours.backward(bf16(4, N), OFFSETS)
+
+
+def test_one_row_has_no_pitch(calls):
+    # the stride of an axis of one element means nothing: a column turned round is one whole row
+    ours = layer()
+    row = bf16(K, 1).t()
+    assert row.stride() == (1, 1) and row.is_contiguous()
+    ours.forward(row, bf16(E, N, K), OFFSETS)
+    ours.backward(bf16(N, 1).t(), OFFSETS)
+    for name, args in calls:
+        ld, k = {"mxfp4_grouped_forward": (args[3], K), "mxfp4_grouped_backward": (args[2], N)}[name]
+        assert ld >= k and ld % 8 == 0
+
+
+def test_one_row_has_no_pitch_in_the_quantizer(calls, monkeypatch):
+    class Row(torch.Tensor):
+        is_cuda = True
+
+    monkeypatch.setattr(abi, "alloc_grouped_blobs", lambda *a: (None,) * 4)
+    abi.quantize_grouped(bf16(20, 1).t().as_subclass(Row), None, None, 1)
+    (_, args), = calls
+    assert args[3] >= 20 and args[3] % 8 == 0
