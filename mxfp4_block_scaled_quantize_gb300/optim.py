@@ -39,6 +39,7 @@ class AdamW:
         self.state_bits = 32 if isinstance(self.exp_avg[0], torch.Tensor) else 8
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.steps = 0
+        self._gpu = self.params[0].get_device() if self.params[0].is_cuda else None   # no tensor's get_device() is None
         self._numel = [p.numel() for p in self.params]
         self._table = np.zeros(len(self.params), dtype=_TABLE)
         self._grads = self._table["g"]   # views and addresses that every step uses
@@ -83,12 +84,14 @@ class AdamW:
         dtype = grads[0].dtype
         if dtype not in (torch.float32, torch.bfloat16) or len(grads) != len(self.params):
             raise ValueError("one fp32 or bf16 gradient for each parameter")
+        gpu = self._gpu
         addresses = [g.data_ptr() for g, n in zip(grads, self._numel)
-                     if g.dtype is dtype and g.numel() == n and g.is_contiguous()]
+                     if g.dtype is dtype and g.numel() == n and g.is_contiguous() and g.get_device() == gpu]
         if len(addresses) != len(self.params):
-            raise ValueError("gradients: contiguous, of one type and the parameters' sizes")
-        if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != 4 or not dynamic.is_cuda):
-            raise ValueError("dynamic: four fp32 on the device")
+            raise ValueError("gradients: contiguous, of one type and the parameters' sizes, on the parameters' GPU")
+        if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != 4 or
+                                    not dynamic.is_contiguous() or dynamic.get_device() != gpu):
+            raise ValueError("dynamic: four consecutive fp32 on the parameters' GPU")
         self.steps = self.steps + 1 if step is None else step
         self._grads[:] = addresses
         flags = (abi.MXFP4_ADAMW_P_F32 if self.dtype == torch.float32 else 0) | \

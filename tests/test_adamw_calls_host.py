@@ -1,0 +1,66 @@
+"""What the optimizer hands to the library, and what it refuses first, without a GPU."""
+import pytest
+import torch
+
+from mxfp4_block_scaled_quantize_gb300 import abi, optim
+
+SIZES = (10, 20)
+
+
+class OnTheGpu(torch.Tensor):
+    """Stands for a tensor on GPU 0: its memory is the host's, and nothing reads it there."""
+    gpu = 0
+
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.gpu
+
+
+class OnAnotherGpu(OnTheGpu):
+    gpu = 1
+
+
+def tensors(kind=OnTheGpu, dtype=torch.float32):
+    return [torch.zeros(n, dtype=dtype).as_subclass(kind) for n in SIZES]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls, noted instead of made."""
+    made = []
+    monkeypatch.setattr(abi, "mxfp4_adamw", lambda *a, **k: made.append(a))
+    return made
+
+
+def test_gradients_elsewhere_are_refused(calls):
+    # a host address would be dereferenced on the GPU
+    opt = optim.AdamW(tensors())
+    for bad in (torch.Tensor, OnAnotherGpu):
+        for j in (0, 1):
+            grads = tensors()
+            grads[j] = torch.zeros(SIZES[j]).as_subclass(bad)
+            with pytest.raises(ValueError, match="GPU"):
+                opt.step(grads)
+    assert not calls and opt.steps == 0
+    opt.step(tensors())
+    assert len(calls) == 1 and opt.steps == 1
+
+
+def test_parameters_on_the_host_are_refused(calls):
+    opt = optim.AdamW([torch.zeros(10)])
+    with pytest.raises(ValueError, match="GPU"):
+        opt.step([torch.zeros(10)])
+    assert not calls and opt.steps == 0
+
+
+def test_values_on_the_device_are_four_in_a_row(calls):
+    opt = optim.AdamW(tensors())
+    four = torch.zeros(4).as_subclass(OnTheGpu)
+    for bad in (torch.zeros(8).as_subclass(OnTheGpu)[::2], torch.zeros(4), four.double(), torch.zeros(5).as_subclass(OnTheGpu),
+                torch.zeros(4).as_subclass(OnAnotherGpu)):
+        with pytest.raises(ValueError, match="dynamic"):
+            opt.step(tensors(), dynamic=bad)
+    assert not calls and opt.steps == 0
+    opt.step(tensors(), dynamic=four)
+    assert calls[0][3].dynamic == four.data_ptr()
