@@ -92,11 +92,13 @@ class AdamW:
         if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != 4 or
                                     not dynamic.is_contiguous() or dynamic.get_device() != gpu):
             raise ValueError("dynamic: four consecutive fp32 on the parameters' GPU")
-        self.steps = self.steps + 1 if step is None else step
+        if step is None:
+            step = self.steps + 1
         self._grads[:] = addresses
         flags = (abi.MXFP4_ADAMW_P_F32 if self.dtype == torch.float32 else 0) | \
                 (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0) | \
                 (abi.MXFP4_ADAMW_STATE_E4M3 if self.state_bits == 8 else 0)
         h = abi.AdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                            grad_scale, self.steps, None if dynamic is None else dynamic.data_ptr())
+                            grad_scale, step, None if dynamic is None else dynamic.data_ptr())
         abi.mxfp4_adamw(len(self.params), self._address, flags, h, stream)
+        self.steps = step

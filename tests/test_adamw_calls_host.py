@@ -64,3 +64,22 @@ def test_values_on_the_device_are_four_in_a_row(calls):
     assert not calls and opt.steps == 0
     opt.step(tensors(), dynamic=four)
     assert calls[0][3].dynamic == four.data_ptr()
+
+
+def test_a_refused_step_does_not_count(calls, monkeypatch):
+    opt = optim.AdamW(tensors())
+    opt.step(tensors())
+
+    def refuse(*args):
+        raise abi.Mxfp4Error(abi.MXFP4_ERR_INVALID_ARG, "mxfp4_adamw")
+
+    with monkeypatch.context() as m:
+        m.setattr(abi, "mxfp4_adamw", refuse)
+        for step in (None, 7):
+            with pytest.raises(abi.Mxfp4Error):
+                opt.step(tensors(), step=step, lr=float("nan"))
+            assert opt.steps == 1
+    opt.step(tensors())
+    assert opt.steps == 2 and calls[-1][3].step == 2
+    opt.step(tensors(), step=7)
+    assert opt.steps == 7 and calls[-1][3].step == 7
