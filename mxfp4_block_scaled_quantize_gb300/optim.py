@@ -32,6 +32,8 @@ class AdamW:
             raise ValueError("fp32 parameters need no masters")
         if state_bits not in (8, 32):
             raise ValueError("state_bits: 32 or 8")
+        if (exp_avg is None) != (exp_avg_sq is None):
+            raise ValueError("exp_avg and exp_avg_sq: both, or neither")
         if exp_avg is None:
             exp_avg = [self._zeros(p, state_bits) for p in self.params]
             exp_avg_sq = [self._zeros(p, state_bits) for p in self.params]
@@ -68,6 +70,9 @@ class AdamW:
         if self.masters is not None:
             put("master", self.masters, torch.float32, self._numel)
         for name, moments in (("m", self.exp_avg), ("v", self.exp_avg_sq)):
+            for x in moments:
+                if isinstance(x, torch.Tensor) != (self.state_bits == 32) or (self.state_bits == 8 and len(x) != 2):
+                    raise ValueError("moments: all fp32 tensors, or all pairs of E4M3 codes and scales")
             if self.state_bits == 32:
                 put(name, moments, torch.float32, self._numel)
             else:

@@ -83,3 +83,16 @@ def test_a_refused_step_does_not_count(calls, monkeypatch):
     assert opt.steps == 2 and calls[-1][3].step == 2
     opt.step(tensors(), step=7)
     assert opt.steps == 7 and calls[-1][3].step == 7
+
+
+def test_moments_come_both_or_not_at_all():
+    p = tensors()
+    m32 = tensors()
+    m8 = [(torch.zeros(n, dtype=torch.float8_e4m3fn).as_subclass(OnTheGpu), torch.zeros(1).as_subclass(OnTheGpu))
+          for n in SIZES]
+    for m, v in ((m32, None), (None, m32), (m8, None), (m32, m8), (m8, m32), ([m32[0], m8[1]], m32), (m8, [m8[0], m32[1]]),
+                 (m8, [m8[0], m8[1] + m8[1]])):
+        with pytest.raises(ValueError):
+            optim.AdamW(p, exp_avg=m, exp_avg_sq=v)
+    assert optim.AdamW(p, exp_avg=m32, exp_avg_sq=m32).state_bits == 32
+    assert optim.AdamW(p, exp_avg=m8, exp_avg_sq=m8).state_bits == 8
