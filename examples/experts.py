@@ -54,8 +54,8 @@ def train(tokens=1024, experts=8, n=512, k=512, top_k=2, steps=60, lr=2e-3, seed
     master = torch.randn(experts, n, k, device="cuda", generator=g) * (0.1 / k ** 0.5)
     weight = master.to(torch.bfloat16)
     layer = MXFP4GroupedLinear(experts, n, k, tokens * top_k)
-    optimizer = AdamW([weight], masters=[master], state_bits=8, lr=lr, weight_decay=0.0)
-    dynamic = torch.empty(4, device="cuda")
+    optimizer = AdamW([weight], masters=[master], state_bits=8, lr=lr, weight_decay=0.0, seed=seed)
+    dynamic = torch.empty(5, device="cuda")
     gate_rows = torch.empty(tokens * top_k, 1, device="cuda")
     gate_rows[places.reshape(-1)] = gates.reshape(-1, 1)
 
@@ -69,7 +69,7 @@ def train(tokens=1024, experts=8, n=512, k=512, top_k=2, steps=60, lr=2e-3, seed
 
     def hyperparameters(t):
         b1, b2 = optimizer.betas
-        dynamic.copy_(torch.tensor([lr, 1 - b1 ** t, 1 - b2 ** t, 1.0]))
+        dynamic.copy_(torch.tensor([lr, 1 - b1 ** t, 1 - b2 ** t, 1.0, t]))
 
     hyperparameters(1)
     side = torch.cuda.Stream()

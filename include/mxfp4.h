@@ -509,10 +509,22 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const voi
  * magnitude of the block, and E4M3 codes of the elements over the scale, to nearest even; the
  * first moment itself, and the square root of the second, where a value above zero never
  * encodes to zero (it takes at least the code of 2^-9).  A value that is not finite encodes to
- * NaN.  All-zero codes with any finite scale are zero moments. */
+ * NaN.  All-zero codes with any finite scale are zero moments.
+ * A code rounded to nearest does not move while a step moves its value by less than half a code
+ * step (1/32 to 1/18 of it) relative to its block's largest, and sqrt(v) decays by 1 - sqrt(beta2)
+ * a step: elements whose gradients shrink beside larger ones follow at once for beta2 < 0.89, only
+ * with their block's largest at 0.95, and not at all at 0.999.  beta2 > 0.95 is therefore refused
+ * with codes to nearest, and wants MXFP4_ADAMW_STOCHASTIC: every code of either moment is the
+ * lower or the upper E4M3 neighbour of the element over the scale, the upper one with the
+ * probability of the element's place between them (to 2^-16), so that the moments follow their
+ * recurrences in expectation for every beta.  The random bits are those of Philox4x32-10 with
+ * `seed` as its key and the counter (i / 8, tensor, step, i / 2^35 + 2^31 for the second moment)
+ * for element i: 16 bits each, half i % 2 (0: low) of word (i / 2) % 4, where `tensor` counts
+ * the call's tensors that have elements.  Same seed, step and tensors: same codes. */
 #define MXFP4_ADAMW_P_F32 1          /* parameters fp32 (else bf16)                            */
 #define MXFP4_ADAMW_G_F32 2          /* gradients fp32 (else bf16)                             */
 #define MXFP4_ADAMW_STATE_E4M3 4     /* moments in 8 bits (else fp32)                          */
+#define MXFP4_ADAMW_STOCHASTIC 8     /* 8-bit moments rounded stochastically (with STATE_E4M3)  */
 #define MXFP4_ADAMW_BLOCK 128
 
 /* One tensor of n elements (n == 0: skipped), dense, every buffer aligned to its element; all
@@ -532,7 +544,8 @@ typedef struct {
 
 /* beta1, beta2 in [0, 1), eps 0 or a normal fp32 above it, step >= 1 (the number of this step).  dynamic: NULL, or
  * four fp32 in device memory read instead of the host's values, so that a captured graph can
- * go on: lr, 1 - beta1^step, 1 - beta2^step, grad_scale. */
+ * go on: lr, 1 - beta1^step, 1 - beta2^step, grad_scale; with MXFP4_ADAMW_STOCHASTIC five, the
+ * fifth the step's number (exact up to 2^24).  seed: read with MXFP4_ADAMW_STOCHASTIC only. */
 typedef struct {
     double lr;
     double beta1;
@@ -542,6 +555,7 @@ typedef struct {
     double grad_scale;
     int64_t step;
     const float* dynamic;
+    uint64_t seed;
 } mxfp4_adamw_params;
 
 mxfp4_status mxfp4_adamw(int32_t count, const mxfp4_adamw_tensor* tensors, int32_t flags,

@@ -41,6 +41,7 @@ MXFP4_GROUPED_WGRAD = 2
 MXFP4_ADAMW_P_F32 = 1
 MXFP4_ADAMW_G_F32 = 2
 MXFP4_ADAMW_STATE_E4M3 = 4
+MXFP4_ADAMW_STOCHASTIC = 8
 MXFP4_ADAMW_BLOCK = 128
 
 
@@ -94,7 +95,7 @@ class AdamwTensor(ctypes.Structure):
 class AdamwParams(ctypes.Structure):
     """mxfp4_adamw_params of include/mxfp4.h."""
     _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + \
-        [("step", ctypes.c_int64), ("dynamic", ctypes.c_void_p)]
+        [("step", ctypes.c_int64), ("dynamic", ctypes.c_void_p), ("seed", ctypes.c_uint64)]
 
 
 class LinearHostTask(ctypes.Structure):

@@ -14,6 +14,18 @@
 // (it takes the smallest code): m / sqrt(v) of a small element beside a large one would otherwise
 // divide by eps.  An element that is not finite becomes NaN and leaves its block's scale alone.
 //
+// Rounding of the codes.  To nearest, a code stays where it is as long as a step moves its value
+// by less than half a code step, 1/32 to 1/18 of it, relative to its block's largest.  A step
+// without gradient takes r to sqrt(beta2) r, which is that far only for beta2 below 0.89: at
+// 0.95 a block's small elements follow once their largest moves by itself, and at 0.999 they do
+// not follow (gradients 100 times smaller in half of each block left v 7400 times too large
+// after 12 000 steps).  So to nearest is for beta2 <= 0.95, and beyond that codes are rounded
+// stochastically: to a value's upper neighbour with the probability of its place between the
+// two, which makes the expected code the value and each moment's expectation that of its
+// recurrence.  What that costs is noise (a pure decay by a factor e has gone through roundings of
+// a relative variance of 1/8 at most) and two Philox calls for 8 elements: 280 M elements take
+// 934 us, bound by arithmetic, and 695 to nearest; 140 M with fp32 gradients 476 and 405.
+//
 // Bound by memory: bf16 parameters with masters and bf16 gradients move 28 bytes an element with
 // fp32 moments and 16.1 with 8-bit ones.  A thread takes 8 consecutive elements, all of whose
 // loads are in flight together; 16 lanes hold a block, so its maxima are four shuffles.  The
@@ -26,6 +38,7 @@
 
 #include "launch.h"
 #include "launch_adamw.h"
+#include "philox.cuh"
 #include "ptx.cuh"
 
 namespace mxfp4 {
@@ -40,6 +53,7 @@ constexpr int kThreads32 = 128;   // fp32 moments
 constexpr int kThreads8 = 32;     // 8-bit moments
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;   // 2^-126
+constexpr double kNearestBeta2 = 0.95;         // largest beta2 with codes to nearest
 constexpr float kMinCode = 0.001953125f;       // 2^-9, the smallest E4M3 value above zero
 
 __device__ __forceinline__ void unpack_bf16(const uint4& u, float* f) {
@@ -156,14 +170,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
     return d;
 }
 
+// Stochastic rounding onto E4M3's magnitudes (steps of g = 2^(e - 3) in [2^e, 2^(e + 1)), 2^-9
+// below 2^-6): a = |y| <= 448 (1 + 2^-22), x: a value with y's sign, r: 16 random bits.  Gives the
+// lower neighbour lo unless (a - lo) / g >= (r + 1/2) / 2^16, so that the chance of the upper one
+// is its share rounded to 2^-16, not cut off.  As in the MXFP4 quantizer: a + noise, noise =
+// g (1 + (65535.5 - r) / 2^16) from bits, rounded toward zero, then onto the multiples of g by
+// adding g 2^23 toward zero, and both offsets taken off again.
+__device__ __forceinline__ float sr_e4m3(float a, float x, uint32_t r) {
+    const uint32_t gbits = (max(__float_as_uint(a) >> 23, 121u) - 3u) << 23;
+    const float noise = __uint_as_float(gbits | ((r ^ 0xFFFFu) << 7) | 0x40u);
+    const uint32_t cbits = gbits + (23u << 23);
+    const float s = __fadd_rz(__fadd_rz(a, noise), __uint_as_float(cbits));
+    const float q = __fsub_rn(s, __uint_as_float(cbits + 1u));   // - (g 2^23 + g)
+    return __uint_as_float(__float_as_uint(q) | (__float_as_uint(x) & 0x80000000u));
+}
+
 // This lane's block (16 lanes) of x: its scale, and the eight codes.  kRoot: values >= 0, of
-// which those above zero stay there.  The quotients x / scale are those of IEEE division, by
+// which those above zero stay there.  kSr: stochastically, by `bits`, of which element k takes half
+// k % 2 of word k / 2.  The quotients x / scale are those of IEEE division, by
 // Markstein's theorem (IBM J. Res. Dev. 34, 1990): from the correctly rounded reciprocal y,
 // q = x y and the exact residual x - q scale give the correctly rounded quotient as
 // q + residual y.  Three operations an element in place of a division; a code is the nearest to
 // the rounded quotient in either case.
-template <bool kRoot>
-__device__ __forceinline__ uint2 encode_block(const float* x, float* scale) {
+template <bool kRoot, bool kSr>
+__device__ __forceinline__ uint2 encode_block(const float* x, float* scale, uint4 bits) {
     const float inf = __int_as_float(0x7F800000);
     float top = 0.0f;
 #pragma unroll
@@ -182,11 +212,13 @@ __device__ __forceinline__ uint2 encode_block(const float* x, float* scale) {
     const float s = fmaxf(__fmul_rn(top, 1.0f / kE4m3Max), kMinScale);
     const float inv = __frcp_rn(s);
     *scale = s;
+    const uint32_t rnd[4] = {bits.x, bits.y, bits.z, bits.w};
     float y[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float q = __fmul_rn(x[k], inv);
         y[k] = __fmaf_rn(__fmaf_rn(-q, s, x[k]), inv, q);
+        if (kSr) y[k] = sr_e4m3(fabsf(y[k]), x[k], k & 1 ? rnd[k >> 1] >> 16 : rnd[k >> 1] & 0xFFFFu);
         if (kRoot) y[k] = x[k] > 0.0f ? fmaxf(y[k], kMinCode) : 0.0f;
     }
     if (odd) {
@@ -225,10 +257,12 @@ __device__ __forceinline__ void sqrt8(const float* v, float* r) {
 
 struct Hyper {
     float beta1, one_beta1, beta2, one_beta2, eps, step_c1, inv_root_c2, decay, grad_scale;
+    uint32_t tensor, step;   // of the random bits' counter
+    uint64_t seed;
 };
 
 // Eight elements of t at i.  kWhole: all eight exist and every access is aligned.
-template <bool kPF32, bool kGF32, bool kState8, bool kWhole>
+template <bool kPF32, bool kGF32, bool kState8, bool kSr, bool kWhole>
 __device__ __forceinline__ void update8(const mxfp4_adamw_tensor& t, const Hyper& h, int64_t i, int64_t n, bool aligned) {
     // past the end a lane still takes part in its block's maximum, with zeros
     const bool wide = kWhole || (aligned && i + 8 <= n);
@@ -274,7 +308,14 @@ __device__ __forceinline__ void update8(const mxfp4_adamw_tensor& t, const Hyper
     store8<kPF32>(t.p, i, n, wide, p);
     if (kState8) {
         float ms, vs;
-        const uint2 mq = encode_block<false>(m, &ms), vq = encode_block<true>(r, &vs);
+        // 8 x 16 bits for each moment: counter (i / 8, tensor, step, i / 2^35 and the moment in the top bit)
+        uint4 mb = make_uint4(0u, 0u, 0u, 0u), vb = mb;
+        if (kSr) {
+            const uint32_t lo = static_cast<uint32_t>(i >> 3), hi = static_cast<uint32_t>(i >> 35);
+            mb = philox4x32_10(lo, h.tensor, h.step, hi, h.seed);
+            vb = philox4x32_10(lo, h.tensor, h.step, hi | 0x80000000u, h.seed);
+        }
+        const uint2 mq = encode_block<false, kSr>(m, &ms, mb), vq = encode_block<true, kSr>(r, &vs, vb);
         store_codes(t.m, i, n, wide, mq);
         store_codes(t.v, i, n, wide, vq);
         if ((threadIdx.x & 15) == 0 && (kWhole || i < n)) {
@@ -287,7 +328,7 @@ __device__ __forceinline__ void update8(const mxfp4_adamw_tensor& t, const Hyper
     }
 }
 
-template <bool kPF32, bool kGF32, bool kState8, int kCap>
+template <bool kPF32, bool kGF32, bool kState8, bool kSr, int kCap>
 __global__ void __launch_bounds__(kState8 ? kThreads8 : kThreads32, kState8 ? 32 : 8) adamw_kernel(const __grid_constant__ AdamwArgs<kCap> a) {
     grid_wait_prerequisites();
     grid_launch_dependents();
@@ -305,7 +346,12 @@ __global__ void __launch_bounds__(kState8 ? kThreads8 : kThreads32, kState8 ? 32
     const float lr = dyn ? __ldg(a.dynamic) : a.lr;
     const float c1 = dyn ? __ldg(a.dynamic + 1) : a.c1, c2 = dyn ? __ldg(a.dynamic + 2) : a.c2;
     Hyper h{a.beta1, a.one_beta1, a.beta2, a.one_beta2, a.eps, lr / c1, 1.0f / sqrtf(c2), lr * a.weight_decay,
-            dyn ? __ldg(a.dynamic + 3) : a.grad_scale};
+            dyn ? __ldg(a.dynamic + 3) : a.grad_scale, 0u, 0u, 0u};
+    if (kSr) {
+        h.tensor = static_cast<uint32_t>(a.first + lo);
+        h.step = dyn ? static_cast<uint32_t>(__ldg(a.dynamic + 4)) : a.step;
+        h.seed = a.seed;
+    }
     // every pointer where an 8-element access may start: 16 bytes apart (codes: 8)
     const uintptr_t all = reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
                           reinterpret_cast<uintptr_t>(t.master) |
@@ -316,21 +362,24 @@ __global__ void __launch_bounds__(kState8 ? kThreads8 : kThreads32, kState8 ? 32
     constexpr int kPass = 8 * (kState8 ? kThreads8 : kThreads32);
     if (aligned && base + kAdamwUnit <= n) {
 #pragma unroll 1
-        for (int k = 0; k < kAdamwUnit; k += kPass) update8<kPF32, kGF32, kState8, true>(t, h, i0 + k, n, true);
+        for (int k = 0; k < kAdamwUnit; k += kPass) update8<kPF32, kGF32, kState8, kSr, true>(t, h, i0 + k, n, true);
     } else {
 #pragma unroll 1
-        for (int k = 0; k < kAdamwUnit; k += kPass) update8<kPF32, kGF32, kState8, false>(t, h, i0 + k, n, aligned);
+        for (int k = 0; k < kAdamwUnit; k += kPass) update8<kPF32, kGF32, kState8, kSr, false>(t, h, i0 + k, n, aligned);
     }
 }
 
 template <int kCap>
 cudaError_t launch(const AdamwArgs<kCap>& a, int flags, cudaStream_t stream) {
     using K = void (*)(AdamwArgs<kCap>);
-    static const K kernels[8] = {
-        adamw_kernel<false, false, false, kCap>, adamw_kernel<true, false, false, kCap>,
-        adamw_kernel<false, true, false, kCap>,  adamw_kernel<true, true, false, kCap>,
-        adamw_kernel<false, false, true, kCap>,  adamw_kernel<true, false, true, kCap>,
-        adamw_kernel<false, true, true, kCap>,   adamw_kernel<true, true, true, kCap>};
+    static const K kernels[16] = {
+        adamw_kernel<false, false, false, false, kCap>, adamw_kernel<true, false, false, false, kCap>,
+        adamw_kernel<false, true, false, false, kCap>,  adamw_kernel<true, true, false, false, kCap>,
+        adamw_kernel<false, false, true, false, kCap>,  adamw_kernel<true, false, true, false, kCap>,
+        adamw_kernel<false, true, true, false, kCap>,   adamw_kernel<true, true, true, false, kCap>,
+        nullptr, nullptr, nullptr, nullptr,   // stochastic rounding is of 8-bit moments
+        adamw_kernel<false, false, true, true, kCap>,   adamw_kernel<true, false, true, true, kCap>,
+        adamw_kernel<false, true, true, true, kCap>,    adamw_kernel<true, true, true, true, kCap>};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -346,7 +395,8 @@ cudaError_t launch(const AdamwArgs<kCap>& a, int flags, cudaStream_t stream) {
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 mxfp4_status check(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, const mxfp4_adamw_params* h) {
-    if (count < 0 || (count > 0 && t == nullptr) || h == nullptr || (flags & ~7)) return MXFP4_ERR_INVALID_ARG;
+    if (count < 0 || (count > 0 && t == nullptr) || h == nullptr || (flags & ~15)) return MXFP4_ERR_INVALID_ARG;
+    if ((flags & MXFP4_ADAMW_STOCHASTIC) && !(flags & MXFP4_ADAMW_STATE_E4M3)) return MXFP4_ERR_INVALID_ARG;
     // the fp32 values that the kernel uses have to lie in the ranges too
     const float b1 = static_cast<float>(h->beta1), b2 = static_cast<float>(h->beta2), eps = static_cast<float>(h->eps);
     if (!(h->beta1 >= 0.0 && b1 < 1.0f) || !(h->beta2 >= 0.0 && b2 < 1.0f) || !(h->eps >= 0.0) || h->step < 1 ||
@@ -364,6 +414,8 @@ mxfp4_status check(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, co
             (s8 && (!aligned_to(x.m_scale, 4) || !aligned_to(x.v_scale, 4))))
             return MXFP4_ERR_MISALIGNED;
     }
+    // codes rounded to nearest do not follow a slower second moment (the head of this file)
+    if (s8 && !(flags & MXFP4_ADAMW_STOCHASTIC) && h->beta2 > kNearestBeta2) return MXFP4_ERR_INVALID_ARG;
     return MXFP4_OK;
 }
 
@@ -382,6 +434,9 @@ mxfp4_status step(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, con
     a.c2 = static_cast<float>(1.0 - std::pow(h.beta2, static_cast<double>(h.step)));
     a.grad_scale = static_cast<float>(h.grad_scale);
     a.dynamic = h.dynamic;
+    a.first = 0;
+    a.step = static_cast<uint32_t>(h.step);
+    a.seed = flags & MXFP4_ADAMW_STOCHASTIC ? h.seed : 0;
     int32_t j = 0;
     while (j < count) {
         int64_t units = 0;
@@ -398,6 +453,7 @@ mxfp4_status step(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, con
             a.end[a.count++] = static_cast<int32_t>(units);
         }
         if (a.count > 0 && launch<kCap>(a, flags, stream) != cudaSuccess) return MXFP4_ERR_CUDA;
+        a.first += a.count;
     }
     return MXFP4_OK;
 }

@@ -21,7 +21,10 @@ struct AdamwArgs {
     int32_t count;
     float beta1, one_beta1, beta2, one_beta2, eps, weight_decay;
     float lr, c1, c2, grad_scale;    // c = 1 - beta^step
-    const float* dynamic;            // or null: lr, c1, c2, grad_scale in device memory
+    const float* dynamic;            // or null: lr, c1, c2, grad_scale (stochastic: and the step) in device memory
+    int32_t first;                   // stochastic: tensors with elements before t[0] in the call,
+    uint32_t step;                   // the step's number
+    uint64_t seed;                   // and the key
 };
 
 }  // namespace mxfp4

@@ -52,6 +52,7 @@
 
 #include "launch.h"
 #include "mx_encode.cuh"
+#include "philox.cuh"
 #include "ptx.cuh"
 #include "quant_tile.cuh"
 
@@ -76,31 +77,11 @@ struct QuantSmem {
 constexpr uint32_t kBarConsumers = 1;          // named barrier of the consumer warps
 
 // ---- stochastic rounding of the elements (the gradient quantizer's `use_sr` flag) -------
-// Random bits: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011), key = the 64-bit seed,
+// Random bits: Philox4x32-10 (philox.cuh), key = the 64-bit seed,
 // counter = (b / 8, a, packing, 0) for blob row a, blob column b (packing 0: row blob of
 // X; 1: col blob, whose row a is column a of X); word (b / 2) % 4 of the result carries
 // the element's 16 bits, in its low half for even b.  One call serves 8 consecutive
 // elements of a blob row.
-__device__ __forceinline__ uint4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_t c2, uint64_t seed) {
-    uint32_t x0 = c0, x1 = c1, x2 = c2, x3 = 0u;
-    uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
-#pragma unroll
-    for (int round = 0; round < 10; ++round) {
-        uint64_t p0, p1;   // full 64-bit products, one wide multiply each
-        asm("mul.wide.u32 %0, %1, 0xD2511F53;" : "=l"(p0) : "r"(x0));
-        asm("mul.wide.u32 %0, %1, 0xCD9E8D57;" : "=l"(p1) : "r"(x2));
-        const uint32_t hi0 = static_cast<uint32_t>(p0 >> 32), lo0 = static_cast<uint32_t>(p0);
-        const uint32_t hi1 = static_cast<uint32_t>(p1 >> 32), lo1 = static_cast<uint32_t>(p1);
-        const uint32_t n0 = hi1 ^ x1 ^ k0, n2 = hi0 ^ x3 ^ k1;
-        x0 = n0;
-        x1 = lo1;
-        x2 = n2;
-        x3 = lo0;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    return make_uint4(x0, x1, x2, x3);
-}
 
 // Stochastic rounding of one element onto the E2M1 magnitudes {0, .5, 1, 1.5, 2, 3, 4, 6}:
 // a = |y| (y the scaled element, |y| < 8 for a finite block), x: a value with y's sign bit,

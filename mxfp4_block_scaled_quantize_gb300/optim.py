@@ -17,10 +17,16 @@ class AdamW:
     parameters (or None: the parameters themselves are updated).  Moments: `state_bits` 32 or 8
     allocates zeros; or exp_avg / exp_avg_sq give them, per tensor an fp32 tensor, or for 8 bits
     a pair (E4M3 codes, fp32 scale per 128 elements), exp_avg_sq then holding the square root of
-    the second moment.  All tensors are updated in place and must stay where they are."""
+    the second moment.  All tensors are updated in place and must stay where they are.
+
+    seed: 8-bit moments are rounded stochastically, with random bits that seed, step and place
+    decide, and follow their recurrences in expectation for every beta.  Without it they are
+    rounded to nearest, and an element whose gradients shrink keeps its second moment for as long
+    as a step moves it by less than half a code step relative to its block's largest; beta2 is
+    then 0.95 at most, and 0.95 by default (else 0.999)."""
 
     def __init__(self, params, masters=None, state_bits=32, exp_avg=None, exp_avg_sq=None, lr=1e-3,
-                 betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01):
+                 betas=None, eps=1e-8, weight_decay=0.01, seed=None):
         self.params = list(params)
         if not self.params:
             raise ValueError("no parameters")
@@ -39,7 +45,20 @@ class AdamW:
             exp_avg_sq = [self._zeros(p, state_bits) for p in self.params]
         self.exp_avg, self.exp_avg_sq = list(exp_avg), list(exp_avg_sq)
         self.state_bits = 32 if isinstance(self.exp_avg[0], torch.Tensor) else 8
+        if seed is not None and self.state_bits != 8:
+            raise ValueError("seed: for 8-bit moments")
+        to_nearest = self.state_bits == 8 and seed is None
+        if betas is None:
+            betas = (0.9, 0.95 if to_nearest else 0.999)
+        elif to_nearest and betas[1] > 0.95:
+            raise ValueError(f"8-bit moments rounded to nearest do not follow beta2 = {betas[1]}: give a seed, for "
+                             "stochastic rounding, or beta2 up to 0.95")
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.seed = 0 if seed is None else seed & (2 ** 64 - 1)
+        self._dynamic = 4 if seed is None else 5
+        self._flags = (abi.MXFP4_ADAMW_P_F32 if self.dtype == torch.float32 else 0) | \
+                      (abi.MXFP4_ADAMW_STATE_E4M3 if self.state_bits == 8 else 0) | \
+                      (abi.MXFP4_ADAMW_STOCHASTIC if seed is not None else 0)
         self.steps = 0
         self._gpu = self.params[0].get_device() if self.params[0].is_cuda else None   # no tensor's get_device() is None
         self._numel = [p.numel() for p in self.params]
@@ -85,7 +104,7 @@ class AdamW:
         """One update with the gradients (contiguous, all fp32 or all bf16, in the order of the
         parameters).  step: this step's number (default: counted from 1); grad_scale: a factor on
         every gradient; dynamic: a CUDA fp32 tensor [lr, 1 - beta1^step, 1 - beta2^step, grad_scale]
-        that takes their place, for steps captured in a graph."""
+        (with a seed, and step) that takes their place, for steps captured in a graph."""
         dtype = grads[0].dtype
         if dtype not in (torch.float32, torch.bfloat16) or len(grads) != len(self.params):
             raise ValueError("one fp32 or bf16 gradient for each parameter")
@@ -94,16 +113,14 @@ class AdamW:
                      if g.dtype is dtype and g.numel() == n and g.is_contiguous() and g.get_device() == gpu]
         if len(addresses) != len(self.params):
             raise ValueError("gradients: contiguous, of one type and the parameters' sizes, on the parameters' GPU")
-        if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != 4 or
+        if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != self._dynamic or
                                     not dynamic.is_contiguous() or dynamic.get_device() != gpu):
-            raise ValueError("dynamic: four consecutive fp32 on the parameters' GPU")
+            raise ValueError(f"dynamic: {self._dynamic} consecutive fp32 on the parameters' GPU")
         if step is None:
             step = self.steps + 1
         self._grads[:] = addresses
-        flags = (abi.MXFP4_ADAMW_P_F32 if self.dtype == torch.float32 else 0) | \
-                (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0) | \
-                (abi.MXFP4_ADAMW_STATE_E4M3 if self.state_bits == 8 else 0)
+        flags = self._flags | (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0)
         h = abi.AdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                            grad_scale, step, None if dynamic is None else dynamic.data_ptr())
+                            grad_scale, step, None if dynamic is None else dynamic.data_ptr(), self.seed)
         abi.mxfp4_adamw(len(self.params), self._address, flags, h, stream)
         self.steps = step
