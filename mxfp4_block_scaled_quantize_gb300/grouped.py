@@ -39,16 +39,16 @@ class MXFP4GroupedLinear:
         self._packed_bytes = abi.mxfp4_grouped_sizes(groups * N, K, groups, equal=True)[:2]
         self.w_blobs = None
         self._has_w = False   # w_blobs hold the blobs of some W
-        self._packed = False  # the last forward took its weights from elsewhere
+        self._away = False    # the products' weights are not w_blobs
+        self._packed = False  # nor were they the last forward's
         self._rows = None     # its rows; None: no backward can follow
         self._c = abi.GroupedLinear(groups, N, K, out_dtype=code, y=self.y.data_ptr())
         self._c.x_blobs[:] = _addresses(self.x_blobs)
         if train:
-            self.w_blobs = abi.alloc_grouped_blobs(groups * N, K, groups, equal=True, device=device)
+            self._keep_w(abi.alloc_grouped_blobs(groups * N, K, groups, equal=True, device=device))
             self.dy_blobs = abi.alloc_grouped_blobs(max_rows, N, groups, device=device)
             self.dx = torch.empty((max_rows, K), dtype=out_dtype, device=device)
             self.dw = torch.empty((groups, N, K), dtype=out_dtype, device=device)
-            self._c.w_blobs[:] = _addresses(self.w_blobs)
             self._c.dy_blobs[:] = _addresses(self.dy_blobs)
             self._c.dx, self._c.dw = self.dx.data_ptr(), self.dw.data_ptr()
 
@@ -57,38 +57,57 @@ class MXFP4GroupedLinear:
         """Index of t's GPU; None elsewhere, which no tensor's get_device() is."""
         return t.get_device() if t.is_cuda else None
 
-    def _check_gpu(self, *tensors):
-        for t in tensors:
-            if t.get_device() != self._gpu:
-                raise ValueError(f"a tensor on {t.device}: the layer's tensors are on its GPU")
+    # The checks are a call's host time next to its launch: few of torch's calls, no loops.
+    @staticmethod
+    def _elsewhere(what):
+        return ValueError(f"{what}: the layer's tensors are on its GPU")
 
-    def _check_rows(self, R, offsets):
-        self._check_gpu(offsets)
+    def _check_rows(self, x, k, rows, offsets):
+        """T, R and the pitch of x's rows."""
+        shape = x.shape
+        if x.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != k or x.stride(1) != 1:
+            raise ValueError(f"bf16 rows of {k} contiguous elements")
+        gpu, T = self._gpu, shape[0]
+        if rows is None:
+            R = T
+        else:
+            R = rows.numel()
+            if rows.dtype is not torch.int32 or not rows.is_contiguous():
+                raise ValueError("rows: contiguous int32 values")
+            if rows.get_device() != gpu:
+                raise self._elsewhere("rows")
         if R > self.max_rows:
             raise ValueError(f"{R} rows for a layer of at most {self.max_rows}")
-        if offsets.dtype != torch.int32 or offsets.numel() != self.groups + 1 or not offsets.is_contiguous():
+        if offsets.dtype is not torch.int32 or offsets.numel() != self.groups + 1 or not offsets.is_contiguous():
             raise ValueError(f"offsets: {self.groups + 1} contiguous int32 values")
-
-    def _pitch(self, x, k):
-        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.size(1) != k or x.stride(1) != 1:
-            raise ValueError(f"bf16 rows of {k} contiguous elements")
-        self._check_gpu(x)
-        return abi.row_pitch(x)
+        if x.get_device() != gpu or offsets.get_device() != gpu:
+            raise self._elsewhere("rows and offsets")
+        return T, R, abi.row_pitch(x)
 
     def _check_w(self, w):
         if w.dtype != torch.bfloat16 or w.shape != (self.groups, self.N, self.K) or not w.is_contiguous():
             raise ValueError(f"W: contiguous bf16 [{self.groups}, {self.N}, {self.K}]")
-        self._check_gpu(w)
+        if w.get_device() != self._gpu:
+            raise self._elsewhere("W")
         if self.w_blobs is None:
-            self.w_blobs = abi.alloc_grouped_blobs(self.groups * self.N, self.K, self.groups, equal=True, dual=False,
-                                                   device=w.device)
-            self._c.w_blobs[:] = _addresses(self.w_blobs)
+            self._keep_w(abi.alloc_grouped_blobs(self.groups * self.N, self.K, self.groups, equal=True, dual=False,
+                                                 device=w.device))
+
+    def _keep_w(self, blobs):
+        self.w_blobs = blobs
+        self._c.w_blobs[:] = self._w_at = _addresses(blobs)
 
     def _check_packed(self, w_q, w_s):
-        for t, n in zip((w_q, w_s), self._packed_bytes):
-            if not isinstance(t, torch.Tensor) or t.element_size() != 1 or t.numel() < n or not t.is_contiguous():
-                raise ValueError("packed weights: contiguous bytes, {} of codes and {} of scales".format(*self._packed_bytes))
-        self._check_gpu(w_q, w_s)
+        q, s = self._packed_bytes
+        try:
+            good = (w_q.element_size() == 1 and w_s.element_size() == 1 and w_q.numel() >= q and w_s.numel() >= s and
+                    w_q.is_contiguous() and w_s.is_contiguous())
+        except AttributeError:   # not tensors
+            good = False
+        if not good:
+            raise ValueError(f"packed weights: contiguous bytes, {q} of codes and {s} of scales")
+        if w_q.get_device() != self._gpu or w_s.get_device() != self._gpu:
+            raise self._elsewhere("packed weights")
 
     def quantize_w(self, w, stream=None):
         """The blobs of W[E, N, K], kept for the products that follow (a forward and its backward use
@@ -100,16 +119,8 @@ class MXFP4GroupedLinear:
         self._has_w, self._rows = True, None
 
     def _forward(self, x, w, offsets, rows, stream):
-        ldx = self._pitch(x, self.K)
-        if rows is None:
-            R = x.size(0)
-        else:
-            R = rows.numel()
-            if rows.dtype != torch.int32 or not rows.is_contiguous():
-                raise ValueError("rows: contiguous int32 values")
-            self._check_gpu(rows)
-        self._check_rows(R, offsets)
-        abi.mxfp4_grouped_forward(self._c, x, x.size(0), ldx, rows, offsets, R, w, stream)
+        T, R, ldx = self._check_rows(x, self.K, rows, offsets)
+        abi.mxfp4_grouped_forward(self._c, x, T, ldx, rows, offsets, R, w, stream)
         self._rows = R
         return self.y if R == self.max_rows else self.y[:R]
 
@@ -119,7 +130,8 @@ class MXFP4GroupedLinear:
             self._check_w(w)
         elif not self._has_w:
             raise ValueError("no weights quantized yet")
-        self._c.w_blobs[0], self._c.w_blobs[1] = self.w_blobs[0].data_ptr(), self.w_blobs[1].data_ptr()
+        if self._away:
+            self._c.w_blobs[:], self._away = self._w_at, False
         y = self._forward(x, w, offsets, rows, stream)
         self._has_w, self._packed = True, False
         return y
@@ -128,6 +140,7 @@ class MXFP4GroupedLinear:
         """Y [R, N] with the row blob of the weights (codes [E * N, Kp / 2], scales in the tensor-core
         layout with each expert's rows padded to 128).  No backward follows it."""
         self._check_packed(w_q, w_s)
+        self._away = True
         self._c.w_blobs[0], self._c.w_blobs[1] = w_q.data_ptr(), w_s.data_ptr()
         y = self._forward(x, None, offsets, rows, stream)
         self._packed = True
@@ -140,8 +153,7 @@ class MXFP4GroupedLinear:
             raise ValueError("backward needs the column blobs of a training layer")
         if self._packed:
             raise ValueError("the last forward took packed weights, which have no column blob")
-        lddy, R = self._pitch(dy, self.N), dy.size(0)
-        self._check_rows(R, offsets)
+        _, R, lddy = self._check_rows(dy, self.N, None, offsets)
         if R != self._rows:   # X's column blob is laid out for that forward's rows
             raise ValueError(f"{R} rows after " + ("no forward" if self._rows is None else
                                                    f"a forward of {self._rows} rows"))

@@ -174,3 +174,28 @@ def test_one_row_has_no_pitch_in_the_quantizer(calls, monkeypatch):
     abi.quantize_grouped(bf16(20, 1).t().as_subclass(Row), None, None, 1)
     (_, args), = calls
     assert args[3] >= 20 and args[3] % 8 == 0
+
+
+def test_forwards_with_own_and_packed_weights_in_turn(calls):
+    # each call's weights are the ones it was given, and a refused call changes nothing for the backward
+    ours = layer()
+    own = [b.data_ptr() for b in ours.w_blobs]
+    w_q, w_s = abi.alloc_grouped_blobs(E * N, K, E, equal=True, dual=False, device="cpu")
+    seen = []
+
+    def note():
+        seen.append(list(calls[-1][1][0].w_blobs[:2]))
+
+    ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)
+    note()
+    with pytest.raises(ValueError):
+        ours.forward_packed(bf16(4, K), w_q, w_s, OFFSETS[:-1])
+    ours.backward(bf16(4, N), OFFSETS)
+    assert list(calls[-1][1][0].w_blobs[2:]) == own[2:]
+    ours.forward(bf16(4, K), None, OFFSETS)
+    note()
+    ours.forward_packed(bf16(4, K), w_q, w_s, OFFSETS)
+    note()
+    ours.forward(bf16(4, K), bf16(E, N, K), OFFSETS)
+    note()
+    assert seen == [own[:2], own[:2], [w_q.data_ptr(), w_s.data_ptr()], own[:2]]
