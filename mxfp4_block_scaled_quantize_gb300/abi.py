@@ -215,11 +215,25 @@ def _ptr(buf) -> Optional[int]:
     return buf.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """The function that gives the current stream's handle.  Torch has the handle alone under names that it does not
+    promise to keep; its public stream object around it takes 3 us more a call."""
+    import torch
+    raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _stream(stream) -> Optional[int]:
+    global _current_stream
     if stream is None:
-        # the handle alone: building torch's stream object around it takes 3 us
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
