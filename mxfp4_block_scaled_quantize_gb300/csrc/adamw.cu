@@ -36,6 +36,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "adamw_math.cuh"
 #include "launch.h"
 #include "launch_adamw.h"
 #include "philox.cuh"
@@ -164,12 +165,6 @@ __device__ __forceinline__ uint2 encode_e4m3(const float* f) {
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
 // Stochastic rounding onto E4M3's magnitudes (steps of g = 2^(e - 3) in [2^e, 2^(e + 1)), 2^-9
 // below 2^-6): a = |y| <= 448 (1 + 2^-22), x: a value with y's sign, r: 16 random bits.  Gives the
 // lower neighbour lo unless (a - lo) / g >= (r + 1/2) / 2^16, so that the chance of the upper one
@@ -187,11 +182,7 @@ __device__ __forceinline__ float sr_e4m3(float a, float x, uint32_t r) {
 
 // This lane's block (16 lanes) of x: its scale, and the eight codes.  kRoot: values >= 0, of
 // which those above zero stay there.  kSr: stochastically, by `bits`, of which element k takes half
-// k % 2 of word k / 2.  The quotients x / scale are those of IEEE division, by
-// Markstein's theorem (IBM J. Res. Dev. 34, 1990): from the correctly rounded reciprocal y,
-// q = x y and the exact residual x - q scale give the correctly rounded quotient as
-// q + residual y.  Three operations an element in place of a division; a code is the nearest to
-// the rounded quotient in either case.
+// k % 2 of word k / 2.  The quotients x / scale are those of adamw_math.cuh.
 template <bool kRoot, bool kSr>
 __device__ __forceinline__ uint2 encode_block(const float* x, float* scale, uint4 bits) {
     const float inf = __int_as_float(0x7F800000);
@@ -216,8 +207,7 @@ __device__ __forceinline__ uint2 encode_block(const float* x, float* scale, uint
     float y[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float q = __fmul_rn(x[k], inv);
-        y[k] = __fmaf_rn(__fmaf_rn(-q, s, x[k]), inv, q);
+        y[k] = quotient(x[k], s, inv);
         if (kSr) y[k] = sr_e4m3(fabsf(y[k]), x[k], k & 1 ? rnd[k >> 1] >> 16 : rnd[k >> 1] & 0xFFFFu);
         if (kRoot) y[k] = x[k] > 0.0f ? fmaxf(y[k], kMinCode) : 0.0f;
     }
@@ -227,32 +217,6 @@ __device__ __forceinline__ uint2 encode_block(const float* x, float* scale, uint
             if (!(fabsf(x[k]) < inf)) y[k] = __int_as_float(0x7FC00000);
     }
     return encode_e4m3(y);
-}
-
-// Square roots of eight values >= 0: y = 1 / sqrt(v) approximately, s = v y, and one correction
-// by the exact residual, s + (v - s^2) y / 2 (Markstein, as above); equal to __fsqrt_rn for
-// every mantissa of both exponent parities (checked over [1, 4)), without its branch an element.
-// Values outside [2^-100, 2^126), where a residual could lose bits, zero among them, take
-// __fsqrt_rn.
-__device__ __forceinline__ void sqrt8(const float* v, float* r) {
-    float lo = v[0], hi = v[0];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) {
-        lo = fminf(lo, v[k]);
-        hi = max_nan(hi, v[k]);
-    }
-    if (lo >= 7.8886091e-31f && hi < 8.5070592e37f) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float y;
-            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v[k]));
-            const float s = __fmul_rn(v[k], y);
-            r[k] = __fmaf_rn(__fmaf_rn(-s, s, v[k]), 0.5f * y, s);
-        }
-    } else {
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(v[k]);
-    }
 }
 
 struct Hyper {
