@@ -24,6 +24,12 @@ class OnTheGpu(torch.Tensor):
     def get_device(self):
         return self.gpu
 
+    @classmethod
+    def __torch_function__(cls, func, types, args=(), kwargs=None):
+        if func is torch.Tensor.get_device:   # called as a function
+            return args[0].gpu
+        return super().__torch_function__(func, types, args, kwargs or {})
+
 
 class OnAnotherGpu(OnTheGpu):
     gpu = 1
