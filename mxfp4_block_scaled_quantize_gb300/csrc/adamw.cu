@@ -46,10 +46,11 @@ namespace mxfp4 {
 namespace {
 
 // Threads of a CTA.  With 8-bit moments the arithmetic (some 65 instructions an element) nearly
-// fills the time of the memory, and many small CTAs keep both busy: one warp takes 717 us for 288 M
-// elements (6.5 TB/s, 0.97 of the measured copy), four warps 754; for 140 M in tensors of odd sizes
-// with fp32 gradients 473 and 455.  With fp32 moments, 72 M elements in 48 tensors, 128 threads take
-// 320 us (6.3 TB/s), 64 322 and one warp 326.
+// fills the time of the memory, and many small CTAs keep both busy: one warp takes 715 us for 280 M
+// elements (6.3 TB/s, 0.94 of the measured copy), two 784, four 748.  For 140 M in tensors of odd
+// sizes with fp32 gradients it is 424, 458 and 405: there four warps gain what they lose on whole
+// tensors, and one warp is kept for both.  With fp32 moments, 69.7 M elements in 48 tensors, 128
+// threads take 280.5 us (7.0 TB/s), 64 284 and one warp 288.  (Steps back to back.)
 constexpr int kThreads32 = 128;   // fp32 moments
 constexpr int kThreads8 = 32;     // 8-bit moments
 constexpr float kE4m3Max = 448.0f;

@@ -10,7 +10,9 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 512;
 constexpr int64_t kTileConstant = 320; // of the cost of a tile, in columns
 // Tokens a group, on average, up to which the few-token products run (8 groups, 4096 x 4096: 26.6 us
-// against 30.7 at 96 tokens, 34.8 against 30.8 at 192).
+// against 30.7 at 96 tokens, 34.8 against 30.8 at 192).  The average is all that the host knows; one
+// large group among 63 of one token, 2048 x 2048, loses little by it: 45.6 us for 5953 rows by these
+// products, 43.4 for 6145 by the others.
 constexpr int64_t kFewTokens = 96;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -167,7 +169,7 @@ enum Ready { kNothing, kOffsets, kOffsetsAndW };
 // Columns of the tiles of `strips` strips of `cols` columns each (forward, dgrad: a group's tokens on
 // average, all that the host knows of them): the width whose modelled time is least.  The
 // tiles go round the clusters in waves, and a tile costs its columns and a constant.  A whole training
-// step at 384, 256 and 128 columns throughout, in us: 64 groups of 384 tokens, 1408 x 2048, 349, 357,
+// step, as graph replays, at 384, 256 and 128 columns throughout, in us: 64 groups of 384 tokens, 1408 x 2048, 349, 357,
 // 425; 8 of 2048, 8192 x 2048, 485, 533, 736; 5 of 222 in fp32 with few tiles to go round 56.0, 53.7,
 // 53.9, where the rule's own mixture takes 53.1.  The constant came from the first two: at 256 the
 // rule took 256 columns for the second one's dgrad, and that step 502 us; it now takes 481.
