@@ -545,7 +545,9 @@ typedef struct {
 /* beta1, beta2 in [0, 1), eps 0 or a normal fp32 above it, step >= 1 (the number of this step).  dynamic: NULL, or
  * four fp32 in device memory read instead of the host's values, so that a captured graph can
  * go on: lr, 1 - beta1^step, 1 - beta2^step, grad_scale; with MXFP4_ADAMW_STOCHASTIC five, the
- * fifth the step's number (exact up to 2^24).  seed: read with MXFP4_ADAMW_STOCHASTIC only. */
+ * fifth the step's number (exact up to 2^24).  seed: read with MXFP4_ADAMW_STOCHASTIC only.
+ * grad_factor: NULL, or an fp32 in device memory that grad_scale is multiplied by (in fp32): the
+ * factor of mxfp4_grad_norm. */
 typedef struct {
     double lr;
     double beta1;
@@ -556,10 +558,67 @@ typedef struct {
     int64_t step;
     const float* dynamic;
     uint64_t seed;
+    const float* grad_factor;
 } mxfp4_adamw_params;
 
 mxfp4_status mxfp4_adamw(int32_t count, const mxfp4_adamw_tensor* tensors, int32_t flags,
                          const mxfp4_adamw_params* params, mxfp4_stream_t stream);
+
+/* ---- layer norm ---------------------------------------------------------------------------
+ * y = (x - mu) r g + b for each row x of X[rows, dim]: mu its mean, r = 1 / sqrt(mean((x - mu)^2) + eps),
+ * g the weight, or 1 + weight with MXFP4_NORM_ADD_ONE (modulation), 1 where weight is NULL; b the
+ * bias, 0 where it is NULL.  All in fp32, y rounded once.
+ *   x, y          bf16, or fp32 with MXFP4_NORM_X_F32; row pitches ldx, ldy elements (>= dim; one row alone: any),
+ *                 aligned to the element.  Addresses of 16 bytes and dim and pitches of 8 elements are fastest.
+ *   weight, bias  [samples, dim] dense, bf16 or (MXFP4_NORM_W_F32) fp32: one for each of `samples` equal runs of
+ *                 consecutive rows; samples 1: for all of X.  rows % samples == 0.
+ *   mean, rstd    fp32[rows], mu and r for the backward pass; or both NULL
+ *   dim           1 .. MXFP4_NORM_MAX_DIM;  rows == 0 does nothing
+ * Backward: with a = dy g and xh = (x - mu) r, dx = r (a - mean(a) - xh mean(a xh)) in the type of x, and
+ * dw = sum of dy xh, db = sum of dy over the rows of each sample, fp32[samples, dim] dense; either may be
+ * NULL.  The same inputs give the same bits.  rows == 0 writes zeros to dw and db.
+ *   workspace     mxfp4_layer_norm_workspace_bytes(dim) bytes, 16-byte aligned, scratch (NULL and 0 where dw
+ *                 and db are NULL); calls that share one are ordered one after the other
+ * dx must not overlap x or dy, nor y x. */
+#define MXFP4_NORM_X_F32 1
+#define MXFP4_NORM_W_F32 2
+#define MXFP4_NORM_ADD_ONE 4
+#define MXFP4_NORM_MAX_DIM 16384
+
+mxfp4_status mxfp4_layer_norm(const void* x, int64_t rows, int64_t dim, int64_t ldx, const void* weight, const void* bias,
+                              int64_t samples, double eps, int32_t flags, void* y, int64_t ldy, float* mean, float* rstd,
+                              mxfp4_stream_t stream);
+mxfp4_status mxfp4_layer_norm_workspace_bytes(int64_t dim, size_t* bytes);
+mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t rows, int64_t dim, int64_t ldx,
+                                       const void* weight, int64_t samples, int32_t flags, const float* mean, const float* rstd,
+                                       void* dx, int64_t lddx, float* dw, float* db, void* workspace, size_t workspace_bytes,
+                                       mxfp4_stream_t stream);
+
+/* ---- the gradients' norm ------------------------------------------------------------------
+ * norm = sqrt(sum over all tensors of sum g^2) and factor = min(1, max_norm / (norm + 1e-6)), or 1
+ * where max_norm is infinite, into out[0] and out[1] (device memory).  With MXFP4_GRAD_SCALE the
+ * gradients are then multiplied by the factor in place, each product rounded once to its type; else
+ * they are only read, and mxfp4_adamw takes the factor as its grad_factor.  The norm holds for
+ * elements of every finite size; an infinite one gives norm inf and factor 0, a NaN makes both NaN.
+ * The same gradients give the same bits.
+ *   tensors    count of them (0 .. MXFP4_GRAD_MAX_TENSORS), n elements each (n == 0: skipped; at most
+ *              2^40 in all), dense, aligned to their element; no two overlap
+ *   max_norm   above 0; may be infinite
+ *   workspace  mxfp4_grad_norm_workspace_bytes(count) bytes, 256-byte aligned, all zero before its
+ *              first use (a call leaves its first 256 bytes zero); calls that share one are ordered
+ *              one after the other, as are replays of graphs that hold them */
+#define MXFP4_GRAD_F32 1             /* gradients fp32 (else bf16)                              */
+#define MXFP4_GRAD_SCALE 2           /* multiply the gradients by the factor in place           */
+#define MXFP4_GRAD_MAX_TENSORS 65536
+
+typedef struct {
+    void* g;
+    int64_t n;
+} mxfp4_grad_tensor;
+
+mxfp4_status mxfp4_grad_norm_workspace_bytes(int32_t count, size_t* bytes);
+mxfp4_status mxfp4_grad_norm(int32_t count, const mxfp4_grad_tensor* tensors, int32_t flags, double max_norm, float* out,
+                             void* workspace, size_t workspace_bytes, mxfp4_stream_t stream);
 
 /* ---- a step from host memory to host memory -------------------------------------------
  * The data path of `MXFP4LinearFunction` (primus_turbo_mxfp4_local.py) for linears whose

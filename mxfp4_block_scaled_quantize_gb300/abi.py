@@ -44,6 +44,15 @@ MXFP4_ADAMW_STATE_E4M3 = 4
 MXFP4_ADAMW_STOCHASTIC = 8
 MXFP4_ADAMW_BLOCK = 128
 
+MXFP4_NORM_X_F32 = 1
+MXFP4_NORM_W_F32 = 2
+MXFP4_NORM_ADD_ONE = 4
+MXFP4_NORM_MAX_DIM = 16384
+
+MXFP4_GRAD_F32 = 1
+MXFP4_GRAD_SCALE = 2
+MXFP4_GRAD_MAX_TENSORS = 65536
+
 
 class GemmTask(ctypes.Structure):
     """mxfp4_gemm_task of include/mxfp4.h."""
@@ -95,7 +104,8 @@ class AdamwTensor(ctypes.Structure):
 class AdamwParams(ctypes.Structure):
     """mxfp4_adamw_params of include/mxfp4.h."""
     _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + \
-        [("step", ctypes.c_int64), ("dynamic", ctypes.c_void_p), ("seed", ctypes.c_uint64)]
+        [("step", ctypes.c_int64), ("dynamic", ctypes.c_void_p), ("seed", ctypes.c_uint64),
+         ("grad_factor", ctypes.c_void_p)]
 
 
 class LinearHostTask(ctypes.Structure):
@@ -131,6 +141,11 @@ EXPORTED = (
     "mxfp4_grouped_forward",
     "mxfp4_grouped_backward",
     "mxfp4_adamw",
+    "mxfp4_layer_norm",
+    "mxfp4_layer_norm_workspace_bytes",
+    "mxfp4_layer_norm_backward",
+    "mxfp4_grad_norm_workspace_bytes",
+    "mxfp4_grad_norm",
     "mxfp4_linear_workspace_bytes",
     "mxfp4_linear_step_host",
     "mxfp4_linear_pipelined_workspace_bytes",
@@ -190,6 +205,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_grouped_forward.argtypes = [ctypes.POINTER(GroupedLinear), vp, i64, i64, vp, vp, i64, vp, vp]
     lib.mxfp4_grouped_backward.argtypes = [ctypes.POINTER(GroupedLinear), vp, i64, vp, i64, vp]
     lib.mxfp4_adamw.argtypes = [i32, vp, i32, ctypes.POINTER(AdamwParams), vp]
+    f64, sz = ctypes.c_double, ctypes.c_size_t
+    lib.mxfp4_layer_norm.argtypes = [vp, i64, i64, i64, vp, vp, i64, f64, i32, vp, i64, vp, vp, vp]
+    lib.mxfp4_layer_norm_workspace_bytes.argtypes = [i64, szp]
+    lib.mxfp4_layer_norm_backward.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, i32, vp, vp, vp, i64, vp, vp, vp, sz, vp]
+    lib.mxfp4_grad_norm_workspace_bytes.argtypes = [i32, szp]
+    lib.mxfp4_grad_norm.argtypes = [i32, vp, i32, f64, vp, vp, sz, vp]
     lib.mxfp4_linear_workspace_bytes.argtypes = [i32, ctypes.POINTER(LinearHostTask),
                                                  ctypes.POINTER(ctypes.c_size_t)]
     lib.mxfp4_linear_step_host.argtypes = [i32, ctypes.POINTER(LinearHostTask), vp, ctypes.c_size_t, vp]
@@ -455,6 +476,36 @@ def mxfp4_adamw(count, tensors, flags, params, stream=None) -> None:
     """tensors: a ctypes array of AdamwTensor, or the address of such a table; params: AdamwParams."""
     address = tensors if isinstance(tensors, int) or tensors is None else ctypes.addressof(tensors)
     _check(load().mxfp4_adamw(count, address, flags, ctypes.byref(params), _stream(stream)), "mxfp4_adamw")
+
+
+def mxfp4_layer_norm(x, rows, dim, ldx, weight, bias, samples, eps, flags, y, ldy, mean=None, rstd=None, stream=None) -> None:
+    _check(load().mxfp4_layer_norm(_ptr(x), rows, dim, ldx, _ptr(weight), _ptr(bias), samples, eps, flags, _ptr(y), ldy,
+                                   _ptr(mean), _ptr(rstd), _stream(stream)), "mxfp4_layer_norm")
+
+
+def mxfp4_layer_norm_workspace_bytes(dim: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp4_layer_norm_workspace_bytes(dim, ctypes.byref(n)), "mxfp4_layer_norm_workspace_bytes")
+    return n.value
+
+
+def mxfp4_layer_norm_backward(dy, lddy, x, rows, dim, ldx, weight, samples, flags, mean, rstd, dx, lddx, dw, db, workspace,
+                              workspace_bytes, stream=None) -> None:
+    _check(load().mxfp4_layer_norm_backward(_ptr(dy), lddy, _ptr(x), rows, dim, ldx, _ptr(weight), samples, flags,
+                                            _ptr(mean), _ptr(rstd), _ptr(dx), lddx, _ptr(dw), _ptr(db), _ptr(workspace),
+                                            workspace_bytes, _stream(stream)), "mxfp4_layer_norm_backward")
+
+
+def mxfp4_grad_norm_workspace_bytes(count: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp4_grad_norm_workspace_bytes(count, ctypes.byref(n)), "mxfp4_grad_norm_workspace_bytes")
+    return n.value
+
+
+def mxfp4_grad_norm(count, tensors, flags, max_norm, out, workspace, workspace_bytes, stream=None) -> None:
+    """tensors: the address of a table of mxfp4_grad_tensor."""
+    _check(load().mxfp4_grad_norm(count, tensors, flags, max_norm, _ptr(out), _ptr(workspace), workspace_bytes,
+                                  _stream(stream)), "mxfp4_grad_norm")
 
 
 def _host_tasks(tasks):

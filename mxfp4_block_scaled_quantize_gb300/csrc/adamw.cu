@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kState8 ? kThreads8 : kThreads32, kState8 ? 32
     const float c1 = dyn ? __ldg(a.dynamic + 1) : a.c1, c2 = dyn ? __ldg(a.dynamic + 2) : a.c2;
     Hyper h{a.beta1, a.one_beta1, a.beta2, a.one_beta2, a.eps, lr / c1, 1.0f / sqrtf(c2), lr * a.weight_decay,
             dyn ? __ldg(a.dynamic + 3) : a.grad_scale, 0u, 0u, 0u};
+    if (a.grad_factor != nullptr) h.grad_scale *= __ldg(a.grad_factor);
     if (kSr) {
         h.tensor = static_cast<uint32_t>(a.first + lo);
         h.step = dyn ? static_cast<uint32_t>(__ldg(a.dynamic + 4)) : a.step;
@@ -367,7 +368,7 @@ mxfp4_status check(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, co
     if (!(h->beta1 >= 0.0 && b1 < 1.0f) || !(h->beta2 >= 0.0 && b2 < 1.0f) || !(h->eps >= 0.0) || h->step < 1 ||
         !std::isfinite(eps) || (h->eps > 0.0 && eps < kMinScale) || !std::isfinite(h->lr) || !std::isfinite(h->weight_decay))
         return MXFP4_ERR_INVALID_ARG;
-    if (!aligned_to(h->dynamic, 4)) return MXFP4_ERR_MISALIGNED;
+    if (!aligned_to(h->dynamic, 4) || !aligned_to(h->grad_factor, 4)) return MXFP4_ERR_MISALIGNED;
     const bool p_f32 = flags & MXFP4_ADAMW_P_F32, g_f32 = flags & MXFP4_ADAMW_G_F32, s8 = flags & MXFP4_ADAMW_STATE_E4M3;
     for (int32_t j = 0; j < count; ++j) {
         const mxfp4_adamw_tensor& x = t[j];
@@ -399,6 +400,7 @@ mxfp4_status step(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, con
     a.c2 = static_cast<float>(1.0 - std::pow(h.beta2, static_cast<double>(h.step)));
     a.grad_scale = static_cast<float>(h.grad_scale);
     a.dynamic = h.dynamic;
+    a.grad_factor = h.grad_factor;
     a.first = 0;
     a.step = static_cast<uint32_t>(h.step);
     a.seed = flags & MXFP4_ADAMW_STOCHASTIC ? h.seed : 0;

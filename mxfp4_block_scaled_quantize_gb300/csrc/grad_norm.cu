@@ -1,0 +1,357 @@
+// grad_norm.cu -- the norm of all gradients of a step, and scaling them by a factor on the device.
+//
+//   norm = sqrt(sum over all tensors of sum g^2),  factor = min(1, max_norm / (norm + 1e-6)),
+//   and, for clipping in place, g = factor g, rounded once.
+//
+// Sums.  A thread adds the squares of 32 elements in fp32 and everything above that in fp64: the
+// norm is off by a few 2^-24 at most however many elements there are, and the order is fixed, so
+// the same gradients give the same bits.  Squares leave fp32's range where the elements do not
+// (1e20, or 1e-25 throughout): a sum of 32 above 2^120 or below 2^-80 is formed again from the
+// registers with the elements times 2^-80 or 2^80, both exact up to what cannot count.
+//
+// The norm is bound by the memory: 2 or 4 bytes an element, and about 1.5 instructions.  Clipping
+// in place reads and writes the gradients once more, and runs through them backward, so that what
+// the norm read last is still in the L2 (129 MB).
+//
+// Work.  A unit of 8192 elements, at addresses that are multiples of 16 bytes whatever the tensor's
+// own alignment: a tensor's first unit leaves out what lies before it.  CTA c takes units c, c + G,
+// ...: all loads of a unit are in flight together.  The last CTA to leave its sum adds them all up;
+// nobody waits for anybody.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "launch.h"
+#include "launch_grad_norm.h"
+#include "ptx.cuh"
+
+namespace mxfp4 {
+namespace {
+
+constexpr float kBig = 1.329227996e36f;        // 2^120
+constexpr float kSmall = 8.271806126e-25f;     // 2^-80
+constexpr float kUp = 1.208925820e24f;         // 2^80
+constexpr double kUp2 = 1.461501637330902918e48;       // 2^160
+constexpr double kSmall2 = 6.842277657836020854e-49;   // 2^-160
+constexpr int kWords = kGradUnit / kGradThreads / 8;   // 16-byte loads of 8 bf16 in a thread's part
+
+// The tensor of a launch's unit, and the element at which the unit starts (below zero, by less than
+// a load, in a tensor's first unit).
+template <int kCap>
+__device__ __forceinline__ const mxfp4_grad_tensor& find(const GradArgs<kCap>& a, int unit, int esize, int64_t* first) {
+    int lo = 0, hi = a.count - 1;   // the tensor of this unit: the first with end > unit
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.end[mid] > unit) hi = mid;
+        else lo = mid + 1;
+    }
+    const mxfp4_grad_tensor& t = a.t[lo];
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(t.g) & 15u) / esize;
+    *first = static_cast<int64_t>(unit - (lo > 0 ? a.end[lo - 1] : 0)) * kGradUnit - skew;
+    return t;
+}
+
+// A thread's 32 elements of the unit at `first`, as 32-bit words: pairs of bf16, or fp32.
+template <bool kF32>
+struct Part {
+    static constexpr int kLoads = kF32 ? 2 * kWords : kWords;
+    static constexpr int kPer = kF32 ? 4 : 8;     // elements of a load
+    static constexpr int kElement = kF32 ? 4 : 2;
+    uint4 w[kLoads];
+
+    __device__ __forceinline__ static int64_t at(int64_t first, int j) {
+        return first + (j * kGradThreads + static_cast<int>(threadIdx.x)) * kPer;
+    }
+    __device__ __forceinline__ static uint32_t load1(const void* g, int64_t i) {
+        return kF32 ? static_cast<const uint32_t*>(g)[i] : static_cast<const uint16_t*>(g)[i];
+    }
+    __device__ __forceinline__ void load(const void* g, int64_t n, int64_t first) {
+        if (first >= 0 && first + kGradUnit <= n) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                w[j] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + at(first, j) * kElement);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int64_t i = at(first, j);
+            w[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (i >= 0 && i + kPer <= n) {
+                w[j] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + i * kElement);
+            } else if (i + kPer > 0 && i < n) {
+                uint32_t* const v = reinterpret_cast<uint32_t*>(&w[j]);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    if (i + k >= 0 && i + k < n) {
+                        if (kF32) v[k] = load1(g, i + k);
+                        else v[k >> 1] |= load1(g, i + k) << (16 * (k & 1));
+                    }
+            }
+        }
+    }
+    __device__ __forceinline__ float sum(float scale) const {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (kF32) {
+                    const float a = __uint_as_float(v[k]) * scale;
+                    s[k] = fmaf(a, a, s[k]);
+                } else {
+                    const float a = __uint_as_float(v[k] << 16) * scale, b = __uint_as_float(v[k] & 0xFFFF0000u) * scale;
+                    s[k] = fmaf(a, a, s[k]);
+                    s[k] = fmaf(b, b, s[k]);
+                }
+            }
+        }
+        return (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    __device__ __forceinline__ bool any() const {
+        uint32_t o = 0;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) o |= w[j].x | w[j].y | w[j].z | w[j].w;
+        return (o & (kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) != 0;
+    }
+    __device__ __forceinline__ double squares() const {
+        const float s = sum(1.0f);
+        if (s >= kSmall && s <= kBig) return static_cast<double>(s);
+        if (s < kSmall) return any() ? static_cast<double>(sum(kUp)) * kSmall2 : 0.0;
+        return static_cast<double>(sum(kSmall)) * kUp2;   // NaN and infinities too
+    }
+    __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            uint32_t* const v = reinterpret_cast<uint32_t*>(&w[j]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (kF32) {
+                    v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[k] << 16) * f,
+                                                                   __uint_as_float(v[k] & 0xFFFF0000u) * f);
+                    v[k] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void* g, int64_t n, int64_t first) const {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int64_t i = at(first, j);
+            if (i >= 0 && i + kPer <= n) {
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g) + i * kElement) = w[j];
+            } else if (i + kPer > 0 && i < n) {
+                const uint32_t* const v = reinterpret_cast<const uint32_t*>(&w[j]);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    if (i + k >= 0 && i + k < n) {
+                        if (kF32) static_cast<uint32_t*>(g)[i + k] = v[k];
+                        else static_cast<uint16_t*>(g)[i + k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
+                    }
+            }
+        }
+    }
+};
+
+// The CTA's sum of x, in thread 0; every thread calls it.
+__device__ __forceinline__ double block_sum(double x, double* shared) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+    __syncthreads();
+    if (lane_id() == 0) shared[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        x = lane_id() < kGradThreads / 32 ? shared[lane_id()] : 0.0;
+#pragma unroll
+        for (int d = kGradThreads / 64; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+    }
+    return x;
+}
+
+template <bool kF32, int kCap>
+__global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_norm_kernel(const __grid_constant__ GradArgs<kCap> a) {
+    __shared__ double shared[kGradThreads / 32];
+    __shared__ bool last;
+    grid_wait_prerequisites();
+    grid_launch_dependents();
+    const int units = a.end[a.count - 1];
+    double sum = 0.0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        int64_t first;
+        const mxfp4_grad_tensor& t = find(a, u, kF32 ? 4 : 2, &first);
+        Part<kF32> p;
+        p.load(t.g, t.n, first);
+        sum += p.squares();
+    }
+    sum = block_sum(sum, shared);
+    if (threadIdx.x == 0) {
+        a.partial[a.slot + blockIdx.x] = sum;
+        __threadfence();
+        last = atomicAdd(&a.head->done, 1u) == static_cast<uint32_t>(a.slots) - 1u;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    sum = 0.0;
+    for (int i = threadIdx.x; i < a.slots; i += kGradThreads) sum += __ldcg(a.partial + i);
+    sum = block_sum(sum, shared);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sum);
+        double factor = 1.0;
+        if (!isinf(a.max_norm)) {
+            factor = a.max_norm / (norm + 1e-6);
+            if (factor > 1.0) factor = 1.0;   // a NaN stays
+        }
+        a.out[0] = static_cast<float>(norm);
+        a.out[1] = static_cast<float>(factor);
+        a.head->done = 0;
+    }
+}
+
+template <bool kF32, int kCap>
+__global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_scale_kernel(const __grid_constant__ GradArgs<kCap> a) {
+    grid_wait_prerequisites();
+    grid_launch_dependents();
+    const float factor = __ldcg(a.out + 1);
+    if (factor == 1.0f) return;
+    const int units = a.end[a.count - 1];
+    for (int u = units - 1 - static_cast<int>(blockIdx.x); u >= 0; u -= gridDim.x) {
+        int64_t first;
+        const mxfp4_grad_tensor& t = find(a, u, kF32 ? 4 : 2, &first);
+        Part<kF32> p;
+        p.load(t.g, t.n, first);
+        p.scale(factor);
+        p.store(t.g, t.n, first);
+    }
+}
+
+__global__ void grad_empty_kernel(float* out) {
+    grid_wait_prerequisites();
+    grid_launch_dependents();
+    out[0] = 0.0f;
+    out[1] = 1.0f;
+}
+
+template <typename Kernel, typename Args>
+cudaError_t launch(Kernel kernel, const Args& a, int ctas, int threads, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+inline int64_t units_of(const mxfp4_grad_tensor& t, int esize) {
+    const int64_t skew = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.g) & 15u) / esize;
+    return (t.n + skew + kGradUnit - 1) / kGradUnit;
+}
+
+// The tensors from t[j] on that one launch takes, and the index behind them; none are left: count 0.
+template <int kCap>
+int32_t fill(GradArgs<kCap>* a, int32_t count, const mxfp4_grad_tensor* t, int32_t j, int esize) {
+    int64_t units = 0;   // below 2^28: check() bounds the elements of a call
+    a->count = 0;
+    for (; j < count && a->count < kCap; ++j) {
+        if (t[j].n == 0) continue;
+        units += units_of(t[j], esize);
+        a->t[a->count] = t[j];
+        a->end[a->count++] = static_cast<int32_t>(units);
+    }
+    return j;
+}
+
+inline int ctas_of(int units, int sms) {
+    const int most = kGradCtasPerSm * (sms < kGradMaxSms ? sms : kGradMaxSms);
+    return units < most ? units : most;
+}
+
+template <bool kF32, int kCap>
+mxfp4_status run(int32_t count, const mxfp4_grad_tensor* t, double max_norm, float* out, void* workspace, bool scale,
+                 int sms, cudaStream_t stream) {
+    GradArgs<kCap> a;
+    const int esize = kF32 ? 4 : 2;
+    a.head = static_cast<GradHead*>(workspace);
+    a.partial = reinterpret_cast<double*>(a.head + 1);
+    a.max_norm = max_norm;
+    a.out = out;
+    a.slots = 0;
+    int32_t starts[kGradLaunches], launches = 0;
+    for (int32_t j = 0; j < count;) {
+        starts[launches] = j;
+        j = fill(&a, count, t, j, esize);
+        if (a.count == 0) break;
+        a.slots += ctas_of(a.end[a.count - 1], sms);
+        ++launches;
+    }
+    if (launches == 0) return launch(grad_empty_kernel, out, 1, 1, stream) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+    a.slot = 0;
+    for (int32_t i = 0; i < launches; ++i) {
+        if (launches > 1) fill(&a, count, t, starts[i], esize);
+        const int ctas = ctas_of(a.end[a.count - 1], sms);
+        if (launch(grad_norm_kernel<kF32, kCap>, a, ctas, kGradThreads, stream) != cudaSuccess) return MXFP4_ERR_CUDA;
+        a.slot += ctas;
+    }
+    if (!scale) return MXFP4_OK;
+    for (int32_t i = launches - 1; i >= 0; --i) {   // what was read last first
+        if (launches > 1) fill(&a, count, t, starts[i], esize);
+        if (launch(grad_scale_kernel<kF32, kCap>, a, ctas_of(a.end[a.count - 1], sms), kGradThreads, stream) != cudaSuccess)
+            return MXFP4_ERR_CUDA;
+    }
+    return MXFP4_OK;
+}
+
+mxfp4_status check(int32_t count, const mxfp4_grad_tensor* t, int32_t flags, double max_norm, const float* out,
+                   const void* workspace, size_t bytes) {
+    size_t need = 0;
+    if (mxfp4_grad_norm_workspace_bytes(count, &need) != MXFP4_OK || (count > 0 && t == nullptr) || (flags & ~3) ||
+        !(max_norm > 0.0) || out == nullptr || workspace == nullptr || bytes < need)
+        return MXFP4_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(out) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MXFP4_ERR_MISALIGNED;
+    const uintptr_t element = flags & MXFP4_GRAD_F32 ? 4 : 2;
+    int64_t total = 0;
+    for (int32_t j = 0; j < count; ++j) {
+        if (t[j].n < 0 || t[j].n > (int64_t{1} << 40) || (t[j].n > 0 && t[j].g == nullptr)) return MXFP4_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(t[j].g) & (element - 1)) return MXFP4_ERR_MISALIGNED;
+        total += t[j].n;
+        if (total > int64_t{1} << 40) return MXFP4_ERR_INVALID_ARG;
+    }
+    return MXFP4_OK;
+}
+
+}  // namespace
+}  // namespace mxfp4
+
+extern "C" {
+
+mxfp4_status mxfp4_grad_norm_workspace_bytes(int32_t count, size_t* bytes) {
+    if (count < 0 || count > MXFP4_GRAD_MAX_TENSORS || bytes == nullptr) return MXFP4_ERR_INVALID_ARG;
+    const size_t launches = static_cast<size_t>(count) / mxfp4::kGradMany + 1;
+    *bytes = sizeof(mxfp4::GradHead) + launches * mxfp4::kGradSlots * sizeof(double);
+    return MXFP4_OK;
+}
+
+mxfp4_status mxfp4_grad_norm(int32_t count, const mxfp4_grad_tensor* tensors, int32_t flags, double max_norm, float* out,
+                             void* workspace, size_t workspace_bytes, mxfp4_stream_t stream) {
+    const mxfp4_status ok = mxfp4::check(count, tensors, flags, max_norm, out, workspace, workspace_bytes);
+    if (ok != MXFP4_OK) return ok;
+    int sms = 0;
+    uint32_t* err = nullptr;
+    const int st = mxfp4::device_info(&sms, &err);
+    if (st != MXFP4_OK) return static_cast<mxfp4_status>(st);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool scale = flags & MXFP4_GRAD_SCALE, f32 = flags & MXFP4_GRAD_F32, few = count <= mxfp4::kGradFew;
+    if (f32)
+        return few ? mxfp4::run<true, mxfp4::kGradFew>(count, tensors, max_norm, out, workspace, scale, sms, s)
+                   : mxfp4::run<true, mxfp4::kGradMany>(count, tensors, max_norm, out, workspace, scale, sms, s);
+    return few ? mxfp4::run<false, mxfp4::kGradFew>(count, tensors, max_norm, out, workspace, scale, sms, s)
+               : mxfp4::run<false, mxfp4::kGradMany>(count, tensors, max_norm, out, workspace, scale, sms, s);
+}
+
+}  // extern "C"

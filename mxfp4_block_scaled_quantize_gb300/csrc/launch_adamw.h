@@ -25,6 +25,7 @@ struct AdamwArgs {
     int32_t first;                   // stochastic: tensors with elements before t[0] in the call,
     uint32_t step;                   // the step's number
     uint64_t seed;                   // and the key
+    const float* grad_factor;        // or null: multiplies the gradients' scale
 };
 
 }  // namespace mxfp4

@@ -1,0 +1,49 @@
+// launch_norm.h -- internal interface of layer norm between its C entry and its kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "mxfp4.h"
+
+namespace mxfp4 {
+
+constexpr int kNormChunks = 304;                  // CTAs that share the rows of a backward pass, at most
+constexpr int kNormSlots = 2 * kNormChunks;       // partial sums that they may leave
+constexpr int kNormWarpRowDim = 1024;             // rows of up to this many elements are one warp's
+
+struct NormArgs {
+    const void* x;
+    const void* dy;          // backward
+    const void* weight;      // [samples, dim] or null
+    const void* bias;
+    void* y;                 // backward: dx
+    float* mean;
+    float* rstd;
+    float* partial_w;        // backward: [chunks of all samples, dim], or null
+    float* partial_b;
+    int64_t ldx, lddy, ldy;
+    int64_t rows;
+    int64_t sample_rows;     // rows of a sample
+    int64_t chunk_rows;      // backward: rows of a CTA, all of one sample
+    int32_t chunks;          // backward: of a sample
+    int32_t dim;
+    float eps;
+    int32_t w_f32;
+    int32_t add_one;
+};
+
+struct NormReduceArgs {
+    const float* partial[2]; // [samples * chunks, dim]
+    float* out[2];           // [samples, dim]
+    int32_t count;           // of the two
+    int32_t chunks;
+    int32_t dim;
+    int64_t samples;
+};
+
+cudaError_t launch_norm_forward(const NormArgs& a, bool f32, int sms, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormArgs& a, bool f32, int64_t ctas, cudaStream_t stream);
+cudaError_t launch_norm_reduce(const NormReduceArgs& a, cudaStream_t stream);
+
+}  // namespace mxfp4

@@ -1,0 +1,138 @@
+// norm.cu -- layer norm's C entries: checks, and how a backward pass shares its rows out.
+#include <cmath>
+#include <cstring>
+
+#include "launch.h"
+#include "launch_norm.h"
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t{1} << 40;
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool shape_ok(int64_t rows, int64_t dim, int64_t samples) {
+    return rows >= 0 && rows <= kMaxRows && dim >= 1 && dim <= MXFP4_NORM_MAX_DIM && samples >= 1 && samples <= kMaxRows &&
+           rows % samples == 0;
+}
+
+// One row alone may have any pitch.
+bool pitch_ok(int64_t ld, int64_t dim, int64_t rows) { return rows <= 1 || (ld >= dim && ld <= (int64_t{1} << 40)); }
+
+}  // namespace
+
+extern "C" {
+
+mxfp4_status mxfp4_layer_norm_workspace_bytes(int64_t dim, size_t* bytes) {
+    if (dim < 1 || dim > MXFP4_NORM_MAX_DIM || bytes == nullptr) return MXFP4_ERR_INVALID_ARG;
+    *bytes = 2 * static_cast<size_t>(mxfp4::kNormSlots) * static_cast<size_t>(dim) * sizeof(float);
+    return MXFP4_OK;
+}
+
+mxfp4_status mxfp4_layer_norm(const void* x, int64_t rows, int64_t dim, int64_t ldx, const void* weight, const void* bias,
+                              int64_t samples, double eps, int32_t flags, void* y, int64_t ldy, float* mean, float* rstd,
+                              mxfp4_stream_t stream) {
+    if (!shape_ok(rows, dim, samples) || !pitch_ok(ldx, dim, rows) || !pitch_ok(ldy, dim, rows) || (flags & ~7) ||
+        !(eps >= 0.0) || !std::isfinite(static_cast<float>(eps)) || (rows > 0 && (x == nullptr || y == nullptr)) ||
+        (mean == nullptr) != (rstd == nullptr))
+        return MXFP4_ERR_INVALID_ARG;
+    const uintptr_t xe = flags & MXFP4_NORM_X_F32 ? 4 : 2, we = flags & MXFP4_NORM_W_F32 ? 4 : 2;
+    if (!aligned_to(x, xe) || !aligned_to(y, xe) || !aligned_to(weight, we) || !aligned_to(bias, we) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4))
+        return MXFP4_ERR_MISALIGNED;
+    int sms = 0;
+    uint32_t* err = nullptr;
+    const int st = mxfp4::device_info(&sms, &err);
+    if (st != MXFP4_OK || rows == 0) return static_cast<mxfp4_status>(st);
+    mxfp4::NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.rows = rows;
+    a.sample_rows = rows / samples;
+    a.dim = static_cast<int32_t>(dim);
+    a.eps = static_cast<float>(eps);
+    a.w_f32 = flags & MXFP4_NORM_W_F32 ? 1 : 0;
+    a.add_one = flags & MXFP4_NORM_ADD_ONE ? 1 : 0;
+    return mxfp4::launch_norm_forward(a, flags & MXFP4_NORM_X_F32, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MXFP4_OK
+               : MXFP4_ERR_CUDA;
+}
+
+mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t rows, int64_t dim, int64_t ldx,
+                                       const void* weight, int64_t samples, int32_t flags, const float* mean, const float* rstd,
+                                       void* dx, int64_t lddx, float* dw, float* db, void* workspace, size_t workspace_bytes,
+                                       mxfp4_stream_t stream) {
+    if (!shape_ok(rows, dim, samples) || !pitch_ok(ldx, dim, rows) || !pitch_ok(lddy, dim, rows) || !pitch_ok(lddx, dim, rows) ||
+        (flags & ~7) || (rows > 0 && (!dy || !x || !mean || !rstd || !dx)))
+        return MXFP4_ERR_INVALID_ARG;
+    const uintptr_t xe = flags & MXFP4_NORM_X_F32 ? 4 : 2, we = flags & MXFP4_NORM_W_F32 ? 4 : 2;
+    if (!aligned_to(x, xe) || !aligned_to(dy, xe) || !aligned_to(dx, xe) || !aligned_to(weight, we) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4) || !aligned_to(dw, 4) || !aligned_to(db, 4) || !aligned_to(workspace, 16))
+        return MXFP4_ERR_MISALIGNED;
+    // Each CTA its rows of one sample, about as many for each as the whole has for kNormChunks CTAs.
+    const int64_t sample_rows = rows / samples;
+    const int64_t chunk_rows = rows > 0 ? cdiv(rows, mxfp4::kNormChunks) : 1;
+    const int64_t chunks = rows > 0 ? cdiv(sample_rows, chunk_rows) : 1;
+    const int64_t ctas = samples * chunks;   // with several chunks a sample: at most rows / chunk_rows + samples, 2 kNormChunks
+    const bool partial = chunks > 1 && (dw != nullptr || db != nullptr);
+    size_t need = 0;
+    if (partial && (mxfp4_layer_norm_workspace_bytes(dim, &need) != MXFP4_OK || workspace == nullptr || workspace_bytes < need))
+        return MXFP4_ERR_INVALID_ARG;
+    if (ctas > 0x7FFFFFFF) return MXFP4_ERR_INVALID_ARG;
+    int sms = 0;
+    uint32_t* err = nullptr;
+    const int st = mxfp4::device_info(&sms, &err);
+    if (st != MXFP4_OK) return static_cast<mxfp4_status>(st);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        const size_t bytes = static_cast<size_t>(samples) * static_cast<size_t>(dim) * sizeof(float);
+        for (float* const v : {dw, db})
+            if (v != nullptr && cudaMemsetAsync(v, 0, bytes, s) != cudaSuccess) return MXFP4_ERR_CUDA;
+        return MXFP4_OK;
+    }
+    mxfp4::NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.dy = dy;
+    a.weight = weight;
+    a.y = dx;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    float* const w = static_cast<float*>(workspace);
+    a.partial_w = dw == nullptr ? nullptr : partial ? w : dw;
+    a.partial_b = db == nullptr ? nullptr : partial ? w + mxfp4::kNormSlots * dim : db;
+    a.ldx = ldx;
+    a.lddy = lddy;
+    a.ldy = lddx;
+    a.rows = rows;
+    a.sample_rows = sample_rows;
+    a.chunk_rows = chunk_rows;
+    a.chunks = static_cast<int32_t>(chunks);
+    a.dim = static_cast<int32_t>(dim);
+    a.w_f32 = flags & MXFP4_NORM_W_F32 ? 1 : 0;
+    a.add_one = flags & MXFP4_NORM_ADD_ONE ? 1 : 0;
+    if (mxfp4::launch_norm_backward(a, flags & MXFP4_NORM_X_F32, ctas, s) != cudaSuccess) return MXFP4_ERR_CUDA;
+    if (!partial) return MXFP4_OK;
+    mxfp4::NormReduceArgs r;
+    std::memset(&r, 0, sizeof(r));
+    for (int i = 0; i < 2; ++i) {
+        float* const out = i == 0 ? dw : db;
+        if (out == nullptr) continue;
+        r.partial[r.count] = i == 0 ? a.partial_w : a.partial_b;
+        r.out[r.count++] = out;
+    }
+    r.chunks = a.chunks;
+    r.dim = a.dim;
+    r.samples = samples;
+    return mxfp4::launch_norm_reduce(r, s) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,8 +1,10 @@
-"""AdamW over the tensors of a model in one launch, with moments in fp32 or in 8 bits.
+"""AdamW over the tensors of a model in one launch, with moments in fp32 or in 8 bits; the norm of all
+gradients, and clipping by it.
 
 The weight update next to the MXFP4 layers: it takes their dW (bf16 or fp32) and writes the bf16
 W that the next step quantizes, from fp32 master copies where they are kept.
 """
+import math
 import operator
 
 import numpy as np
@@ -13,9 +15,67 @@ from . import abi
 _TABLE = np.dtype([(name, np.uint64) for name in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] +
                   [("n", np.int64)])
 
+_GRADS = np.dtype([("g", np.uint64), ("n", np.int64)])
+
 _dtype = operator.attrgetter("dtype")
 _elements, _contiguous = torch.Tensor.numel, torch.Tensor.is_contiguous
 _device, _address = torch.Tensor.get_device, torch.Tensor.data_ptr
+
+
+def _check_grads(grads, numel, gpu):
+    """The type of the gradients, one for each count of numel, on GPU gpu."""
+    dtype = grads[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16) or len(grads) != len(numel):
+        raise ValueError("one fp32 or bf16 gradient for each parameter")
+    # one of torch's functions after the other over all gradients, which takes less time than a loop's method calls
+    if not (list(map(_dtype, grads)).count(dtype) == len(grads) and list(map(_elements, grads)) == numel and
+            all(map(_contiguous, grads)) and list(map(_device, grads)).count(gpu) == len(grads)):
+        raise ValueError("gradients: contiguous, of one type and the parameters' sizes, on the parameters' GPU")
+    return dtype
+
+
+class GradNorm:
+    """The norm of all gradients of `params` (CUDA tensors: their sizes and GPU are taken).
+
+    Its results are `out`, fp32 [norm, factor] on the GPU, factor = min(1, max_norm / (norm + 1e-6)).
+    They live until the next call, and calls of one GradNorm, or replays of graphs that hold them, come
+    one after the other: give each of two that may overlap a GradNorm of its own."""
+
+    def __init__(self, params):
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        if len(params) > abi.MXFP4_GRAD_MAX_TENSORS:
+            raise ValueError(f"{abi.MXFP4_GRAD_MAX_TENSORS} parameters at most")
+        self._gpu = params[0].get_device() if params[0].is_cuda else None   # no tensor's get_device() is None
+        self._numel = [p.numel() for p in params]
+        self._table = np.zeros(len(params), dtype=_GRADS)
+        self._table["n"] = self._numel
+        self._grads = self._table["g"]   # a view and an address that every call uses
+        self._address = self._table.ctypes.data
+        self._workspace = torch.zeros(abi.mxfp4_grad_norm_workspace_bytes(len(params)), dtype=torch.uint8,
+                                      device=params[0].device)
+        self.out = torch.empty(2, dtype=torch.float32, device=params[0].device)
+
+    def measure(self, grads, max_norm=math.inf, stream=None):
+        """`out` for these gradients (contiguous, all fp32 or all bf16, in the order of the parameters), which
+        are only read: AdamW's step, given max_norm, does this and scales by the factor itself."""
+        return self._run(list(map(_address, grads)), _check_grads(grads, self._numel, self._gpu), max_norm, 0, stream)
+
+    def clip_(self, grads, max_norm, stream=None):
+        """The same, and the gradients multiplied by the factor in place."""
+        return self._run(list(map(_address, grads)), _check_grads(grads, self._numel, self._gpu), max_norm,
+                         abi.MXFP4_GRAD_SCALE, stream)
+
+    def _run(self, addresses, dtype, max_norm, flags, stream):
+        if not max_norm > 0:
+            raise ValueError(f"a largest norm above 0, not {max_norm}")
+        self._grads[:] = addresses
+        if dtype is torch.float32:
+            flags |= abi.MXFP4_GRAD_F32
+        abi.mxfp4_grad_norm(len(addresses), self._address, flags, max_norm, self.out, self._workspace,
+                            self._workspace.numel(), stream)
+        return self.out
 
 
 class AdamW:
@@ -66,6 +126,8 @@ class AdamW:
                       (abi.MXFP4_ADAMW_STATE_E4M3 if self.state_bits == 8 else 0) | \
                       (abi.MXFP4_ADAMW_STOCHASTIC if seed is not None else 0)
         self.steps = 0
+        # made here, not at the first use: its workspace is zeroed once, which a step being captured would put off
+        self.grad_norm = GradNorm(self.params) if len(self.params) <= abi.MXFP4_GRAD_MAX_TENSORS else None
         self._gpu = self.params[0].get_device() if self.params[0].is_cuda else None   # no tensor's get_device() is None
         self._numel = [p.numel() for p in self.params]
         self._table = np.zeros(len(self.params), dtype=_TABLE)
@@ -106,26 +168,29 @@ class AdamW:
                     [-(-n // abi.MXFP4_ADAMW_BLOCK) for n in self._numel])
         self._table["n"] = self._numel
 
-    def step(self, grads, step=None, lr=None, grad_scale=1.0, dynamic=None, stream=None):
+    def step(self, grads, step=None, lr=None, grad_scale=1.0, dynamic=None, stream=None, max_norm=None):
         """One update with the gradients (contiguous, all fp32 or all bf16, in the order of the
         parameters).  step: this step's number (default: counted from 1); grad_scale: a factor on
         every gradient; dynamic: a CUDA fp32 tensor [lr, 1 - beta1^step, 1 - beta2^step, grad_scale]
-        (with a seed, and step) that takes their place, for steps captured in a graph."""
-        dtype = grads[0].dtype
-        if dtype not in (torch.float32, torch.bfloat16) or len(grads) != len(self.params):
-            raise ValueError("one fp32 or bf16 gradient for each parameter")
-        # one of torch's functions after the other over all gradients, which takes less time than a loop's method calls
-        if not (list(map(_dtype, grads)).count(dtype) == len(grads) and list(map(_elements, grads)) == self._numel and
-                all(map(_contiguous, grads)) and list(map(_device, grads)).count(self._gpu) == len(grads)):
-            raise ValueError("gradients: contiguous, of one type and the parameters' sizes, on the parameters' GPU")
+        (with a seed, and step) that takes their place, for steps captured in a graph.  max_norm: the
+        gradients, as they are given, are scaled down to that norm where theirs is larger; their
+        norm and the factor are then in `grad_norm.out`."""
+        dtype = _check_grads(grads, self._numel, self._gpu)
         if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != self._dynamic or
                                     not dynamic.is_contiguous() or dynamic.get_device() != self._gpu):
             raise ValueError(f"dynamic: {self._dynamic} consecutive fp32 on the parameters' GPU")
         if step is None:
             step = self.steps + 1
-        self._grads[:] = list(map(_address, grads))
+        addresses = list(map(_address, grads))
+        self._grads[:] = addresses
         flags = self._flags | (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0)
+        factor = None
+        if max_norm is not None:
+            if self.grad_norm is None:
+                raise ValueError(f"max_norm: for up to {abi.MXFP4_GRAD_MAX_TENSORS} parameters")
+            self.grad_norm._run(addresses, dtype, max_norm, 0, stream)
+            factor = self.grad_norm.out.data_ptr() + 4
         h = abi.AdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                            grad_scale, step, None if dynamic is None else dynamic.data_ptr(), self.seed)
+                            grad_scale, step, None if dynamic is None else dynamic.data_ptr(), self.seed, factor)
         abi.mxfp4_adamw(len(self.params), self._address, flags, h, stream)
         self.steps = step
