@@ -3,7 +3,7 @@
 //   norm = sqrt(sum over all tensors of sum g^2),  factor = min(1, max_norm / (norm + 1e-6)),
 //   and, for clipping in place, g = factor g, rounded once.
 //
-// Sums.  A thread adds the squares of 32 elements in fp32 and everything above that in fp64: the
+// Sums.  A thread adds the squares of 32 elements (fp32: 16) in fp32 and everything above that in fp64: the
 // norm is off by a few 2^-24 at most however many elements there are, and the order is fixed, so
 // the same gradients give the same bits.  Squares leave fp32's range where the elements do not
 // (1e20, or 1e-25 throughout): a sum of 32 above 2^120 or below 2^-80 is formed again from the
@@ -13,10 +13,10 @@
 // in place reads and writes the gradients once more, and runs through them backward, so that what
 // the norm read last is still in the L2 (129 MB).
 //
-// Work.  A unit of 8192 elements, at addresses that are multiples of 16 bytes whatever the tensor's
-// own alignment: a tensor's first unit leaves out what lies before it.  CTA c takes units c, c + G,
-// ...: all loads of a unit are in flight together.  The last CTA to leave its sum adds them all up;
-// nobody waits for anybody.
+// Work.  A unit of 16 KB, at addresses that are multiples of 16 bytes whatever the tensor's own
+// alignment: a tensor's first unit leaves out what lies before it.  A CTA takes a range of consecutive
+// units, each one's loads under way while the one before is added up.  The last CTA to leave its sum
+// adds them all up; nobody waits for anybody.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -33,28 +33,57 @@ constexpr float kSmall = 8.271806126e-25f;     // 2^-80
 constexpr float kUp = 1.208925820e24f;         // 2^80
 constexpr double kUp2 = 1.461501637330902918e48;       // 2^160
 constexpr double kSmall2 = 6.842277657836020854e-49;   // 2^-160
-constexpr int kWords = kGradUnit / kGradThreads / 8;   // 16-byte loads of 8 bf16 in a thread's part
+constexpr int kLoads = kGradUnitBytes / kGradThreads / 16;   // 16-byte loads of a thread's part
 
-// The tensor of a launch's unit, and the element at which the unit starts (below zero, by less than
-// a load, in a tensor's first unit).
-template <int kCap>
-__device__ __forceinline__ const mxfp4_grad_tensor& find(const GradArgs<kCap>& a, int unit, int esize, int64_t* first) {
-    int lo = 0, hi = a.count - 1;   // the tensor of this unit: the first with end > unit
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.end[mid] > unit) hi = mid;
-        else lo = mid + 1;
+template <bool kF32>
+constexpr int kElements = kGradUnitBytes / (kF32 ? 4 : 2);   // of a unit
+
+// A walk through consecutive units, in either direction: the tensor of each and the element at which it starts
+// (below zero, by less than a load, in a tensor's first unit).
+template <bool kF32, int kCap>
+struct Walk {
+    const GradArgs<kCap>& a;
+    int j;          // tensor
+    void* g;
+    int64_t n, first;
+
+    __device__ __forceinline__ Walk(const GradArgs<kCap>& args, int unit) : a(args) {
+        int lo = 0, hi = a.count - 1;   // the first tensor with end > unit
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.end[mid] > unit) hi = mid;
+            else lo = mid + 1;
+        }
+        j = lo;
+        at(unit);
     }
-    const mxfp4_grad_tensor& t = a.t[lo];
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(t.g) & 15u) / esize;
-    *first = static_cast<int64_t>(unit - (lo > 0 ? a.end[lo - 1] : 0)) * kGradUnit - skew;
-    return t;
-}
+    __device__ __forceinline__ void at(int unit) {
+        g = a.t[j].g;
+        n = a.t[j].n;
+        const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(g) & 15u) / (kF32 ? 4 : 2);
+        first = static_cast<int64_t>(unit - (j > 0 ? a.end[j - 1] : 0)) * kElements<kF32> - skew;
+    }
+    __device__ __forceinline__ void up(int unit) {
+        if (unit >= a.end[j]) {
+            ++j;
+            at(unit);
+        } else {
+            first += kElements<kF32>;
+        }
+    }
+    __device__ __forceinline__ void down(int unit) {
+        if (j > 0 && unit < a.end[j - 1]) {
+            --j;
+            at(unit);
+        } else {
+            first -= kElements<kF32>;
+        }
+    }
+};
 
-// A thread's 32 elements of the unit at `first`, as 32-bit words: pairs of bf16, or fp32.
+// A thread's part of the unit at `first`, as 32-bit words: pairs of bf16, or fp32.
 template <bool kF32>
 struct Part {
-    static constexpr int kLoads = kF32 ? 2 * kWords : kWords;
     static constexpr int kPer = kF32 ? 4 : 8;     // elements of a load
     static constexpr int kElement = kF32 ? 4 : 2;
     uint4 w[kLoads];
@@ -66,7 +95,7 @@ struct Part {
         return kF32 ? static_cast<const uint32_t*>(g)[i] : static_cast<const uint16_t*>(g)[i];
     }
     __device__ __forceinline__ void load(const void* g, int64_t n, int64_t first) {
-        if (first >= 0 && first + kGradUnit <= n) {
+        if (first >= 0 && first + kElements<kF32> <= n) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
                 w[j] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + at(first, j) * kElement);
@@ -155,6 +184,11 @@ struct Part {
     }
 };
 
+// The first of the units of CTA `cta`.
+__device__ __forceinline__ int range_start(int units, int cta) {
+    return static_cast<int>(static_cast<int64_t>(units) * cta / gridDim.x);
+}
+
 // The CTA's sum of x, in thread 0; every thread calls it.
 __device__ __forceinline__ double block_sum(double x, double* shared) {
 #pragma unroll
@@ -177,12 +211,18 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_norm_kernel
     grid_wait_prerequisites();
     grid_launch_dependents();
     const int units = a.end[a.count - 1];
+    int u = range_start(units, blockIdx.x);
+    const int end = range_start(units, blockIdx.x + 1);   // above u: there are no more CTAs than units
     double sum = 0.0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        int64_t first;
-        const mxfp4_grad_tensor& t = find(a, u, kF32 ? 4 : 2, &first);
-        Part<kF32> p;
-        p.load(t.g, t.n, first);
+    Walk<kF32, kCap> w(a, u);
+    Part<kF32> next;
+    next.load(w.g, w.n, w.first);
+    for (; u < end; ++u) {
+        const Part<kF32> p = next;
+        if (u + 1 < end) {
+            w.up(u + 1);
+            next.load(w.g, w.n, w.first);
+        }
         sum += p.squares();
     }
     sum = block_sum(sum, shared);
@@ -215,15 +255,22 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_scale_kerne
     grid_wait_prerequisites();
     grid_launch_dependents();
     const float factor = __ldcg(a.out + 1);
-    if (factor == 1.0f) return;
     const int units = a.end[a.count - 1];
-    for (int u = units - 1 - static_cast<int>(blockIdx.x); u >= 0; u -= gridDim.x) {
-        int64_t first;
-        const mxfp4_grad_tensor& t = find(a, u, kF32 ? 4 : 2, &first);
-        Part<kF32> p;
-        p.load(t.g, t.n, first);
+    const int start = range_start(units, blockIdx.x);
+    int u = range_start(units, blockIdx.x + 1) - 1;
+    Walk<kF32, kCap> w(a, u);
+    Part<kF32> next;
+    next.load(w.g, w.n, w.first);
+    for (; u >= start; --u) {
+        Part<kF32> p = next;
+        void* const g = w.g;
+        const int64_t n = w.n, first = w.first;
+        if (u > start) {
+            w.down(u - 1);
+            next.load(w.g, w.n, w.first);
+        }
         p.scale(factor);
-        p.store(t.g, t.n, first);
+        p.store(g, n, first);
     }
 }
 
@@ -250,13 +297,14 @@ cudaError_t launch(Kernel kernel, const Args& a, int ctas, int threads, cudaStre
 
 inline int64_t units_of(const mxfp4_grad_tensor& t, int esize) {
     const int64_t skew = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.g) & 15u) / esize;
-    return (t.n + skew + kGradUnit - 1) / kGradUnit;
+    const int64_t unit = kGradUnitBytes / esize;
+    return (t.n + skew + unit - 1) / unit;
 }
 
 // The tensors from t[j] on that one launch takes, and the index behind them; none are left: count 0.
 template <int kCap>
 int32_t fill(GradArgs<kCap>* a, int32_t count, const mxfp4_grad_tensor* t, int32_t j, int esize) {
-    int64_t units = 0;   // below 2^28: check() bounds the elements of a call
+    int64_t units = 0;   // below 2^29: check() bounds the elements of a call
     a->count = 0;
     for (; j < count && a->count < kCap; ++j) {
         if (t[j].n == 0) continue;

@@ -8,9 +8,9 @@
 
 namespace mxfp4 {
 
-constexpr int kGradUnit = 8192;        // elements of a CTA's unit of work
+constexpr int kGradUnitBytes = 16384;  // a CTA's unit of work
 constexpr int kGradThreads = 256;
-constexpr int kGradCtasPerSm = 6;
+constexpr int kGradCtasPerSm = 4;
 constexpr int kGradMaxSms = 256;
 constexpr int kGradSlots = kGradCtasPerSm * kGradMaxSms;   // partial sums of one launch
 constexpr int kGradFew = 48;           // tensors of the small launch's table,

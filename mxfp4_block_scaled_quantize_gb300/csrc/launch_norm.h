@@ -8,9 +8,14 @@
 
 namespace mxfp4 {
 
-constexpr int kNormChunks = 304;                  // CTAs that share the rows of a backward pass, at most
-constexpr int kNormSlots = 2 * kNormChunks;       // partial sums that they may leave
-constexpr int kNormWarpRowDim = 1024;             // rows of up to this many elements are one warp's
+constexpr int kNormWarpRowDim = 512;     // rows of up to this many elements are one warp's,
+constexpr int kNormThinDim = 2048;       // of up to this many a CTA's with 8 a thread, longer ones with 16
+constexpr int kNormStages = 8;           // rows that a CTA may have on their way to shared memory
+
+// CTAs that share the rows of a backward pass: as many as 152 SMs hold at a time, and the partial
+// rows that they leave at most.
+inline int norm_chunks(int64_t dim) { return dim <= 1024 ? 608 : dim <= 4096 ? 304 : 152; }
+inline int64_t norm_slots(int64_t dim) { return 2 * norm_chunks(dim); }
 
 struct NormArgs {
     const void* x;
@@ -31,6 +36,8 @@ struct NormArgs {
     float eps;
     int32_t w_f32;
     int32_t add_one;
+    int32_t stages;          // rows on their way to shared memory (its ring), where rows are copied there
+    uint32_t* err;
 };
 
 struct NormReduceArgs {

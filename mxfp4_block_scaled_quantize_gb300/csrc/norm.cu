@@ -26,7 +26,7 @@ extern "C" {
 
 mxfp4_status mxfp4_layer_norm_workspace_bytes(int64_t dim, size_t* bytes) {
     if (dim < 1 || dim > MXFP4_NORM_MAX_DIM || bytes == nullptr) return MXFP4_ERR_INVALID_ARG;
-    *bytes = 2 * static_cast<size_t>(mxfp4::kNormSlots) * static_cast<size_t>(dim) * sizeof(float);
+    *bytes = 2 * static_cast<size_t>(mxfp4::norm_slots(dim)) * static_cast<size_t>(dim) * sizeof(float);
     return MXFP4_OK;
 }
 
@@ -61,6 +61,7 @@ mxfp4_status mxfp4_layer_norm(const void* x, int64_t rows, int64_t dim, int64_t 
     a.eps = static_cast<float>(eps);
     a.w_f32 = flags & MXFP4_NORM_W_F32 ? 1 : 0;
     a.add_one = flags & MXFP4_NORM_ADD_ONE ? 1 : 0;
+    a.err = err;
     return mxfp4::launch_norm_forward(a, flags & MXFP4_NORM_X_F32, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MXFP4_OK
                : MXFP4_ERR_CUDA;
@@ -77,11 +78,11 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     if (!aligned_to(x, xe) || !aligned_to(dy, xe) || !aligned_to(dx, xe) || !aligned_to(weight, we) || !aligned_to(mean, 4) ||
         !aligned_to(rstd, 4) || !aligned_to(dw, 4) || !aligned_to(db, 4) || !aligned_to(workspace, 16))
         return MXFP4_ERR_MISALIGNED;
-    // Each CTA its rows of one sample, about as many for each as the whole has for kNormChunks CTAs.
+    // Each CTA its rows of one sample, about as many for each as the whole has for norm_chunks(dim) CTAs.
     const int64_t sample_rows = rows / samples;
-    const int64_t chunk_rows = rows > 0 ? cdiv(rows, mxfp4::kNormChunks) : 1;
+    const int64_t chunk_rows = rows > 0 ? cdiv(rows, mxfp4::norm_chunks(dim)) : 1;
     const int64_t chunks = rows > 0 ? cdiv(sample_rows, chunk_rows) : 1;
-    const int64_t ctas = samples * chunks;   // with several chunks a sample: at most rows / chunk_rows + samples, 2 kNormChunks
+    const int64_t ctas = samples * chunks;   // with several chunks a sample: at most rows / chunk_rows + samples, norm_slots(dim)
     const bool partial = chunks > 1 && (dw != nullptr || db != nullptr);
     size_t need = 0;
     if (partial && (mxfp4_layer_norm_workspace_bytes(dim, &need) != MXFP4_OK || workspace == nullptr || workspace_bytes < need))
@@ -108,7 +109,7 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     a.rstd = const_cast<float*>(rstd);
     float* const w = static_cast<float*>(workspace);
     a.partial_w = dw == nullptr ? nullptr : partial ? w : dw;
-    a.partial_b = db == nullptr ? nullptr : partial ? w + mxfp4::kNormSlots * dim : db;
+    a.partial_b = db == nullptr ? nullptr : partial ? w + mxfp4::norm_slots(dim) * dim : db;
     a.ldx = ldx;
     a.lddy = lddy;
     a.ldy = lddx;
@@ -119,6 +120,7 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     a.dim = static_cast<int32_t>(dim);
     a.w_f32 = flags & MXFP4_NORM_W_F32 ? 1 : 0;
     a.add_one = flags & MXFP4_NORM_ADD_ONE ? 1 : 0;
+    a.err = err;
     if (mxfp4::launch_norm_backward(a, flags & MXFP4_NORM_X_F32, ctas, s) != cudaSuccess) return MXFP4_ERR_CUDA;
     if (!partial) return MXFP4_OK;
     mxfp4::NormReduceArgs r;

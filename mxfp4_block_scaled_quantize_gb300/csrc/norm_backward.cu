@@ -3,88 +3,126 @@
 // With xh = (x - mu) r and a = dy g (g = w or 1 + w):
 //   dx = r (a - mean(a) - xh mean(a xh)),  dw = sum over rows of dy xh,  db = sum over rows of dy.
 //
-// One pass over X and dY: a CTA takes a range of consecutive rows of one sample (rows of up to 1024
+// One pass over X and dY: a CTA takes a range of consecutive rows of one sample (rows of up to 512
 // elements: a warp each), keeps its columns' sums of dw and db in registers across them, and
 // leaves them as one partial row; a second kernel adds the partial rows in a fixed order, so the same
-// inputs give the same bits.  A sample that is one CTA's needs no second kernel.  Bound by the
-// memory: x and dy in, dx out; the partial rows are 2 / chunk_rows of that.
+// inputs give the same bits.  A sample that is one CTA's needs no second kernel.  Rows come as in the
+// forward pass, x and dy side by side in a slot of the ring.  Bound by the memory: x and dy in, dx
+// out; the partial rows are 4 / chunk_rows of x and dy in bf16.
 #include "norm_row.cuh"
 
 namespace mxfp4 {
 namespace {
 
-template <bool kF32, bool kWide, int kGroups, bool kWarpRow, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_constant__ NormArgs a) {
+template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) uint8_t slots[];
     using Part = RowPart<kF32, kWide, kGroups>;
-    constexpr int kE = Part::kElements;
+    constexpr int kE = Part::kElements, kP = Part::kPairs;
     constexpr int kSize = kF32 ? 4 : 2;
     constexpr int kWarps = kThreads / 32;
-    __shared__ float2 shared[2][32];
-    __shared__ float sums[kWarpRow ? kWarps : 1][kWarpRow ? 32 * kE : 1];
-    const int t = kWarpRow ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
-    const int threads = kWarpRow ? 32 : static_cast<int>(blockDim.x);
+    constexpr bool kWarp = kMode == kWarpRow, kRing = kMode == kRingRow;
+    __shared__ uint64_t shared[2][32];
+    __shared__ RowRing ring;
+    __shared__ float sums[kWarp ? kWarps : 1][kWarp ? 32 * kE : 1];
+    const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
+    const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
     const int64_t sample = blockIdx.x / a.chunks;
     const int64_t in_sample = static_cast<int64_t>(blockIdx.x % a.chunks) * a.chunk_rows;
     const int64_t first = sample * a.sample_rows + in_sample;
     const int64_t end = sample * a.sample_rows + min(in_sample + a.chunk_rows, a.sample_rows);
-    const int64_t stride = kWarpRow ? kWarps : 1;
+    const int64_t stride = kWarp ? kWarps : 1;
     const float inv = 1.0f / static_cast<float>(a.dim);
+    const uint8_t *const xs = static_cast<const uint8_t*>(a.x), *const ys = static_cast<const uint8_t*>(a.dy);
+    const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize;
+    if (kRing) ring_init(ring, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
-    float g[kE], dw[kE], db[kE];
+    int issued = 0;
+    auto copy = [&](int64_t r, int slot) {   // thread 0
+        if (*static_cast<volatile int*>(&ring.abort) != 0) return;
+        ++issued;
+        const uint32_t bar = smem_addr(&ring.full[slot]), to = smem_addr(slots + 2 * slot * bytes);
+        mbar_arrive_expect_tx(bar, 2 * bytes);
+        bulk_load(to, xs + r * a.ldx * kSize, bytes, bar);
+        bulk_load(to + bytes, ys + r * a.lddy * kSize, bytes, bar);
+    };
+    if (kRing && threadIdx.x == 0)
+        for (int i = 0; i < a.stages && first + i < end; ++i) copy(first + i, i);
+    uint64_t g[kP], dw[kP], db[kP];
 #pragma unroll
-    for (int k = 0; k < kE; ++k) {
-        g[k] = 1.0f;
-        dw[k] = 0.0f;
-        db[k] = 0.0f;
+    for (int i = 0; i < kP; ++i) {
+        g[i] = both(1.0f);
+        dw[i] = 0ull;
+        db[i] = 0ull;
     }
     if (a.weight != nullptr) {
         load_vector<kWide, kGroups>(a.weight, sample * a.dim, a.w_f32, a.dim, t, threads, g);
         if (a.add_one)
 #pragma unroll
-            for (int k = 0; k < kE; ++k) g[k] += 1.0f;
+            for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
     }
-    int64_t row = first + (kWarpRow ? threadIdx.x >> 5 : 0);
+    int64_t row = first + (kWarp ? threadIdx.x >> 5 : 0);
     Part nx, ny;
     float nmean = 0.0f, nrstd = 0.0f;
     auto fetch = [&](int64_t r) {
-        nx.load(static_cast<const uint8_t*>(a.x) + r * a.ldx * kSize, a.dim, t, threads);
-        ny.load(static_cast<const uint8_t*>(a.dy) + r * a.lddy * kSize, a.dim, t, threads);
+        if (!kRing) {
+            nx.load(xs + r * a.ldx * kSize, a.dim, t, threads);
+            ny.load(ys + r * a.lddy * kSize, a.dim, t, threads);
+        }
         nmean = __ldg(a.mean + r);
         nrstd = __ldg(a.rstd + r);
     };
     if (row < end) fetch(row);
-    int turn = 0;
+    int turn = 0, slot = 0;
+    uint32_t phase = 0;
     for (; row < end; row += stride, turn ^= 1) {
-        const Part x = nx, y = ny;
+        if (kRing) {
+            ring_wait(ring, slot, phase, a.err);
+            nx.load(slots + 2 * slot * bytes, a.dim, t, threads);
+            ny.load(slots + (2 * slot + 1) * bytes, a.dim, t, threads);
+        }
         const float mean = nmean, rstd = nrstd;
+        uint64_t xh[kP], c[kP], sa = 0ull, sx = 0ull;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {   // dy is zero behind the row's end
+            const uint64_t d = ny.pair(i);
+            xh[i] = mul2(add2(nx.pair(i), both(-mean)), both(rstd));
+            c[i] = mul2(d, g[i]);
+            dw[i] = fma2(d, xh[i], dw[i]);
+            db[i] = add2(db[i], d);
+            sa = add2(sa, c[i]);
+            sx = fma2(c[i], xh[i], sx);
+        }
         if (row + stride < end) fetch(row + stride);
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < kE; ++k) {   // dy is zero behind the row's end
-            const float xh = (x.get(k) - mean) * rstd, d = y.get(k), c = d * g[k];
-            dw[k] = fmaf(d, xh, dw[k]);
-            db[k] += d;
-            sum.x += c;
-            sum.y = fmaf(c, xh, sum.y);
+        const float2 s1 = unpack2(sa), s2 = unpack2(sx);
+        const float2 sum = row_sum2<kMode, kWarps>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y)), shared[turn]);
+        if (kRing) {
+            if (threadIdx.x == 0 && row + a.stages < end) copy(row + a.stages, slot);
+            if (++slot == a.stages) {
+                slot = 0;
+                phase ^= 1u;
+            }
         }
-        sum = row_sum2<kWarpRow>(sum, shared[turn]);
-        const float m1 = sum.x * inv, m2 = sum.y * inv;
-        float out[kE];
+        const uint64_t m1 = both(-sum.x * inv), m2 = both(-sum.y * inv);
 #pragma unroll
-        for (int k = 0; k < kE; ++k) {
-            const float xh = (x.get(k) - mean) * rstd;
-            out[k] = rstd * (fmaf(-xh, m2, y.get(k) * g[k]) - m1);
-        }
-        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, out, a.dim, t, threads);
+        for (int i = 0; i < kP; ++i) c[i] = mul2(add2(fma2(xh[i], m2, c[i]), m1), both(rstd));
+        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, c, a.dim, t, threads);
     }
+    if (kRing && threadIdx.x == 0) ring_drain(ring, a.stages, issued);
     float* const to[2] = {a.partial_w, a.partial_b};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (to[i] == nullptr) continue;
         float* const out = to[i] + static_cast<int64_t>(blockIdx.x) * a.dim;
-        const float* const v = i == 0 ? dw : db;
-        if (kWarpRow) {
+        float v[kE];
+#pragma unroll
+        for (int k = 0; k < kP; ++k) {
+            const float2 f = unpack2(i == 0 ? dw[k] : db[k]);
+            v[2 * k] = f.x;
+            v[2 * k + 1] = f.y;
+        }
+        if (kWarp) {
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < kE; ++k) sums[threadIdx.x >> 5][kWide ? Part::column(k, t, 32) : k * 32 + t] = v[k];
@@ -137,34 +175,45 @@ bool wide(const NormArgs& a) {
 }
 
 template <typename Args>
-cudaError_t launch_dependent(void (*kernel)(Args), const Args& a, dim3 grid, int threads, cudaStream_t stream) {
+cudaError_t launch_dependent(void (*kernel)(Args), const Args& a, dim3 grid, int threads, int smem, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <bool kF32, bool kWide, int kGroups, bool kWarpRow, int kThreads>
-cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
-    const int threads = kWarpRow ? kThreads : ((a.dim + 8 * kGroups - 1) / (8 * kGroups) + 31) / 32 * 32;
-    return launch_dependent(norm_backward_kernel<kF32, kWide, kGroups, kWarpRow, kThreads>, a,
-                            dim3(static_cast<unsigned>(ctas), 1, 1), threads, stream);
+// kCtas: CTAs that an SM holds, by registers.
+template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
+    const auto kernel = norm_backward_kernel<kF32, kWide, kGroups, kMode, kThreads, kCtas>;
+    const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
+    // The ring: as many rows as fit beside the CTAs that share the SM.
+    constexpr int kBudget = 208 * 1024 / kCtas;
+    const int slot_bytes = 2 * a.dim * (kF32 ? 4 : 2);
+    a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStages ? kBudget / slot_bytes : kNormStages;
+    if (kMode == kRingRow) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), threads, a.stages * slot_bytes, stream);
 }
 
 template <bool kF32, bool kWide>
 cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
-    if (a.dim <= 256) return launch<kF32, kWide, 1, true, 256>(a, ctas, stream);
-    if (a.dim <= 512) return launch<kF32, kWide, 2, true, 256>(a, ctas, stream);
-    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 4, true, 256>(a, ctas, stream);
-    if (a.dim <= 4096) return launch<kF32, kWide, 2, false, 256>(a, ctas, stream);
-    if (a.dim <= 8192) return launch<kF32, kWide, 2, false, 512>(a, ctas, stream);
-    return launch<kF32, kWide, 2, false, 1024>(a, ctas, stream);
+    constexpr RowMode kLong = kWide ? kRingRow : kCtaRow;
+    if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256, 2>(a, ctas, stream);
+    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256, 2>(a, ctas, stream);
+    if (a.dim <= kNormThinDim) return launch<kF32, kWide, 1, kLong, 256, 2>(a, ctas, stream);
+    if (a.dim <= 4096) return launch<kF32, kWide, 2, kLong, 256, 2>(a, ctas, stream);
+    if (a.dim <= 8192) return launch<kF32, kWide, 2, kLong, 512, 1>(a, ctas, stream);
+    return launch<kF32, kWide, 2, kLong, 1024, 1>(a, ctas, stream);
 }
 
 }  // namespace
@@ -177,7 +226,7 @@ cudaError_t launch_norm_backward(const NormArgs& a, bool f32, int64_t ctas, cuda
 cudaError_t launch_norm_reduce(const NormReduceArgs& a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.dim + 31) / 32), static_cast<unsigned>(a.samples < 65535 ? a.samples : 65535),
                     static_cast<unsigned>(a.count));
-    return launch_dependent(norm_reduce_kernel, a, grid, 32 * kStrips, stream);
+    return launch_dependent(norm_reduce_kernel, a, grid, 32 * kStrips, 0, stream);
 }
 
 }  // namespace mxfp4

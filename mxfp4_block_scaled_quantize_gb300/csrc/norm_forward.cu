@@ -8,8 +8,10 @@
 // own rounding and the first sum's left, which counts where |mu| is far above the deviation.  All
 // of it in fp32; y is rounded once.  Bound by the memory.
 //
-// A warp takes a row of up to 1024 elements, a CTA a longer one, 16 elements a thread.  CTAs stay for
-// many rows, with the vectors in registers, and load their next row before they work on this one.
+// A warp takes a row of up to 512 elements, a CTA a longer one.  CTAs stay for many rows, with the
+// vectors in registers.  Rows whose addresses are multiples of 16 bytes come through a ring in shared
+// memory (kRingRow), which has up to 8 of them on their way whatever the registers hold; others are
+// loaded into registers one row ahead.
 #include <atomic>
 
 #include "norm_row.cuh"
@@ -17,31 +19,47 @@
 namespace mxfp4 {
 namespace {
 
-template <bool kF32, bool kWide, int kGroups, bool kWarpRow, int kThreads>
+template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float2 shared[2][32];
+    extern __shared__ __align__(16) uint8_t slots[];
+    __shared__ float sums[32];
+    __shared__ uint64_t squares[32];
+    __shared__ RowRing ring;
     using Part = RowPart<kF32, kWide, kGroups>;
-    constexpr int kE = Part::kElements;
+    constexpr int kP = Part::kPairs, kWarps = kThreads / 32;
     constexpr int kSize = kF32 ? 4 : 2;
-    const int t = kWarpRow ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
-    const int threads = kWarpRow ? 32 : static_cast<int>(blockDim.x);
-    const int64_t stride = kWarpRow ? static_cast<int64_t>(gridDim.x) * (kThreads / 32) : gridDim.x;
-    int64_t row = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    constexpr bool kWarp = kMode == kWarpRow, kRing = kMode == kRingRow;
+    const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
+    const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
+    const int64_t stride = kWarp ? static_cast<int64_t>(gridDim.x) * (kThreads / 32) : gridDim.x;
+    int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const float inv = 1.0f / static_cast<float>(a.dim);
+    const uint8_t* const xs = static_cast<const uint8_t*>(a.x);
+    const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize;
+    if (kRing) ring_init(ring, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
-    float g[kE], b[kE];
+    int issued = 0;
+    auto copy = [&](int64_t r, int slot) {   // thread 0
+        if (*static_cast<volatile int*>(&ring.abort) != 0) return;
+        ++issued;
+        mbar_arrive_expect_tx(smem_addr(&ring.full[slot]), bytes);
+        bulk_load(smem_addr(slots + slot * bytes), xs + r * a.ldx * kSize, bytes, smem_addr(&ring.full[slot]));
+    };
+    if (kRing && threadIdx.x == 0)
+        for (int i = 0; i < a.stages && row + i * stride < a.rows; ++i) copy(row + i * stride, i);
+    uint64_t g[kP], b[kP];
 #pragma unroll
-    for (int k = 0; k < kE; ++k) {
-        g[k] = 1.0f;
-        b[k] = 0.0f;
+    for (int i = 0; i < kP; ++i) {
+        g[i] = both(1.0f);
+        b[i] = 0ull;
     }
     int64_t sample = -1;
     Part next;
-    if (row < a.rows) next.load(static_cast<const uint8_t*>(a.x) + row * a.ldx * kSize, a.dim, t, threads);
+    if (!kRing && row < a.rows) next.load(xs + row * a.ldx * kSize, a.dim, t, threads);
+    int slot = 0;
+    uint32_t phase = 0;
     for (; row < a.rows; row += stride) {
-        const Part x = next;
-        if (row + stride < a.rows) next.load(static_cast<const uint8_t*>(a.x) + (row + stride) * a.ldx * kSize, a.dim, t, threads);
         const int64_t s = row < a.sample_rows ? 0 : row / a.sample_rows;
         if (s != sample) {
             sample = s;
@@ -49,35 +67,52 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
                 load_vector<kWide, kGroups>(a.weight, s * a.dim, a.w_f32, a.dim, t, threads, g);
                 if (a.add_one)
 #pragma unroll
-                    for (int k = 0; k < kE; ++k) g[k] += 1.0f;
+                    for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
             }
             if (a.bias != nullptr) load_vector<kWide, kGroups>(a.bias, s * a.dim, a.w_f32, a.dim, t, threads, b);
         }
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < kE; ++k) sum.x += x.get(k);
-        sum = row_sum2<kWarpRow>(sum, shared[0]);
-        float mean = sum.x * inv;
-        sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < kE; ++k) {
-            const float d = Part::column(k, t, threads) < a.dim ? x.get(k) - mean : 0.0f;
-            sum.x += d;
-            sum.y = fmaf(d, d, sum.y);
+        if (kRing) {
+            ring_wait(ring, slot, phase, a.err);
+            next.load(slots + slot * bytes, a.dim, t, threads);
         }
-        sum = row_sum2<kWarpRow>(sum, shared[1]);
-        const float rest = sum.x * inv;
-        mean += rest;
-        const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, sum.y * inv), 0.0f) + a.eps);
-        float y[kE];
+        uint64_t x[kP], sum = 0ull;
 #pragma unroll
-        for (int k = 0; k < kE; ++k) y[k] = fmaf((x.get(k) - mean) * rstd, g[k], b[k]);
-        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, y, a.dim, t, threads);
+        for (int i = 0; i < kP; ++i) {
+            x[i] = next.pair(i);
+            sum = add2(sum, x[i]);
+        }
+        if (!kRing && row + stride < a.rows) next.load(xs + (row + stride) * a.ldx * kSize, a.dim, t, threads);
+        const float2 halves = unpack2(sum);
+        float mean = row_sum<kMode, kWarps>(halves.x + halves.y, sums) * inv;
+        if (kRing) {
+            if (threadIdx.x == 0 && row + a.stages * stride < a.rows) copy(row + a.stages * stride, slot);
+            if (++slot == a.stages) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+        uint64_t square = 0ull;
+        sum = 0ull;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            x[i] = Part::inside(add2(x[i], both(-mean)), i, a.dim, t, threads);
+            sum = add2(sum, x[i]);
+            square = fma2(x[i], x[i], square);
+        }
+        const float2 s1 = unpack2(sum), s2 = unpack2(square);
+        const float2 total = row_sum2<kMode, kWarps>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y)), squares);
+        const float rest = total.x * inv;
+        mean += rest;
+        const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, total.y * inv), 0.0f) + a.eps);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) x[i] = fma2(mul2(add2(x[i], both(-rest)), both(rstd)), g[i], b[i]);
+        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, x, a.dim, t, threads);
         if (a.mean != nullptr && t == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
         }
     }
+    if (kRing && threadIdx.x == 0) ring_drain(ring, a.stages, issued);
 }
 
 bool wide(const NormArgs& a) {
@@ -86,18 +121,30 @@ bool wide(const NormArgs& a) {
     return (all & 15u) == 0 && a.dim % 8 == 0 && (a.rows == 1 || (a.ldx % 8 == 0 && a.ldy % 8 == 0));
 }
 
-template <bool kF32, bool kWide, int kGroups, bool kWarpRow, int kThreads>
-cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
-    const auto kernel = norm_forward_kernel<kF32, kWide, kGroups, kWarpRow, kThreads>;
-    const int threads = kWarpRow ? kThreads : ((a.dim + 8 * kGroups - 1) / (8 * kGroups) + 31) / 32 * 32;
-    const int64_t need = kWarpRow ? (a.rows + kThreads / 32 - 1) / (kThreads / 32) : a.rows;
-    static std::atomic<int> per_sm[kThreads / 32 + 1];   // resident CTAs an SM, by warps of the CTA
-    int n = per_sm[threads / 32].load(std::memory_order_relaxed);
+template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads>
+cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
+    const auto kernel = norm_forward_kernel<kF32, kWide, kGroups, kMode, kThreads>;
+    const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
+    const int64_t need = kMode == kWarpRow ? (a.rows + kThreads / 32 - 1) / (kThreads / 32) : a.rows;
+    // The ring: as many rows as fit beside the CTAs that share the SM.
+    constexpr int kBudget = kThreads <= 256 ? 48 * 1024 : 192 * 1024;
+    const int row_bytes = a.dim * (kF32 ? 4 : 2);
+    a.stages = kMode != kRingRow ? 0 : kBudget / row_bytes < kNormStages ? kBudget / row_bytes : kNormStages;
+    const int smem = a.stages * row_bytes;
+    // resident CTAs an SM, by device and warps of the CTA (with the largest ring)
+    static std::atomic<int> per_sm[64][kThreads / 32 + 1];
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>& known = per_sm[dev & 63][threads / 32];
+    n = known.load(std::memory_order_relaxed);
     if (n == 0) {
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
+        const int most = kMode == kRingRow ? kBudget : 0;
+        if (most > 0) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, most);
         if (e != cudaSuccess) return e;
         if (n < 1) n = 1;
-        per_sm[threads / 32].store(n, std::memory_order_relaxed);
+        known.store(n, std::memory_order_relaxed);
     }
     const int64_t most = static_cast<int64_t>(n) * sms;
     cudaLaunchAttribute attr[1];
@@ -106,6 +153,7 @@ cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -114,12 +162,13 @@ cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
 
 template <bool kF32, bool kWide>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
-    if (a.dim <= 256) return launch<kF32, kWide, 1, true, 256>(a, sms, stream);
-    if (a.dim <= 512) return launch<kF32, kWide, 2, true, 256>(a, sms, stream);
-    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 4, true, 256>(a, sms, stream);
-    if (a.dim <= 4096) return launch<kF32, kWide, 2, false, 256>(a, sms, stream);
-    if (a.dim <= 8192) return launch<kF32, kWide, 2, false, 512>(a, sms, stream);
-    return launch<kF32, kWide, 2, false, 1024>(a, sms, stream);
+    constexpr RowMode kLong = kWide ? kRingRow : kCtaRow;
+    if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256>(a, sms, stream);
+    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256>(a, sms, stream);
+    if (a.dim <= kNormThinDim) return launch<kF32, kWide, 1, kLong, 256>(a, sms, stream);
+    if (a.dim <= 4096) return launch<kF32, kWide, 2, kLong, 256>(a, sms, stream);
+    if (a.dim <= 8192) return launch<kF32, kWide, 2, kLong, 512>(a, sms, stream);
+    return launch<kF32, kWide, 2, kLong, 1024>(a, sms, stream);
 }
 
 }  // namespace

@@ -8,12 +8,41 @@
 
 namespace mxfp4 {
 
+// Two fp32 in one instruction each.
+__device__ __forceinline__ uint64_t pack2(float2 v) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(v.x), "f"(v.y));
+    return p;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(make_float2(v, v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // A thread's 8 kGroups elements of a row.  kWide: groups of 8 consecutive elements, one or two 16-byte
 // accesses each (pitches and dim are multiples of 8 and every address of 16 bytes); else elements
 // `threads` apart, one by one.  Threads past the row hold zeros.
 template <bool kF32, bool kWide, int kGroups>
 struct RowPart {
     static constexpr int kElements = 8 * kGroups;
+    static constexpr int kPairs = kElements / 2;
     static constexpr int kWords = kElements / (kF32 ? 1 : 2);
     uint32_t w[kWords];
 
@@ -46,79 +75,145 @@ struct RowPart {
             }
         }
     }
-    __device__ __forceinline__ float get(int k) const {
-        if (kF32) return __uint_as_float(w[k]);
-        return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+    // Elements 2i and 2i + 1.
+    __device__ __forceinline__ uint64_t pair(int i) const {
+        if (kF32) return pack2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])));
+        return pack2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
     }
-    // f[k] for the elements of the row, rounded once to its type.
-    __device__ __forceinline__ static void store(void* row, const float* f, int dim, int t, int threads) {
+    // v with zeros behind the row's end.
+    __device__ __forceinline__ static uint64_t inside(uint64_t v, int i, int dim, int t, int threads) {
+        if (kWide) return column(2 * i, t, threads) < dim ? v : 0ull;
+        float2 f = unpack2(v);
+        if (column(2 * i, t, threads) >= dim) f.x = 0.0f;
+        if (column(2 * i + 1, t, threads) >= dim) f.y = 0.0f;
+        return pack2(f);
+    }
+    // The pairs v, each element rounded once to the row's type, to the row's elements.
+    __device__ __forceinline__ static void store(void* row, const uint64_t* v, int dim, int t, int threads) {
         if (kWide) {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 const int c = (j * threads + t) * 8;
                 if (c >= dim) continue;
+                float2 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = unpack2(v[4 * j + i]);
                 if (kF32) {
                     float4* const d = reinterpret_cast<float4*>(static_cast<float*>(row) + c);
-                    d[0] = make_float4(f[8 * j], f[8 * j + 1], f[8 * j + 2], f[8 * j + 3]);
-                    d[1] = make_float4(f[8 * j + 4], f[8 * j + 5], f[8 * j + 6], f[8 * j + 7]);
+                    d[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+                    d[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
                 } else {
-                    uint32_t v[4];
+                    uint32_t h[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * j + 2 * i], f[8 * j + 2 * i + 1]);
-                        v[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
+                        h[i] = *reinterpret_cast<const uint32_t*>(&b);
                     }
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < kElements; ++k) {
-                const int c = k * threads + t;
-                if (c >= dim) continue;
-                if (kF32) static_cast<float*>(row)[c] = f[k];
-                else static_cast<__nv_bfloat16*>(row)[c] = __float2bfloat16_rn(f[k]);
+            for (int i = 0; i < kPairs; ++i) {
+                const float2 f = unpack2(v[i]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = (2 * i + h) * threads + t;
+                    if (c >= dim) continue;
+                    if (kF32) static_cast<float*>(row)[c] = h ? f.y : f.x;
+                    else static_cast<__nv_bfloat16*>(row)[c] = __float2bfloat16_rn(h ? f.y : f.x);
+                }
             }
         }
     }
 };
 
-// A thread's part of a vector of fp32 or bf16, as floats, `past` behind the row's end.
+// A thread's part of a vector of fp32 or bf16, as pairs, zero behind the row's end.
 template <bool kWide, int kGroups>
-__device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32, int dim, int t, int threads, float* f) {
+__device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32, int dim, int t, int threads, uint64_t* f) {
     if (f32) {
         RowPart<true, kWide, kGroups> p;
         p.load(static_cast<const float*>(v) + at, dim, t, threads);
 #pragma unroll
-        for (int k = 0; k < 8 * kGroups; ++k) f[k] = p.get(k);
+        for (int i = 0; i < 4 * kGroups; ++i) f[i] = p.pair(i);
     } else {
         RowPart<false, kWide, kGroups> p;
         p.load(static_cast<const uint16_t*>(v) + at, dim, t, threads);
 #pragma unroll
-        for (int k = 0; k < 8 * kGroups; ++k) f[k] = p.get(k);
+        for (int i = 0; i < 4 * kGroups; ++i) f[i] = p.pair(i);
     }
 }
 
-__device__ __forceinline__ float2 warp_sum2(float2 v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, d);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, d);
+// Threads of a CTA that has a row to itself.
+inline int row_threads(int dim, int groups) { return ((dim + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
+
+// How a kernel takes its rows: one a warp; one a CTA, straight into registers; or one a CTA, through a
+// ring of rows in shared memory that bulk copies fill ahead of it.
+enum RowMode { kWarpRow, kCtaRow, kRingRow };
+
+// The ring: `stages` slots of `bytes`, a barrier each.  Thread 0 fills a slot again once every thread has
+// its part of it in registers, which a barrier of the row's sums tells it.  A wait that runs out is
+// recorded, no slot is filled any more, and the rows go on with what the slots hold: no thread is left
+// waiting for another.
+struct RowRing {
+    uint64_t full[kNormStages];
+    int abort;
+};
+
+__device__ __forceinline__ void ring_init(RowRing& r, int stages) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(smem_addr(&r.full[i]), 1);
+        r.abort = 0;
+        fence_barrier_init();
     }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void ring_wait(RowRing& r, int slot, uint32_t phase, uint32_t* err) {
+    mbar_wait(smem_addr(&r.full[slot]), phase, err, kErrNorm, &r.abort);
+}
+
+// Thread 0, before it ends: copies that a wait gave up on may still be on their way.
+__device__ __forceinline__ void ring_drain(RowRing& r, int stages, int issued) {
+    if (*static_cast<volatile int*>(&r.abort) == 0) return;   // every copy has been waited for
+    for (int i = issued < stages ? 0 : issued - stages; i < issued; ++i)
+        mbar_wait_quiet(smem_addr(&r.full[i % stages]), (i / stages) & 1, kWaitLimitNs);
+}
+
+template <int kLanes>
+__device__ __forceinline__ uint64_t lanes_sum2(uint64_t v) {
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
     return v;
 }
 
-// Two sums over the row's threads, in all of them and in the same order in each.  A row of several
-// warps goes through `shared` ([32] of its own for each of two calls in a row: one barrier a call).
-template <bool kWarpRow>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* shared) {
-    v = warp_sum2(v);
-    if (kWarpRow) return v;
-    const int warps = blockDim.x >> 5;
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+
+// A sum (two sums) over the row's threads, in all of them and in the same order in each.  A row of several warps, of
+// kWarps at most, goes through `shared`, which two calls in a row do not share: one barrier a call.
+template <RowMode kMode, int kWarps>
+__device__ __forceinline__ float row_sum(float v, float* shared) {
+    v = lanes_sum<32>(v);
+    if (kMode == kWarpRow) return v;
     if (lane_id() == 0) shared[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = static_cast<int>(lane_id()) < warps ? shared[lane_id()] : make_float2(0.0f, 0.0f);
-    return warp_sum2(v);
+    const int i = static_cast<int>(lane_id()) & (kWarps - 1);
+    return lanes_sum<kWarps>(i < static_cast<int>(blockDim.x >> 5) ? shared[i] : 0.0f);
+}
+
+template <RowMode kMode, int kWarps>
+__device__ __forceinline__ float2 row_sum2(uint64_t v, uint64_t* shared) {
+    v = lanes_sum2<32>(v);
+    if (kMode == kWarpRow) return unpack2(v);
+    if (lane_id() == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int i = static_cast<int>(lane_id()) & (kWarps - 1);
+    return unpack2(lanes_sum2<kWarps>(i < static_cast<int>(blockDim.x >> 5) ? shared[i] : 0ull));
 }
 
 }  // namespace mxfp4

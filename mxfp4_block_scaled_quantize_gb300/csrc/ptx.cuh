@@ -23,8 +23,9 @@ enum : uint32_t {
     kErrSelftest = 1u << 6,
     kErrNonFinite = 1u << 7,   // not a wait: a tensorwise FP8 amax was NaN or inf
     kErrGroups = 1u << 8,      // not a wait: group offsets or a row index out of range
+    kErrNorm = 1u << 9,
 };
-constexpr uint32_t kErrWaitBits = kErrNonFinite - 1;
+constexpr uint32_t kErrWaitBits = (kErrNonFinite - 1) | kErrNorm;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
