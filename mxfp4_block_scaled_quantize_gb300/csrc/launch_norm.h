@@ -8,14 +8,16 @@
 
 namespace mxfp4 {
 
-constexpr int kNormWarpRowDim = 512;     // rows of up to this many elements are one warp's,
-constexpr int kNormThinDim = 2048;       // of up to this many a CTA's with 8 a thread, longer ones with 16
+constexpr int kNormWarpRowDim = 512;     // rows of up to this many elements are one warp's, longer ones a CTA's
 constexpr int kNormStages = 8;           // rows that a CTA may have on their way to shared memory
 
-// CTAs that share the rows of a backward pass: as many as 152 SMs hold at a time, and the partial
-// rows that they leave at most.
-inline int norm_chunks(int64_t dim) { return dim <= 1024 ? 608 : dim <= 4096 ? 304 : 152; }
+// CTAs that share the rows of a backward pass, each of which leaves a partial row of dw and db: as many as
+// 152 SMs hold at a time, 512 threads each.
+inline int norm_chunks(int64_t dim) {
+    return dim <= kNormWarpRowDim ? 608 : dim <= 1024 ? 1216 : dim <= 2048 ? 608 : dim <= 4096 ? 304 : 152;
+}
 inline int64_t norm_slots(int64_t dim) { return 2 * norm_chunks(dim); }
+constexpr int64_t kNormLeastRows = 4;    // of a CTA, where there are few: a partial row costs as much as two rows of x
 
 struct NormArgs {
     const void* x;

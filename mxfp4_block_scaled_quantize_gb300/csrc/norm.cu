@@ -80,7 +80,8 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
         return MXFP4_ERR_MISALIGNED;
     // Each CTA its rows of one sample, about as many for each as the whole has for norm_chunks(dim) CTAs.
     const int64_t sample_rows = rows / samples;
-    const int64_t chunk_rows = rows > 0 ? cdiv(rows, mxfp4::norm_chunks(dim)) : 1;
+    const int64_t even = cdiv(rows, mxfp4::norm_chunks(dim));
+    const int64_t chunk_rows = even > mxfp4::kNormLeastRows ? even : mxfp4::kNormLeastRows;
     const int64_t chunks = rows > 0 ? cdiv(sample_rows, chunk_rows) : 1;
     const int64_t ctas = samples * chunks;   // with several chunks a sample: at most rows / chunk_rows + samples, norm_slots(dim)
     const bool partial = chunks > 1 && (dw != nullptr || db != nullptr);

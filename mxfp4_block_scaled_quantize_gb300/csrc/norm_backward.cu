@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     const int64_t stride = kWarp ? kWarps : 1;
     const float inv = 1.0f / static_cast<float>(a.dim);
     const uint8_t *const xs = static_cast<const uint8_t*>(a.x), *const ys = static_cast<const uint8_t*>(a.dy);
-    const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize;
+    const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize, part_bytes = ring_bytes<kWide>(bytes);
     if (kRing) ring_init(ring, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
@@ -42,10 +42,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     auto copy = [&](int64_t r, int slot) {   // thread 0
         if (*static_cast<volatile int*>(&ring.abort) != 0) return;
         ++issued;
-        const uint32_t bar = smem_addr(&ring.full[slot]), to = smem_addr(slots + 2 * slot * bytes);
-        mbar_arrive_expect_tx(bar, 2 * bytes);
-        bulk_load(to, xs + r * a.ldx * kSize, bytes, bar);
-        bulk_load(to + bytes, ys + r * a.lddy * kSize, bytes, bar);
+        const uint32_t bar = smem_addr(&ring.full[slot]), to = smem_addr(slots + 2 * slot * part_bytes);
+        if (ring_edge<kWide>(r, a.rows)) {
+            mbar_arrive(bar);
+            return;
+        }
+        const uint8_t *const x = xs + r * a.ldx * kSize, *const y = ys + r * a.lddy * kSize;
+        mbar_arrive_expect_tx(bar, ring_moved<kWide>(x, bytes) + ring_moved<kWide>(y, bytes));
+        ring_copy<kWide>(to, x, bytes, bar);
+        ring_copy<kWide>(to + part_bytes, y, bytes, bar);
     };
     if (kRing && threadIdx.x == 0)
         for (int i = 0; i < a.stages && first + i < end; ++i) copy(first + i, i);
@@ -79,8 +84,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     for (; row < end; row += stride, turn ^= 1) {
         if (kRing) {
             ring_wait(ring, slot, phase, a.err);
-            nx.load(slots + 2 * slot * bytes, a.dim, t, threads);
-            ny.load(slots + (2 * slot + 1) * bytes, a.dim, t, threads);
+            const uint8_t *const x = xs + row * a.ldx * kSize, *const y = ys + row * a.lddy * kSize;
+            if (ring_edge<kWide>(row, a.rows)) {
+                nx.load(x, a.dim, t, threads);
+                ny.load(y, a.dim, t, threads);
+            } else {
+                nx.load(slots + 2 * slot * part_bytes + ring_skew<kWide>(x), a.dim, t, threads);
+                ny.load(slots + (2 * slot + 1) * part_bytes + ring_skew<kWide>(y), a.dim, t, threads);
+            }
         }
         const float mean = nmean, rstd = nrstd;
         uint64_t xh[kP], c[kP], sa = 0ull, sx = 0ull;
@@ -143,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     }
 }
 
-// Sums of the partial rows: 32 columns of one sample a CTA, 8 strips of its partial rows.
-constexpr int kStrips = 8;
+// Sums of the partial rows: 32 columns of one sample a CTA, 32 strips of its partial rows.
+constexpr int kStrips = 32;
 __global__ void __launch_bounds__(32 * kStrips) norm_reduce_kernel(const __grid_constant__ NormReduceArgs a) {
     __shared__ float sums[kStrips][33];
     grid_wait_prerequisites();
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(32 * kStrips) norm_reduce_kernel(const __grid_
         const float* const p = a.partial[blockIdx.z] + s * a.chunks * a.dim;
         float v = 0.0f;
         if (c < a.dim)
-#pragma unroll 8
+#pragma unroll 10
             for (int i = strip; i < a.chunks; i += kStrips) v += __ldcg(p + static_cast<int64_t>(i) * a.dim + c);
         __syncthreads();
         sums[strip][lane] = v;
@@ -196,7 +207,7 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
     const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
     // The ring: as many rows as fit beside the CTAs that share the SM.
     constexpr int kBudget = 208 * 1024 / kCtas;
-    const int slot_bytes = 2 * a.dim * (kF32 ? 4 : 2);
+    const int slot_bytes = 2 * static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStages ? kBudget / slot_bytes : kNormStages;
     if (kMode == kRingRow) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
@@ -207,13 +218,13 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
 
 template <bool kF32, bool kWide>
 cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
-    constexpr RowMode kLong = kWide ? kRingRow : kCtaRow;
     if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256, 2>(a, ctas, stream);
     if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256, 2>(a, ctas, stream);
-    if (a.dim <= kNormThinDim) return launch<kF32, kWide, 1, kLong, 256, 2>(a, ctas, stream);
-    if (a.dim <= 4096) return launch<kF32, kWide, 2, kLong, 256, 2>(a, ctas, stream);
-    if (a.dim <= 8192) return launch<kF32, kWide, 2, kLong, 512, 1>(a, ctas, stream);
-    return launch<kF32, kWide, 2, kLong, 1024, 1>(a, ctas, stream);
+    if (a.dim <= 1024) return launch<kF32, kWide, 2, kRingRow, 64, 8>(a, ctas, stream);
+    if (a.dim <= 2048) return launch<kF32, kWide, 2, kRingRow, 128, 4>(a, ctas, stream);
+    if (a.dim <= 4096) return launch<kF32, kWide, 2, kRingRow, 256, 2>(a, ctas, stream);
+    if (a.dim <= 8192) return launch<kF32, kWide, 2, kRingRow, 512, 1>(a, ctas, stream);
+    return launch<kF32, kWide, 2, kRingRow, 1024, 1>(a, ctas, stream);
 }
 
 }  // namespace

@@ -3,15 +3,15 @@
 //   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r g + b, g = w or 1 + w,
 //   with w and b for the whole of X, for each sample of it (consecutive rows), or not at all.
 //
-// A row is read once and stays in registers: the sum, then the sum of the squares of the centred
-// values.  The sum of the centred values themselves goes with them and corrects the mean by what its
-// own rounding and the first sum's left, which counts where |mu| is far above the deviation.  All
-// of it in fp32; y is rounded once.  Bound by the memory.
+// A row is read once and stays in registers, and its threads meet once.  Each warp centres its part at the mean m_w that
+// it finds for it, and gives m_w, the rest r_w = sum(x - m_w) that m_w's rounding left, and
+// sum((x - m_w)^2) - r_w^2 / n_w; with d_w = m_w - m_0 + r_w / n_w the row's mean is m_0 + D, D = sum(n_w d_w) / n, and its
+// squares are the warps' and n_w (d_w - D)^2.  So nothing is lost where |mu| is far above the deviation.  All of it in
+// fp32; y is rounded once.  Bound by the memory, and by instructions not far below it.
 //
 // A warp takes a row of up to 512 elements, a CTA a longer one.  CTAs stay for many rows, with the
-// vectors in registers.  Rows whose addresses are multiples of 16 bytes come through a ring in shared
-// memory (kRingRow), which has up to 8 of them on their way whatever the registers hold; others are
-// loaded into registers one row ahead.
+// vectors in registers.  A CTA's rows come through a ring in shared memory, which has up to 8 of them on
+// their way whatever the registers hold; a warp's are loaded into registers one row ahead.
 #include <atomic>
 
 #include "norm_row.cuh"
@@ -22,8 +22,7 @@ namespace {
 template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) uint8_t slots[];
-    __shared__ float sums[32];
-    __shared__ uint64_t squares[32];
+    __shared__ float4 parts[2][32];   // of a row's warps: m, r, squares
     __shared__ RowRing ring;
     using Part = RowPart<kF32, kWide, kGroups>;
     constexpr int kP = Part::kPairs, kWarps = kThreads / 32;
@@ -35,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
     int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const float inv = 1.0f / static_cast<float>(a.dim);
     const uint8_t* const xs = static_cast<const uint8_t*>(a.x);
-    const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize;
+    const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize, slot_bytes = ring_bytes<kWide>(bytes);
     if (kRing) ring_init(ring, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
@@ -43,8 +42,14 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
     auto copy = [&](int64_t r, int slot) {   // thread 0
         if (*static_cast<volatile int*>(&ring.abort) != 0) return;
         ++issued;
-        mbar_arrive_expect_tx(smem_addr(&ring.full[slot]), bytes);
-        bulk_load(smem_addr(slots + slot * bytes), xs + r * a.ldx * kSize, bytes, smem_addr(&ring.full[slot]));
+        const uint32_t bar = smem_addr(&ring.full[slot]);
+        if (ring_edge<kWide>(r, a.rows)) {
+            mbar_arrive(bar);
+            return;
+        }
+        const uint8_t* const from = xs + r * a.ldx * kSize;
+        mbar_arrive_expect_tx(bar, ring_moved<kWide>(from, bytes));
+        ring_copy<kWide>(smem_addr(slots + slot * slot_bytes), from, bytes, bar);
     };
     if (kRing && threadIdx.x == 0)
         for (int i = 0; i < a.stages && row + i * stride < a.rows; ++i) copy(row + i * stride, i);
@@ -54,6 +59,23 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
         g[i] = both(1.0f);
         b[i] = 0ull;
     }
+    // elements of this warp, and of the warp that this lane stands for when the warps' parts are joined
+    auto elements = [&](int warp) {
+        constexpr int kStep = kWide ? 8 : 1;   // columns of a lane's group
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < 2 * kP; k += kStep)
+            n += min(max(a.dim - Part::column(k, kWarp ? 0 : 32 * warp, threads), 0), 32 * kStep);
+        return n;
+    };
+    const int joined = kWarp ? 0 : static_cast<int>(lane_id()) & (kWarps - 1);
+    float n_joined = 0.0f, inv_joined = 0.0f;
+    if (joined < (kWarp ? 1 : static_cast<int>(blockDim.x >> 5))) {
+        n_joined = static_cast<float>(elements(joined));
+        inv_joined = n_joined > 0.0f ? 1.0f / n_joined : 0.0f;
+    }
+    const float inv_own = kWarp ? inv_joined : __shfl_sync(0xFFFFFFFFu, inv_joined, threadIdx.x >> 5);
+    int turn = 0;
     int64_t sample = -1;
     Part next;
     if (!kRing && row < a.rows) next.load(xs + row * a.ldx * kSize, a.dim, t, threads);
@@ -73,7 +95,9 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
         }
         if (kRing) {
             ring_wait(ring, slot, phase, a.err);
-            next.load(slots + slot * bytes, a.dim, t, threads);
+            const uint8_t* const from = xs + row * a.ldx * kSize;
+            if (ring_edge<kWide>(row, a.rows)) next.load(from, a.dim, t, threads);
+            else next.load(slots + slot * slot_bytes + ring_skew<kWide>(from), a.dim, t, threads);
         }
         uint64_t x[kP], sum = 0ull;
 #pragma unroll
@@ -83,29 +107,44 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
         }
         if (!kRing && row + stride < a.rows) next.load(xs + (row + stride) * a.ldx * kSize, a.dim, t, threads);
         const float2 halves = unpack2(sum);
-        float mean = row_sum<kMode, kWarps>(halves.x + halves.y, sums) * inv;
-        if (kRing) {
-            if (threadIdx.x == 0 && row + a.stages * stride < a.rows) copy(row + a.stages * stride, slot);
-            if (++slot == a.stages) {
-                slot = 0;
-                phase ^= 1u;
-            }
-        }
+        float mean = lanes_sum<32>(halves.x + halves.y) * inv_own;
         uint64_t square = 0ull;
         sum = 0ull;
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            x[i] = Part::inside(add2(x[i], both(-mean)), i, a.dim, t, threads);
+            x[i] = add2(x[i], Part::inside(-mean, i, a.dim, t, threads));
             sum = add2(sum, x[i]);
             square = fma2(x[i], x[i], square);
         }
         const float2 s1 = unpack2(sum), s2 = unpack2(square);
-        const float2 total = row_sum2<kMode, kWarps>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y)), squares);
-        const float rest = total.x * inv;
-        mean += rest;
-        const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, total.y * inv), 0.0f) + a.eps);
+        const float2 own = unpack2(lanes_sum2<32>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y))));
+        float shift, var;   // the row's mean less this warp's, and its variance
+        if (kWarp) {
+            shift = own.x * inv_own;
+            var = fmaf(-shift, shift, own.y * inv_own);
+        } else {
+            if (lane_id() == 0) parts[turn][threadIdx.x >> 5] = make_float4(mean, own.x, own.y, 0.0f);
+            __syncthreads();
+            if (kRing) {
+                if (threadIdx.x == 0 && row + a.stages * stride < a.rows) copy(row + a.stages * stride, slot);
+                if (++slot == a.stages) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+            const float first = parts[turn][0].x;
+            const float4 p = n_joined > 0.0f ? parts[turn][joined] : make_float4(first, 0.0f, 0.0f, 0.0f);
+            turn ^= 1;
+            const float rest = p.y * inv_joined, d = (p.x - first) + rest;
+            const float all = lanes_sum<kWarps>(n_joined * d) * inv, off = d - all;
+            var = lanes_sum<kWarps>(fmaf(n_joined * off, off, fmaf(-rest, p.y, p.z))) * inv;
+            shift = all - (mean - first);
+        }
+        mean += shift;
+        const float rstd = rsqrtf(fmaxf(var, 0.0f) + a.eps);
+        const uint64_t by = both(rstd), less = both(-shift * rstd);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) x[i] = fma2(mul2(add2(x[i], both(-rest)), both(rstd)), g[i], b[i]);
+        for (int i = 0; i < kP; ++i) x[i] = fma2(fma2(x[i], by, less), g[i], b[i]);
         Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, x, a.dim, t, threads);
         if (a.mean != nullptr && t == 0) {
             a.mean[row] = mean;
@@ -127,8 +166,8 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
     const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
     const int64_t need = kMode == kWarpRow ? (a.rows + kThreads / 32 - 1) / (kThreads / 32) : a.rows;
     // The ring: as many rows as fit beside the CTAs that share the SM.
-    constexpr int kBudget = kThreads <= 256 ? 48 * 1024 : 192 * 1024;
-    const int row_bytes = a.dim * (kF32 ? 4 : 2);
+    constexpr int kBudget = kThreads <= 128 ? 44 * 1024 : kThreads <= 256 ? 96 * 1024 : 192 * 1024;
+    const int row_bytes = static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / row_bytes < kNormStages ? kBudget / row_bytes : kNormStages;
     const int smem = a.stages * row_bytes;
     // resident CTAs an SM, by device and warps of the CTA (with the largest ring)
@@ -162,13 +201,13 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
 
 template <bool kF32, bool kWide>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
-    constexpr RowMode kLong = kWide ? kRingRow : kCtaRow;
     if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256>(a, sms, stream);
     if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256>(a, sms, stream);
-    if (a.dim <= kNormThinDim) return launch<kF32, kWide, 1, kLong, 256>(a, sms, stream);
-    if (a.dim <= 4096) return launch<kF32, kWide, 2, kLong, 256>(a, sms, stream);
-    if (a.dim <= 8192) return launch<kF32, kWide, 2, kLong, 512>(a, sms, stream);
-    return launch<kF32, kWide, 2, kLong, 1024>(a, sms, stream);
+    if (a.dim <= 1024) return launch<kF32, kWide, 1, kRingRow, 128>(a, sms, stream);
+    if (a.dim <= 2048) return launch<kF32, kWide, 2, kRingRow, 128>(a, sms, stream);
+    if (a.dim <= 4096) return launch<kF32, kWide, 4, kRingRow, 128>(a, sms, stream);
+    if (a.dim <= 8192) return launch<kF32, kWide, 4, kRingRow, 256>(a, sms, stream);
+    return launch<kF32, kWide, 4, kRingRow, 512>(a, sms, stream);
 }
 
 }  // namespace

@@ -80,13 +80,10 @@ struct RowPart {
         if (kF32) return pack2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])));
         return pack2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
     }
-    // v with zeros behind the row's end.
-    __device__ __forceinline__ static uint64_t inside(uint64_t v, int i, int dim, int t, int threads) {
-        if (kWide) return column(2 * i, t, threads) < dim ? v : 0ull;
-        float2 f = unpack2(v);
-        if (column(2 * i, t, threads) >= dim) f.x = 0.0f;
-        if (column(2 * i + 1, t, threads) >= dim) f.y = 0.0f;
-        return pack2(f);
+    // v, with zeros behind the row's end: for all elements of a wide group the same.
+    __device__ __forceinline__ static uint64_t inside(float v, int i, int dim, int t, int threads) {
+        if (kWide) return both(column(2 * i, t, threads) < dim ? v : 0.0f);
+        return pack2(make_float2(column(2 * i, t, threads) < dim ? v : 0.0f, column(2 * i + 1, t, threads) < dim ? v : 0.0f));
     }
     // The pairs v, each element rounded once to the row's type, to the row's elements.
     __device__ __forceinline__ static void store(void* row, const uint64_t* v, int dim, int t, int threads) {
@@ -147,11 +144,11 @@ __device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32,
 // Threads of a CTA that has a row to itself.
 inline int row_threads(int dim, int groups) { return ((dim + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
 
-// How a kernel takes its rows: one a warp; one a CTA, straight into registers; or one a CTA, through a
+// How a kernel takes its rows: one a warp, straight into registers; or one a CTA, through a
 // ring of rows in shared memory that bulk copies fill ahead of it.
-enum RowMode { kWarpRow, kCtaRow, kRingRow };
+enum RowMode { kWarpRow, kRingRow };
 
-// The ring: `stages` slots of `bytes`, a barrier each.  Thread 0 fills a slot again once every thread has
+// The ring: `stages` slots of a row's bytes, a barrier each.  Thread 0 fills a slot again once every thread has
 // its part of it in registers, which a barrier of the row's sums tells it.  A wait that runs out is
 // recorded, no slot is filled any more, and the rows go on with what the slots hold: no thread is left
 // waiting for another.
@@ -159,6 +156,36 @@ struct RowRing {
     uint64_t full[kNormStages];
     int abort;
 };
+
+// How a row lies in its slot.  Bulk copies move whole 16 bytes: a row that does not start or end at a
+// multiple of 16 comes with what lies around it in its 16 bytes, which belongs to the rows beside it; the first and the
+// last row have no such neighbour, and are loaded directly (`edge`).
+template <bool kWide>
+__device__ __forceinline__ bool ring_edge(int64_t row, int64_t rows) {
+    return !kWide && (row == 0 || row == rows - 1);
+}
+
+// Bytes of a slot's row of `bytes`.
+template <bool kWide>
+__host__ __device__ __forceinline__ uint32_t ring_bytes(uint32_t bytes) {
+    return kWide ? bytes : ((bytes + 15u) & ~15u) + 16u;
+}
+
+template <bool kWide>
+__device__ __forceinline__ uint32_t ring_skew(const uint8_t* row) {
+    return kWide ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u;
+}
+
+// Bytes that the copy of a row of `bytes` moves, and the copy.
+template <bool kWide>
+__device__ __forceinline__ uint32_t ring_moved(const uint8_t* row, uint32_t bytes) {
+    return kWide ? bytes : (ring_skew<kWide>(row) + bytes + 15u) & ~15u;
+}
+
+template <bool kWide>
+__device__ __forceinline__ void ring_copy(uint32_t to, const uint8_t* row, uint32_t bytes, uint32_t bar) {
+    bulk_load(to, row - ring_skew<kWide>(row), ring_moved<kWide>(row, bytes), bar);
+}
 
 __device__ __forceinline__ void ring_init(RowRing& r, int stages) {
     if (threadIdx.x == 0) {

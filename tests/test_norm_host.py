@@ -67,7 +67,7 @@ def test_partial_rows_fit_the_workspace():
     for samples in list(range(1, 320)) + [600, 1000]:
         for each in list(range(1, 40)) + [303, 304, 305, 1000, 4097]:
             rows = samples * each
-            chunk = -(-rows // 304)
+            chunk = max(-(-rows // 608), 4)
             chunks = -(-each // chunk)
             assert chunks == 1 or samples * chunks <= slots
 
