@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     __shared__ float sums[kWarp ? kWarps : 1][kWarp ? 32 * kE : 1];
     const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
     const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
+    const RowShape shape{a.dim, t, threads};
     const int64_t sample = blockIdx.x / a.chunks;
     const int64_t in_sample = static_cast<int64_t>(blockIdx.x % a.chunks) * a.chunk_rows;
     const int64_t first = sample * a.sample_rows + in_sample;
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         db[i] = 0ull;
     }
     if (a.weight != nullptr) {
-        load_vector<kWide, kGroups>(a.weight, sample * a.dim, a.w_f32, a.dim, t, threads, g);
+        load_vector<kF32, kWide, kGroups>(a.weight, sample * a.dim, a.w_f32, shape, g);
         if (a.add_one)
 #pragma unroll
             for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
@@ -72,8 +73,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     float nmean = 0.0f, nrstd = 0.0f;
     auto fetch = [&](int64_t r) {
         if (!kRing) {
-            nx.load(xs + r * a.ldx * kSize, a.dim, t, threads);
-            ny.load(ys + r * a.lddy * kSize, a.dim, t, threads);
+            nx.load(xs + r * a.ldx * kSize, shape);
+            ny.load(ys + r * a.lddy * kSize, shape);
         }
         nmean = __ldg(a.mean + r);
         nrstd = __ldg(a.rstd + r);
@@ -86,11 +87,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
             ring_wait(ring, slot, phase, a.err);
             const uint8_t *const x = xs + row * a.ldx * kSize, *const y = ys + row * a.lddy * kSize;
             if (ring_edge<kWide>(row, a.rows)) {
-                nx.load(x, a.dim, t, threads);
-                ny.load(y, a.dim, t, threads);
+                nx.load(x, shape);
+                ny.load(y, shape);
             } else {
-                nx.load(slots + 2 * slot * part_bytes + ring_skew<kWide>(x), a.dim, t, threads);
-                ny.load(slots + (2 * slot + 1) * part_bytes + ring_skew<kWide>(y), a.dim, t, threads);
+                nx.template load<true>(slots + 2 * slot * part_bytes + ring_skew<kWide>(x), shape);
+                ny.template load<true>(slots + (2 * slot + 1) * part_bytes + ring_skew<kWide>(y), shape);
             }
         }
         const float mean = nmean, rstd = nrstd;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         const uint64_t m1 = both(-sum.x * inv), m2 = both(-sum.y * inv);
 #pragma unroll
         for (int i = 0; i < kP; ++i) c[i] = mul2(add2(fma2(xh[i], m2, c[i]), m1), both(rstd));
-        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, c, a.dim, t, threads);
+        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, c, shape);
     }
     if (kRing && threadIdx.x == 0) ring_drain(ring, a.stages, issued);
     float* const to[2] = {a.partial_w, a.partial_b};
@@ -126,17 +127,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     for (int i = 0; i < 2; ++i) {
         if (to[i] == nullptr) continue;
         float* const out = to[i] + static_cast<int64_t>(blockIdx.x) * a.dim;
-        float v[kE];
-#pragma unroll
-        for (int k = 0; k < kP; ++k) {
-            const float2 f = unpack2(i == 0 ? dw[k] : db[k]);
-            v[2 * k] = f.x;
-            v[2 * k + 1] = f.y;
-        }
+        const uint64_t* const v = i == 0 ? dw : db;
         if (kWarp) {
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < kE; ++k) sums[threadIdx.x >> 5][kWide ? Part::column(k, t, 32) : k * 32 + t] = v[k];
+            for (int k = 0; k < kP; ++k) {
+                const float2 f = unpack2(v[k]);
+                sums[threadIdx.x >> 5][Part::column(2 * k, shape)] = f.x;
+                sums[threadIdx.x >> 5][Part::column(2 * k + 1, shape)] = f.y;
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < a.dim; c += kThreads) {
                 float s = 0.0f;
@@ -144,11 +143,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
                 for (int w = 0; w < kWarps; ++w) s += sums[w][c];
                 out[c] = s;
             }
+        } else if (kWide && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+            RowPart<true, true, kGroups>::store(out, v, shape);
         } else {
 #pragma unroll
-            for (int k = 0; k < kE; ++k) {
-                const int c = Part::column(k, t, threads);
-                if (c < a.dim) out[c] = v[k];
+            for (int k = 0; k < kP; ++k) {
+                const float2 f = unpack2(v[k]);
+                if (Part::inside(2 * k, shape)) out[Part::column(2 * k, shape)] = f.x;
+                if (Part::inside(2 * k + 1, shape)) out[Part::column(2 * k + 1, shape)] = f.y;
             }
         }
     }

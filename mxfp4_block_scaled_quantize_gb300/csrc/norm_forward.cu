@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
     constexpr bool kWarp = kMode == kWarpRow, kRing = kMode == kRingRow;
     const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
     const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
+    const RowShape shape{a.dim, t, threads};
     const int64_t stride = kWarp ? static_cast<int64_t>(gridDim.x) * (kThreads / 32) : gridDim.x;
     int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const float inv = 1.0f / static_cast<float>(a.dim);
@@ -61,11 +62,11 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
     }
     // elements of this warp, and of the warp that this lane stands for when the warps' parts are joined
     auto elements = [&](int warp) {
-        constexpr int kStep = kWide ? 8 : 1;   // columns of a lane's group
+        const RowShape first{a.dim, kWarp ? 0 : 32 * warp, threads};
         int n = 0;
 #pragma unroll
-        for (int k = 0; k < 2 * kP; k += kStep)
-            n += min(max(a.dim - Part::column(k, kWarp ? 0 : 32 * warp, threads), 0), 32 * kStep);
+        for (int k = 0; k < 2 * kP; k += Part::kTurn)
+            n += min(max(a.dim - Part::column(k, first), 0), 32 * Part::kTurn);
         return n;
     };
     const int joined = kWarp ? 0 : static_cast<int>(lane_id()) & (kWarps - 1);
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
     int turn = 0;
     int64_t sample = -1;
     Part next;
-    if (!kRing && row < a.rows) next.load(xs + row * a.ldx * kSize, a.dim, t, threads);
+    if (!kRing && row < a.rows) next.load(xs + row * a.ldx * kSize, shape);
     int slot = 0;
     uint32_t phase = 0;
     for (; row < a.rows; row += stride) {
@@ -86,18 +87,18 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
         if (s != sample) {
             sample = s;
             if (a.weight != nullptr) {
-                load_vector<kWide, kGroups>(a.weight, s * a.dim, a.w_f32, a.dim, t, threads, g);
+                load_vector<kF32, kWide, kGroups>(a.weight, s * a.dim, a.w_f32, shape, g);
                 if (a.add_one)
 #pragma unroll
                     for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
             }
-            if (a.bias != nullptr) load_vector<kWide, kGroups>(a.bias, s * a.dim, a.w_f32, a.dim, t, threads, b);
+            if (a.bias != nullptr) load_vector<kF32, kWide, kGroups>(a.bias, s * a.dim, a.w_f32, shape, b);
         }
         if (kRing) {
             ring_wait(ring, slot, phase, a.err);
             const uint8_t* const from = xs + row * a.ldx * kSize;
-            if (ring_edge<kWide>(row, a.rows)) next.load(from, a.dim, t, threads);
-            else next.load(slots + slot * slot_bytes + ring_skew<kWide>(from), a.dim, t, threads);
+            if (ring_edge<kWide>(row, a.rows)) next.load(from, shape);
+            else next.template load<true>(slots + slot * slot_bytes + ring_skew<kWide>(from), shape);
         }
         uint64_t x[kP], sum = 0ull;
 #pragma unroll
@@ -105,14 +106,14 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
             x[i] = next.pair(i);
             sum = add2(sum, x[i]);
         }
-        if (!kRing && row + stride < a.rows) next.load(xs + (row + stride) * a.ldx * kSize, a.dim, t, threads);
+        if (!kRing && row + stride < a.rows) next.load(xs + (row + stride) * a.ldx * kSize, shape);
         const float2 halves = unpack2(sum);
         float mean = lanes_sum<32>(halves.x + halves.y) * inv_own;
         uint64_t square = 0ull;
         sum = 0ull;
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            x[i] = add2(x[i], Part::inside(-mean, i, a.dim, t, threads));
+            x[i] = add2(x[i], Part::within(-mean, i, shape));
             sum = add2(sum, x[i]);
             square = fma2(x[i], x[i], square);
         }
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_con
         const uint64_t by = both(rstd), less = both(-shift * rstd);
 #pragma unroll
         for (int i = 0; i < kP; ++i) x[i] = fma2(fma2(x[i], by, less), g[i], b[i]);
-        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, x, a.dim, t, threads);
+        Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, x, shape);
         if (a.mean != nullptr && t == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
@@ -199,15 +200,23 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// Elements a thread: 32 where rows come in 16-byte accesses, for the join of a row's warps costs each warp as much as
+// some 16 elements (8 a thread: 2.9 TB/s at 1024 elements, 16: 3.6 TB/s at 2048 and 4.4 at 4096, 32: 5.2 at 4096 and
+// 6.2 at 8192); 16 where they do not, which the registers of the single accesses' addresses fill.
 template <bool kF32, bool kWide>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
     if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256>(a, sms, stream);
     if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256>(a, sms, stream);
-    if (a.dim <= 1024) return launch<kF32, kWide, 1, kRingRow, 128>(a, sms, stream);
-    if (a.dim <= 2048) return launch<kF32, kWide, 2, kRingRow, 128>(a, sms, stream);
-    if (a.dim <= 4096) return launch<kF32, kWide, 4, kRingRow, 128>(a, sms, stream);
-    if (a.dim <= 8192) return launch<kF32, kWide, 4, kRingRow, 256>(a, sms, stream);
-    return launch<kF32, kWide, 4, kRingRow, 512>(a, sms, stream);
+    if (kWide) {
+        if (a.dim <= 1024) return launch<kF32, true, 4, kWarpRow, 128>(a, sms, stream);
+        if (a.dim <= 4096) return launch<kF32, true, 4, kRingRow, 128>(a, sms, stream);
+        if (a.dim <= 8192) return launch<kF32, true, 4, kRingRow, 256>(a, sms, stream);
+        return launch<kF32, true, 4, kRingRow, 512>(a, sms, stream);
+    }
+    if (a.dim <= 2048) return launch<kF32, false, 2, kRingRow, 128>(a, sms, stream);
+    if (a.dim <= 4096) return launch<kF32, false, 2, kRingRow, 256>(a, sms, stream);
+    if (a.dim <= 8192) return launch<kF32, false, 2, kRingRow, 512>(a, sms, stream);
+    return launch<kF32, false, 2, kRingRow, 1024>(a, sms, stream);
 }
 
 }  // namespace

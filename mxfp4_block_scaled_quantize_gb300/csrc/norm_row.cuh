@@ -36,42 +36,67 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
+// A row, and a thread's place in it.
+struct RowShape {
+    int dim, t, threads;
+};
+
 // A thread's 8 kGroups elements of a row.  kWide: groups of 8 consecutive elements, one or two 16-byte
-// accesses each (pitches and dim are multiples of 8 and every address of 16 bytes); else elements
-// `threads` apart, one by one.  Threads past the row hold zeros.
+// accesses each (pitches and dim are multiples of 8 and every address of 16 bytes); else pairs of bf16, in one
+// access where the row starts at a multiple of 4 bytes, or single fp32.  Threads past the row hold zeros.
 template <bool kF32, bool kWide, int kGroups>
 struct RowPart {
     static constexpr int kElements = 8 * kGroups;
     static constexpr int kPairs = kElements / 2;
     static constexpr int kWords = kElements / (kF32 ? 1 : 2);
+    static constexpr int kTurn = kWide ? 8 : kF32 ? 1 : 2;   // neighbours that a thread takes together
     uint32_t w[kWords];
 
-    __device__ __forceinline__ static int column(int k, int t, int threads) {
-        return kWide ? ((k >> 3) * threads + t) * 8 + (k & 7) : k * threads + t;
+    __device__ __forceinline__ static int column(int k, const RowShape& s) {
+        return ((k / kTurn) * s.threads + s.t) * kTurn + k % kTurn;
     }
-    __device__ __forceinline__ void load(const void* row, int dim, int t, int threads) {
+    __device__ __forceinline__ static bool inside(int k, const RowShape& s) { return column(k, s) < s.dim; }
+
+    // kPadded: the bytes behind the row may be read (its slot in shared memory).
+    template <bool kPadded = false>
+    __device__ __forceinline__ void load(const void* row, const RowShape& s) {
+        const uint8_t* const p = static_cast<const uint8_t*>(row);
         if (kWide) {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                const int c = (j * threads + t) * 8;
                 constexpr int kLoads = kF32 ? 2 : 1;
 #pragma unroll
                 for (int h = 0; h < kLoads; ++h) {
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (c < dim) v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(c) * (kF32 ? 4 : 2))[h];
+                    if (inside(8 * j, s)) v = reinterpret_cast<const uint4*>(p + static_cast<int64_t>(column(8 * j, s)) * (kF32 ? 4 : 2))[h];
                     uint32_t* const d = w + (j * kLoads + h) * 4;
                     d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
                 }
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) w[k] = 0u;
+        } else if (kF32) {
 #pragma unroll
             for (int k = 0; k < kElements; ++k) {
-                const int c = k * threads + t;
-                if (c >= dim) continue;
-                if (kF32) w[k] = static_cast<const uint32_t*>(row)[c];
-                else w[k >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(row)[c]) << (16 * (k & 1));
+                w[k] = 0u;
+                if (inside(k, s)) w[k] = reinterpret_cast<const uint32_t*>(p)[column(k, s)];
+            }
+        } else if ((reinterpret_cast<uintptr_t>(p) & 3u) == 0) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const int c = column(2 * i, s);
+                w[i] = 0u;
+                if (c + (kPadded ? 0 : 1) < s.dim) w[i] = *reinterpret_cast<const uint32_t*>(p + 2 * c);
+                else if (c < s.dim) w[i] = *reinterpret_cast<const uint16_t*>(p + 2 * c);
+                if (kPadded && c + 1 >= s.dim) w[i] &= 0xFFFFu;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const int c = column(2 * i, s);
+                const uint16_t* const q = reinterpret_cast<const uint16_t*>(p) + c;
+                uint32_t lo = 0u, hi = 0u;
+                if (c < s.dim) lo = q[0];
+                if (c + 1 < s.dim) hi = q[1];
+                w[i] = lo | hi << 16;
             }
         }
     }
@@ -80,65 +105,86 @@ struct RowPart {
         if (kF32) return pack2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])));
         return pack2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
     }
-    // v, with zeros behind the row's end: for all elements of a wide group the same.
-    __device__ __forceinline__ static uint64_t inside(float v, int i, int dim, int t, int threads) {
-        if (kWide) return both(column(2 * i, t, threads) < dim ? v : 0.0f);
-        return pack2(make_float2(column(2 * i, t, threads) < dim ? v : 0.0f, column(2 * i + 1, t, threads) < dim ? v : 0.0f));
+    // v for each of the two, zero behind the row's end.
+    __device__ __forceinline__ static uint64_t within(float v, int i, const RowShape& s) {
+        if (kWide) return both(inside(2 * i, s) ? v : 0.0f);
+        return pack2(make_float2(inside(2 * i, s) ? v : 0.0f, inside(2 * i + 1, s) ? v : 0.0f));
     }
     // The pairs v, each element rounded once to the row's type, to the row's elements.
-    __device__ __forceinline__ static void store(void* row, const uint64_t* v, int dim, int t, int threads) {
+    __device__ __forceinline__ static void store(void* row, const uint64_t* v, const RowShape& s) {
+        uint8_t* const p = static_cast<uint8_t*>(row);
         if (kWide) {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                const int c = (j * threads + t) * 8;
-                if (c >= dim) continue;
+                if (!inside(8 * j, s)) continue;
                 float2 f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = unpack2(v[4 * j + i]);
                 if (kF32) {
-                    float4* const d = reinterpret_cast<float4*>(static_cast<float*>(row) + c);
+                    float4* const d = reinterpret_cast<float4*>(p + 4 * static_cast<int64_t>(column(8 * j, s)));
                     d[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
                     d[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
                 } else {
                     uint32_t h[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
-                        h[i] = *reinterpret_cast<const uint32_t*>(&b);
-                    }
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c) = make_uint4(h[0], h[1], h[2], h[3]);
+                    for (int i = 0; i < 4; ++i) h[i] = to_bf16(f[i]);
+                    *reinterpret_cast<uint4*>(p + 2 * static_cast<int64_t>(column(8 * j, s))) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
-        } else {
+        } else if (kF32) {
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {
                 const float2 f = unpack2(v[i]);
+                if (inside(2 * i, s)) reinterpret_cast<float*>(p)[column(2 * i, s)] = f.x;
+                if (inside(2 * i + 1, s)) reinterpret_cast<float*>(p)[column(2 * i + 1, s)] = f.y;
+            }
+        } else {
+            const bool together = (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = (2 * i + h) * threads + t;
-                    if (c >= dim) continue;
-                    if (kF32) static_cast<float*>(row)[c] = h ? f.y : f.x;
-                    else static_cast<__nv_bfloat16*>(row)[c] = __float2bfloat16_rn(h ? f.y : f.x);
+            for (int i = 0; i < kPairs; ++i) {
+                const int c = column(2 * i, s);
+                const uint32_t h = to_bf16(unpack2(v[i]));
+                uint16_t* const q = reinterpret_cast<uint16_t*>(p) + c;
+                if (together && c + 1 < s.dim) {
+                    *reinterpret_cast<uint32_t*>(q) = h;
+                } else {
+                    if (c < s.dim) q[0] = static_cast<uint16_t>(h);
+                    if (c + 1 < s.dim) q[1] = static_cast<uint16_t>(h >> 16);
                 }
             }
         }
     }
+    __device__ __forceinline__ static uint32_t to_bf16(float2 f) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t*>(&b);
+    }
 };
 
-// A thread's part of a vector of fp32 or bf16, as pairs, zero behind the row's end.
-template <bool kWide, int kGroups>
-__device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32, int dim, int t, int threads, uint64_t* f) {
-    if (f32) {
-        RowPart<true, kWide, kGroups> p;
-        p.load(static_cast<const float*>(v) + at, dim, t, threads);
+// A thread's part of a vector of fp32 or bf16, as pairs in the places of Part, zero behind the row's end.
+template <bool kF32, bool kWide, int kGroups>
+__device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32, const RowShape& s, uint64_t* f) {
+    using Part = RowPart<kF32, kWide, kGroups>;
+    if (kWide) {
+        if (f32) {
+            RowPart<true, true, kGroups> p;
+            p.load(static_cast<const float*>(v) + at, s);
 #pragma unroll
-        for (int i = 0; i < 4 * kGroups; ++i) f[i] = p.pair(i);
-    } else {
-        RowPart<false, kWide, kGroups> p;
-        p.load(static_cast<const uint16_t*>(v) + at, dim, t, threads);
+            for (int i = 0; i < Part::kPairs; ++i) f[i] = p.pair(i);
+        } else {
+            RowPart<false, true, kGroups> p;
+            p.load(static_cast<const uint16_t*>(v) + at, s);
 #pragma unroll
-        for (int i = 0; i < 4 * kGroups; ++i) f[i] = p.pair(i);
+            for (int i = 0; i < Part::kPairs; ++i) f[i] = p.pair(i);
+        }
+        return;
     }
+    auto one = [&](int k) {
+        if (!Part::inside(k, s)) return 0.0f;
+        const int64_t i = at + Part::column(k, s);
+        return f32 ? static_cast<const float*>(v)[i] : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(v)[i]) << 16);
+    };
+#pragma unroll
+    for (int i = 0; i < Part::kPairs; ++i) f[i] = pack2(make_float2(one(2 * i), one(2 * i + 1)));
 }
 
 // Threads of a CTA that has a row to itself.
