@@ -497,6 +497,37 @@ mxfp4_status mxfp4_grouped_forward(const mxfp4_grouped_linear* layer, const void
 mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const void* dy, int64_t lddy,
                                     const int32_t* offsets, int64_t rows, mxfp4_stream_t stream);
 
+/* ---- a layer of experts for a few tokens --------------------------------------------------
+ * y_t = sum over token t's chosen experts e of w_e W2_e . (silu(g) u), [g; u] = W1_e . x_t, silu(g) = g / (1 + exp(-g)), in
+ * two kernels: the top_k experts with the largest logits (equal ones: the lowest index first; a NaN counts as the
+ * largest), w_e = softmax(logits)_e, divided by the sum of the chosen ones with MXFP4_EXPERTS_NORMALIZE.  An expert whose
+ * weight is zero (a logit of -inf, or far enough below the largest) is not computed and adds nothing; a token whose
+ * logits are all -inf (a row that pads a batch) gets zeros.
+ *   x, y       bf16 [tokens, dim], row pitches ldx, ldy (>= dim), tokens 0 .. MXFP4_EXPERTS_MAX_TOKENS; y must not overlap x
+ *   logits     [tokens, experts], bf16 or (MXFP4_EXPERTS_LOGITS_F32) fp32, row pitch ldl (>= experts)
+ *              x, y and logits aligned to their elements; of one row the pitches are not read
+ *   up_q, up_s      W1's row blob as mxfp4_quantize_grouped packs [experts * 2 inner, dim] in equal groups: an expert's
+ *              `inner` rows of g, then its `inner` rows of u; 16-byte aligned
+ *   down_q, down_s  W2's, [experts * dim, inner] in equal groups
+ *   sizes      experts 1 .. MXFP4_MAX_GROUPS, top_k 1 .. min(experts, MXFP4_EXPERTS_MAX_TOP_K); dim and inner as far as the
+ *              activations of 8 routed rows fit the shared memory: up to 7500 and 4000 whatever the rest
+ *              (mxfp4_experts_workspace_bytes tells: it refuses what the call refuses)
+ *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned; its first 4 * ceil(dim / 128) words are zero before the first use
+ *              (a call leaves them zero); calls that share one are ordered one after the other, as are replays of
+ *              graphs that hold them
+ * x, the weights and the sums are not rounded on the way: the products are those of the values that the blobs stand for, in
+ * fp32, and the activations between the two keep 22 bits.  y is rounded once.  The same inputs give the same bits. */
+#define MXFP4_EXPERTS_LOGITS_F32 1
+#define MXFP4_EXPERTS_NORMALIZE 2
+#define MXFP4_EXPERTS_MAX_TOKENS 64
+#define MXFP4_EXPERTS_MAX_TOP_K 16
+
+mxfp4_status mxfp4_experts_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim, int64_t inner, size_t* bytes);
+mxfp4_status mxfp4_experts_forward(const void* x, int64_t tokens, int64_t ldx, const void* logits, int64_t ldl, int64_t experts,
+                                   int64_t top_k, int64_t dim, int64_t inner, const void* up_q, const void* up_s,
+                                   const void* down_q, const void* down_s, void* y, int64_t ldy, int32_t flags, void* workspace,
+                                   size_t workspace_bytes, mxfp4_stream_t stream);
+
 /* ---- optimizer step ----------------------------------------------------------------------
  * One AdamW step (decoupled weight decay) over any number of tensors, in one launch per 320 of
  * them.  Per element, g the gradient times grad_scale:

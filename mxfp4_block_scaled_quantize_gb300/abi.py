@@ -44,6 +44,11 @@ MXFP4_ADAMW_STATE_E4M3 = 4
 MXFP4_ADAMW_STOCHASTIC = 8
 MXFP4_ADAMW_BLOCK = 128
 
+MXFP4_EXPERTS_LOGITS_F32 = 1
+MXFP4_EXPERTS_NORMALIZE = 2
+MXFP4_EXPERTS_MAX_TOKENS = 64
+MXFP4_EXPERTS_MAX_TOP_K = 16
+
 MXFP4_NORM_X_F32 = 1
 MXFP4_NORM_W_F32 = 2
 MXFP4_NORM_ADD_ONE = 4
@@ -141,6 +146,8 @@ EXPORTED = (
     "mxfp4_grouped_forward",
     "mxfp4_grouped_backward",
     "mxfp4_adamw",
+    "mxfp4_experts_workspace_bytes",
+    "mxfp4_experts_forward",
     "mxfp4_layer_norm",
     "mxfp4_layer_norm_workspace_bytes",
     "mxfp4_layer_norm_backward",
@@ -206,6 +213,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_grouped_backward.argtypes = [ctypes.POINTER(GroupedLinear), vp, i64, vp, i64, vp]
     lib.mxfp4_adamw.argtypes = [i32, vp, i32, ctypes.POINTER(AdamwParams), vp]
     f64, sz = ctypes.c_double, ctypes.c_size_t
+    lib.mxfp4_experts_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, szp]
+    lib.mxfp4_experts_forward.argtypes = [vp, i64, i64, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, i64, i32, vp, sz, vp]
     lib.mxfp4_layer_norm.argtypes = [vp, i64, i64, i64, vp, vp, i64, f64, i32, vp, i64, vp, vp, vp]
     lib.mxfp4_layer_norm_workspace_bytes.argtypes = [i64, szp]
     lib.mxfp4_layer_norm_backward.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, i32, vp, vp, vp, i64, vp, vp, vp, sz, vp]
@@ -476,6 +485,20 @@ def mxfp4_adamw(count, tensors, flags, params, stream=None) -> None:
     """tensors: a ctypes array of AdamwTensor, or the address of such a table; params: AdamwParams."""
     address = tensors if isinstance(tensors, int) or tensors is None else ctypes.addressof(tensors)
     _check(load().mxfp4_adamw(count, address, flags, ctypes.byref(params), _stream(stream)), "mxfp4_adamw")
+
+
+def mxfp4_experts_workspace_bytes(tokens: int, experts: int, top_k: int, dim: int, inner: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mxfp4_experts_workspace_bytes(tokens, experts, top_k, dim, inner, ctypes.byref(n)),
+           "mxfp4_experts_workspace_bytes")
+    return n.value
+
+
+def mxfp4_experts_forward(x, tokens, ldx, logits, ldl, experts, top_k, dim, inner, up_q, up_s, down_q, down_s, y, ldy, flags,
+                          workspace, workspace_bytes, stream=None) -> None:
+    _check(load().mxfp4_experts_forward(_ptr(x), tokens, ldx, _ptr(logits), ldl, experts, top_k, dim, inner, _ptr(up_q),
+                                        _ptr(up_s), _ptr(down_q), _ptr(down_s), _ptr(y), ldy, flags, _ptr(workspace),
+                                        workspace_bytes, _stream(stream)), "mxfp4_experts_forward")
 
 
 def mxfp4_layer_norm(x, rows, dim, ldx, weight, bias, samples, eps, flags, y, ldy, mean=None, rstd=None, stream=None) -> None:

@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4_gb300.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "gemm_pair.cu", "quantize_fp8.cu", "gemm_fp8.cu",
            "host_step.cu", "grouped.cu", "quantize_grouped.cu", "gemm_grouped.cu",
-           "adamw.cu", "grad_norm.cu", "norm.cu", "norm_forward.cu", "norm_backward.cu"]
+           "adamw.cu", "grad_norm.cu", "norm.cu", "norm_forward.cu", "norm_backward.cu", "experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,741 @@
+// experts.cu -- a whole mixture-of-experts layer for a few tokens, in two kernels.
+//
+//   p = softmax(logits), the top_k largest of them (ties: the lowest index), w = p or p / sum of the chosen p,
+//   y_t = sum over the chosen experts e of w_e W2_e . (silu(g) u),   [g; u] = W1_e . x_t,   silu(g) = g / (1 + exp(-g)),
+//   W1 [E, 2 inner, dim], W2 [E, dim, inner] in MXFP4 (E2M1 codes, an E8M0 scale for 32 along the row).
+//
+// For a few tokens the time is that of the chosen experts' weights, each read once: 17 / 32 bytes an element at 23 bytes a
+// clock and SM.  So the activations stay as they are (rounding them to 4 bits would save nothing), and a product has the
+// weights as the 16 rows of a small matrix instruction (mma.sync m16n8k16: the tensor pipe is at a tenth of its rate here, and
+// the tcgen05 forms would want 128 rows of one expert and 4-bit or 8-bit activations) and up to 16 routed rows
+// as its columns.
+//
+// Numbers.  A code is exact in fp16.  x is bf16 times a power of two that brings its row's largest value to 2^14 .. 2^15: exact
+// in fp16 but for what lies 2^-29 and more below that.  The activations between the products are fp32, and the second
+// product takes them as the sum of two fp16 (22 bits).  A block of 32 is summed by the matrix instruction in fp32 and then
+// multiplied by its scale in fp32, as all sums are.  y is rounded once.
+//
+// Work.  A unit is 32 rows of an expert's weights (16 of g and the same 16 of u) against a pass of its routed rows.  A CTA, one
+// an SM, takes a range of consecutive units, so it stages an expert's activations in shared memory once.  A unit's length is cut
+// into slices of 128 elements (2 KB of codes), dealt round the CTA's 16 warps without regard to where a unit ends; each warp has
+// several slices on their way to shared memory by asynchronous copies of its own, and meets the others only to add up a unit.
+//   Rows of a unit: 32 q + i for q = 0 .. 3 and a few consecutive i of a group of 128, so that their scales (16 bytes for the
+//   four q of one i in the scale layout) are consecutive too.
+//   The sum over experts: each unit of the second product leaves its rows, weighted, in fp32; the CTA that
+//   leaves the last one for 32 columns adds them up in the order of the tokens' choices.  No CTA waits for another, and the
+//   order of additions is fixed.
+//
+// The routing is so little work (64 tokens of 64 experts: 1 us) that every CTA does it for itself; the second kernel does
+// it, and asks for its first weights, while the first one is still at work.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "launch.h"
+#include "launch_experts.h"
+#include "ptx.cuh"
+
+namespace mxfp4 {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnitRows = 32;
+constexpr int kSlice = 128;                              // elements of a row
+constexpr int kSliceBytes = kUnitRows * kSlice / 2;      // codes
+constexpr int kStageBytes = kSliceBytes + 4 * kUnitRows; // and a word of four scales for each row
+constexpr int kMaxStages = 4;
+constexpr int kMaxPass = 16;                             // routed rows of a pass
+constexpr int kSharedMost = 227 * 1024;
+
+struct Row {           // of a pass
+    int32_t token;
+    int32_t slot;      // token * top_k + place among the token's choices; -1: not routed here
+    float back;        // undoes the power of two of its activations
+    float weight;
+};
+
+// Shared memory: this head, then [experts] masks, [tokens * top_k] weights and experts, [experts] used experts,
+// the activations, the unit's sums and the warps' stages.
+struct Head {
+    Row rows[kMaxPass];
+    int32_t used;
+    int32_t units;     // (expert, pass) pairs
+    int32_t last;
+    int32_t pad;
+};
+
+__host__ __device__ inline int align16(int n) { return (n + 15) & ~15; }
+
+struct Layout {
+    int masks, weights, ids, list, acts, sums, stages, total;
+    __host__ __device__ Layout(int experts, int tokens, int top_k, int k, int pass_rows, bool pairs, int stage_count) {
+        const int choices = tokens * top_k;
+        masks = align16(sizeof(Head));
+        weights = masks + align16(8 * experts);
+        ids = weights + align16(4 * choices);
+        list = ids + align16(2 * choices);
+        // an expert's passes: one, and one more for every further pass_rows of its tokens
+        acts = list + align16(4 * ((experts < choices ? experts : choices) + choices / pass_rows));
+        sums = acts + pass_rows * pitch(k) * (pairs ? 2 : 1);
+        stages = sums + (kWarps / 2) * kUnitRows * pass_rows * 4;
+        total = stages + kWarps * stage_count * kStageBytes;
+    }
+    // Bytes from one row of the activations to the next: 64 more than a multiple of 128, so that the 16-byte
+    // loads of two rows' four lanes each meet all banks once.
+    __host__ __device__ static int pitch(int k) { return 2 * ((k + kSlice - 1) / kSlice * kSlice) + 64; }
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most `left` (0 .. 3) of this thread's groups are under way.
+__device__ __forceinline__ void copies_wait(int left) {
+    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Eight codes as four pairs of fp16.
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t* h) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+__device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^(byte - 127) for byte b of w.
+__device__ __forceinline__ float scale_of(uint32_t w, int b) {
+    const uint32_t e = (b < 3 ? w << (23 - 8 * b) : w >> 1) & 0x7F800000u;
+    return __uint_as_float(e > 0x00400000u ? e : 0x00400000u);
+}
+
+__device__ __forceinline__ uint32_t max_all(uint32_t v) {
+    uint32_t m;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(v));
+    return m;
+}
+__device__ __forceinline__ uint32_t min_all(uint32_t v) {
+    uint32_t m;
+    asm volatile("redux.sync.min.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(v));
+    return m;
+}
+__device__ __forceinline__ float sum_all(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+
+__device__ __forceinline__ float logit_of(const ExpertsArgs& a, int64_t t, int e) {
+    const int64_t i = t * a.ldl + e;
+    return a.logits_f32 ? __ldcg(static_cast<const float*>(a.logits) + i)
+                        : __uint_as_float(static_cast<uint32_t>(__ldcg(static_cast<const uint16_t*>(a.logits) + i)) << 16);
+}
+
+// The choices of a warp's tokens.  kPer: 32 kPer experts at most.  Order: value, then lowest index; a NaN is
+// above all values, as in a sort.
+template <int kPer>
+__device__ void choose(const ExpertsArgs& a, unsigned long long* masks, float* weights, uint16_t* ids) {
+    const int lane = static_cast<int>(lane_id());
+    for (int t = threadIdx.x >> 5; t < a.tokens; t += kWarps) {
+        float v[kPer];
+        uint32_t key[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = i * 32 + lane;
+            v[i] = e < a.experts ? logit_of(a, t, e) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t u = __float_as_uint(v[i] + 0.0f);   // one zero
+            key[i] = v[i] != v[i] ? 0xFFFFFFFFu : u & 0x80000000u ? ~u : u | 0x80000000u;
+            if (i * 32 + lane >= a.experts) key[i] = 0u;       // below every value
+        }
+        float mine = 0.0f, top = 0.0f;   // lane j: the value of choice j
+        int id = 0;
+        for (int j = 0; j < a.top_k; ++j) {
+            uint32_t best = 0u;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = i;
+                }
+            const uint32_t most = max_all(best);
+            const int e = static_cast<int>(min_all(best == most ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu));
+            float value = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (i * 32 + lane == e) {
+                    key[i] = 0u;
+                    value = v[i];
+                }
+            value = __shfl_sync(0xFFFFFFFFu, value, e & 31);
+            if (j == 0) top = value;
+            if (lane == j) {
+                mine = value;
+                id = e;
+            }
+        }
+        const float none = __int_as_float(0xFF800000);
+        const float p = lane < a.top_k && mine != none ? expf(mine - top) : 0.0f;
+        float sum = p;
+        if (!a.normalize) {
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (i * 32 + lane < a.experts && v[i] != none) sum += expf(v[i] - top);
+        }
+        sum = sum_all(sum);
+        if (lane < a.top_k) {
+            const float w = sum == 0.0f ? 0.0f : p / sum;   // 0: every logit is -inf
+            weights[t * a.top_k + lane] = w;
+            ids[t * a.top_k + lane] = static_cast<uint16_t>(id);
+            if (w != 0.0f) atomicOr(&masks[id], 1ull << t);   // not where it changes nothing
+        }
+    }
+}
+
+// The routing: each expert's tokens, and the list of (expert, pass) pairs that have any.
+__device__ void route(const ExpertsArgs& a, Head* head, unsigned long long* masks, float* weights, uint16_t* ids, uint32_t* list) {
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) masks[e] = 0ull;
+    __syncthreads();
+    if (a.experts <= 64) choose<2>(a, masks, weights, ids);
+    else if (a.experts <= 256) choose<8>(a, masks, weights, ids);
+    else choose<32>(a, masks, weights, ids);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = static_cast<int>(lane_id());
+        int units = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < a.experts ? __popcll(masks[e]) : 0;
+            const int passes = (n + a.passes_rows - 1) / a.passes_rows;
+            int before = passes;   // inclusive sum over the lanes
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, before, d);
+                if (lane >= d) before += up;
+            }
+            for (int p = 0; p < passes; ++p) list[units + before - passes + p] = static_cast<uint32_t>(e) | static_cast<uint32_t>(p) << 16;
+            units += __shfl_sync(0xFFFFFFFFu, before, 31);
+        }
+        if (lane == 0) head->units = units;
+    }
+    __syncthreads();
+}
+
+// What each of the two kernels multiplies.
+struct Up {
+    static constexpr bool kPairs = false;
+    // The weights' row for row lr of tile `tile`; -1: none.
+    __device__ __forceinline__ static int row(const ExpertsArgs& a, int tile, int lr) {
+        const int r = hidden(tile, lr & 15);
+        return r < a.inner ? (lr < 16 ? r : a.inner + r) : -1;
+    }
+    __device__ __forceinline__ static int hidden(int tile, int m) {
+        return 128 * (tile >> 3) + 32 * (m & 3) + 4 * (tile & 7) + (m >> 2);
+    }
+};
+struct Down {
+    static constexpr bool kPairs = true;
+    __device__ __forceinline__ static int row(const ExpertsArgs& a, int tile, int lr) {
+        const int m = lr & 15, r = 128 * (tile >> 2) + 32 * (m & 3) + 8 * (tile & 3) + 4 * (lr >> 4) + (m >> 2);
+        return r < a.dim ? r : -1;
+    }
+};
+
+// A warp's stream of slices: item i is slice i % slices of unit i / slices of the CTA's range.
+template <typename Product>
+struct Stream {
+    const ExpertsArgs& a;
+    const uint32_t* list;
+    uint32_t to;             // the warp's stages
+    int first, slices, items;
+    int item, unit, stage;   // next to be asked for
+    int64_t at[4];           // this lane's four rows of the unit: their codes' place, or -1
+    int64_t scale;           // and the place of its row's scales
+
+    __device__ __forceinline__ Stream(const ExpertsArgs& args, const uint32_t* l, uint32_t stages, int first_unit, int units)
+        : a(args), list(l), to(stages), first(first_unit), slices((args.k + kSlice - 1) / kSlice), items(units * slices),
+          item(threadIdx.x >> 5), unit(-1), stage(0) {}
+
+    __device__ __forceinline__ void place(int u) {
+        unit = u;
+        const int pair = (first + u) / a.tiles, tile = (first + u) - pair * a.tiles;
+        const int64_t e = list[pair] & 0xFFFFu;
+        const int lane = static_cast<int>(lane_id());
+        const int64_t pitch = static_cast<int64_t>(slices) * (kSlice / 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = Product::row(a, tile, 8 * i + (lane >> 2));
+            at[i] = r < 0 ? -1 : (e * a.rows + r) * pitch + (lane & 3) * 16;
+        }
+        const int r = Product::row(a, tile, lane);
+        const int64_t atom = (e * ((a.rows + 127) / 128) + r / 128) * slices;
+        scale = r < 0 ? -1 : atom * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+    }
+    // Asks for the next item, or for nothing: a group of copies either way.
+    __device__ __forceinline__ void ask() {
+        if (item < items) {
+            const int u = item / slices, s = item - u * slices;
+            if (u != unit) place(u);
+            const int lane = static_cast<int>(lane_id());
+            const uint32_t d = to + static_cast<uint32_t>(stage * kStageBytes);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                copy16(d + static_cast<uint32_t>(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)),
+                       a.q + (at[i] < 0 ? 0 : at[i] + s * (kSlice / 2)), at[i] >= 0);
+            }
+            copy4(d + static_cast<uint32_t>(kSliceBytes + 4 * lane), a.s + (scale < 0 ? 0 : scale + s * 512), scale >= 0);
+            item += kWarps;
+            if (++stage == a.stages) stage = 0;
+        }
+        copies_commit();
+    }
+};
+
+// The unit's sums so far += one slice.  acts: this lane's place in the activations (row g, 16 bytes t of the slice's first
+// block), `low` bytes further their low parts.
+template <int kCols, bool kPairs>
+__device__ __forceinline__ void multiply(const uint8_t* stage, const uint8_t* acts, int pitch, int low, float (*acc)[kCols][4]) {
+    const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
+    const uint32_t* const words = reinterpret_cast<const uint32_t*>(stage + kSliceBytes);
+    uint32_t sw[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        sw[m][0] = words[16 * m + g];
+        sw[m][1] = words[16 * m + g + 8];
+    }
+    const uint8_t* const codes = stage + g * 64 + t * 4;
+    const int turn = ((g >> 1) & 3) << 4;
+#pragma unroll
+    for (int b = 0; b < kSlice / 32; ++b) {
+        uint4 x[kCols], xl[kCols];
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+            x[n] = *reinterpret_cast<const uint4*>(acts + 8 * n * pitch + b * 64);
+            if (kPairs) xl[n] = *reinterpret_cast<const uint4*>(acts + low + 8 * n * pitch + b * 64);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            uint32_t lo[4], hi[4];
+            decode8(*reinterpret_cast<const uint32_t*>(codes + 1024 * m + ((b << 4) ^ turn)), lo);
+            decode8(*reinterpret_cast<const uint32_t*>(codes + 1024 * m + 512 + ((b << 4) ^ turn)), hi);
+            const float s0 = scale_of(sw[m][0], b), s1 = scale_of(sw[m][1], b);
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma(p, lo[0], hi[0], lo[1], hi[1], x[n].x, x[n].y);
+                mma(p, lo[2], hi[2], lo[3], hi[3], x[n].z, x[n].w);
+                if (kPairs) {
+                    mma(p, lo[0], hi[0], lo[1], hi[1], xl[n].x, xl[n].y);
+                    mma(p, lo[2], hi[2], lo[3], hi[3], xl[n].z, xl[n].w);
+                }
+                acc[m][n][0] = fmaf(s0, p[0], acc[m][n][0]);
+                acc[m][n][1] = fmaf(s0, p[1], acc[m][n][1]);
+                acc[m][n][2] = fmaf(s1, p[2], acc[m][n][2]);
+                acc[m][n][3] = fmaf(s1, p[3], acc[m][n][3]);
+            }
+        }
+    }
+}
+
+// 2^k that brings `top` to 2^14 .. 2^15 (k <= 126), and 2^-k.
+__device__ __forceinline__ float lift(float top, float* back) {
+    const int e = static_cast<int>(__float_as_uint(top) >> 23);   // of a finite value >= 0
+    const int k = e == 0 ? 126 : min(14 - (e - 127), 126);
+    *back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+__device__ __forceinline__ float finite_or_zero(float v) {
+    v = fabsf(v);
+    return v < __int_as_float(0x7F800000) ? v : 0.0f;
+}
+
+__device__ __forceinline__ float x_of(const ExpertsArgs& a, int64_t row, int c) {
+    return c < a.k ? __uint_as_float(static_cast<uint32_t>(__ldg(a.x + row * a.ldx + c)) << 16) : 0.0f;
+}
+
+// Eight elements of x's row from c on.
+__device__ __forceinline__ void x8(const ExpertsArgs& a, int64_t row, int c, bool wide, float* f) {
+    if (wide && c < a.k) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(a.x + row * a.ldx + c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = x_of(a, row, c + i);
+}
+
+// Eight elements of the row of h from c on.
+__device__ __forceinline__ void h8(const ExpertsArgs& a, int64_t row, int c, bool wide, float* f) {
+    const float* const p = a.h + row * a.inner + c;
+    if (wide && c < a.k) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+        f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+        f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < a.k ? __ldcg(p + i) : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The rows of a pass and their activations.  `all`: the first product of few tokens, whose rows are all tokens
+// whatever the expert: `staged` then says that they are there already.
+template <typename Product>
+__device__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, const unsigned long long* masks, const float* weights,
+                           const uint16_t* ids, uint32_t pair, bool all, bool staged) {
+    const int e = static_cast<int>(pair & 0xFFFFu), pass = static_cast<int>(pair >> 16);
+    const int pitch = Layout::pitch(a.k), rows = a.passes_rows;
+    __syncthreads();   // the rows before are done with
+    if (threadIdx.x < static_cast<unsigned>(rows)) {
+        const int n = threadIdx.x;
+        unsigned long long m = masks[e];
+        int token = -1, slot = -1;
+        if (all) {
+            token = n < a.tokens ? n : -1;
+        } else {
+            int skip = pass * rows + n;
+            for (; skip > 0 && m != 0; --skip) m &= m - 1;
+            token = m != 0 ? __ffsll(static_cast<long long>(m)) - 1 : -1;
+        }
+        if (token >= 0 && (masks[e] >> token & 1ull))
+            for (int j = 0; j < a.top_k; ++j)   // an expert is among a token's choices once
+                if (ids[token * a.top_k + j] == e) slot = token * a.top_k + j;
+        head->rows[n].token = token;
+        head->rows[n].slot = slot;
+        head->rows[n].weight = slot >= 0 ? weights[slot] : 0.0f;
+    }
+    __syncthreads();
+    if (!staged) {
+        const int lane = static_cast<int>(lane_id());
+        for (int n = threadIdx.x >> 5; n < rows; n += kWarps) {
+            const int64_t row = Product::kPairs ? head->rows[n].slot : head->rows[n].token;
+            uint4* const to = reinterpret_cast<uint4*>(acts + n * pitch);
+            const int groups = (pitch - 64) / 16;   // of 8 elements
+            if (row < 0) {
+                for (int c = lane; c < groups; c += 32) {
+                    to[c] = make_uint4(0u, 0u, 0u, 0u);
+                    if (Product::kPairs) to[rows * pitch / 16 + c] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (lane == 0) head->rows[n].back = 0.0f;
+                continue;
+            }
+            const bool wide = Product::kPairs
+                                  ? a.inner % 8 == 0
+                                  : a.k % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.x + row * a.ldx)) & 15u) == 0;
+            float top = 0.0f, f[8];
+            for (int c = lane; c < groups; c += 32) {
+                if (Product::kPairs) h8(a, row, 8 * c, wide, f);
+                else x8(a, row, 8 * c, wide, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_or_zero(f[i]));
+            }
+            top = __uint_as_float(max_all(__float_as_uint(top)));
+            float back;
+            const float up = lift(top, &back);
+            if (lane == 0) head->rows[n].back = back;
+            for (int c = lane; c < groups; c += 32) {
+                if (Product::kPairs) h8(a, row, 8 * c, wide, f);
+                else x8(a, row, 8 * c, wide, f);
+                uint32_t w[4], l[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = f[2 * i] * up, q = f[2 * i + 1] * up;
+                    w[i] = half2_of(p, q);
+                    if (Product::kPairs) {
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                        const float inf = __int_as_float(0x7F800000);
+                        l[i] = half2_of(fabsf(h.x) < inf ? p - h.x : 0.0f, fabsf(h.y) < inf ? q - h.y : 0.0f);
+                    }
+                }
+                to[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (Product::kPairs) to[rows * pitch / 16 + c] = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// What becomes of a unit's sums, in shared memory as [kWarps / 2][kUnitRows][columns].
+__device__ __forceinline__ float unit_sum(const float* sums, int cols, int row, int n) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps / 2; ++w) v += sums[(w * kUnitRows + row) * cols + n];
+    return v;
+}
+
+__device__ __forceinline__ void finish(Up, const ExpertsArgs& a, Head* head, const float* sums, const float*, const uint16_t*,
+                                       int tile, int cols) {
+    for (int i = threadIdx.x; i < 16 * cols; i += kThreads) {
+        const int m = i / cols, n = i - m * cols, r = Up::hidden(tile, m);
+        const Row& row = head->rows[n];
+        if (row.slot < 0 || r >= a.inner) continue;
+        const float g = unit_sum(sums, cols, m, n) * row.back, u = unit_sum(sums, cols, 16 + m, n) * row.back;
+        a.h[static_cast<int64_t>(row.slot) * a.inner + r] = g / (1.0f + expf(-g)) * u;
+    }
+}
+
+__device__ __forceinline__ void finish(Down, const ExpertsArgs& a, Head* head, const float* sums, const float* weights, const uint16_t*,
+                                       int tile, int cols) {
+    for (int i = threadIdx.x; i < kUnitRows * cols; i += kThreads) {
+        const int lr = i / cols, n = i - lr * cols, r = Down::row(a, tile, lr);
+        const Row& row = head->rows[n];
+        if (row.slot < 0 || r < 0) continue;
+        __stcg(a.part + static_cast<int64_t>(row.slot) * a.dim + r, unit_sum(sums, cols, lr, n) * row.back * row.weight);
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        head->last = atomicAdd(a.done + tile, 1u) == static_cast<uint32_t>(head->units) - 1u;
+    }
+    __syncthreads();
+    if (!head->last) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < a.tokens * kUnitRows; i += kThreads) {
+        const int t = i / kUnitRows, r = Down::row(a, tile, i % kUnitRows);
+        if (r < 0) continue;
+        float v = 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int slot = t * a.top_k + j;
+            if (weights[slot] != 0.0f) v += __ldcg(a.part + static_cast<int64_t>(slot) * a.dim + r);
+        }
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        a.y[t * a.ldy + r] = *reinterpret_cast<const uint16_t*>(&h);
+    }
+    if (threadIdx.x == 0) a.done[tile] = 0u;
+}
+
+template <typename Product, int kCols>
+__global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a) {
+    extern __shared__ __align__(16) uint8_t shared[];
+    const Layout at(a.experts, a.tokens, a.top_k, a.k, a.passes_rows, Product::kPairs, a.stages);
+    Head* const head = reinterpret_cast<Head*>(shared);
+    unsigned long long* const masks = reinterpret_cast<unsigned long long*>(shared + at.masks);
+    float* const weights = reinterpret_cast<float*>(shared + at.weights);
+    uint16_t* const ids = reinterpret_cast<uint16_t*>(shared + at.ids);
+    uint32_t* const list = reinterpret_cast<uint32_t*>(shared + at.list);
+    uint8_t* const acts = shared + at.acts;
+    float* const sums = reinterpret_cast<float*>(shared + at.sums);
+    const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+
+    // The second kernel starts when every CTA of the first has passed its wait: what came before the call is complete.
+    if (!Product::kPairs) grid_wait_prerequisites();
+    grid_launch_dependents();
+    route(a, head, masks, weights, ids, list);
+    const int all_units = head->units * a.tiles;
+    const int from = static_cast<int>(static_cast<int64_t>(all_units) * blockIdx.x / gridDim.x);
+    const int units = static_cast<int>(static_cast<int64_t>(all_units) * (blockIdx.x + 1) / gridDim.x) - from;
+    uint8_t* const own = shared + at.stages + warp * a.stages * kStageBytes;
+    Stream<Product> stream(a, list, smem_addr(own), from, units);
+    for (int i = 0; i < a.stages; ++i) stream.ask();
+    if (Product::kPairs) grid_wait_prerequisites();
+    if (Product::kPairs && all_units == 0)   // nobody chose anything
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<int64_t>(a.tokens) * a.dim;
+             i += static_cast<int64_t>(gridDim.x) * kThreads)
+            a.y[i / a.dim * a.ldy + i % a.dim] = 0;
+
+    const int slices = stream.slices, pitch = Layout::pitch(a.k), low = a.passes_rows * pitch;
+    const bool all = !Product::kPairs && a.tokens <= a.passes_rows;
+    int item = warp, stage = 0, pair = -1;
+    bool staged = false;
+    for (int u = 0; u < units; ++u) {
+        const int p = (from + u) / a.tiles, tile = from + u - p * a.tiles;
+        if (p != pair) {
+            stage_rows<Product>(a, head, acts, masks, weights, ids, list[p], all, staged);
+            pair = p;
+            staged = all;
+        }
+        float acc[2][kCols][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+        for (; item < (u + 1) * slices; item += kWarps) {
+            copies_wait(a.stages - 1);
+            __syncwarp();
+            multiply<kCols, Product::kPairs>(own + stage * kStageBytes, acts + g * pitch + t * 16 + (item - u * slices) * (kSlice * 2),
+                                             pitch, low, acc);
+            __syncwarp();
+            stream.ask();
+            if (++stage == a.stages) stage = 0;
+        }
+        // A warp's place is that of its slices in the unit, so that what a token's sums add up in what order does not
+        // depend on the tokens beside it.  The upper half, then the lower half with it, then the sum over eight.
+        constexpr int kWide = 8 * kCols;
+        const int place = (warp - u * slices) & (kWarps - 1);
+        float* const mine = sums + (place & (kWarps / 2 - 1)) * kUnitRows * kWide;
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+            if ((place >= kWarps / 2) == (half == 1)) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float2* const d = reinterpret_cast<float2*>(mine + (16 * m + 8 * h + g) * kWide + 8 * n + 2 * t);
+                            float2 v = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+                            if (half == 0) {
+                                const float2 w = *d;
+                                v.x += w.x;
+                                v.y += w.y;
+                            }
+                            *d = v;
+                        }
+            }
+            __syncthreads();
+        }
+        finish(Product(), a, head, sums, weights, ids, tile, kWide);
+        __syncthreads();
+    }
+    copies_wait(0);
+}
+
+// Sets passes and stages for the kernel of `a`, and gives its shared memory, or 0 where it does not fit.
+int shape(ExpertsArgs* a, bool pairs) {
+    for (int cols = a->tokens <= 8 ? 1 : 2; cols >= 1; --cols) {
+        a->passes_rows = 8 * cols;
+        for (a->stages = kMaxStages; a->stages >= 2; --a->stages) {
+            const Layout l(a->experts, a->tokens, a->top_k, a->k, a->passes_rows, pairs, a->stages);
+            if (l.total <= kSharedMost) return l.total;
+        }
+    }
+    return 0;
+}
+
+template <typename Product, int kCols>
+cudaError_t launch(const ExpertsArgs& a, int smem, int sms, cudaStream_t stream) {
+    const auto kernel = experts_kernel<Product, kCols>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename Product>
+cudaError_t launch(ExpertsArgs a, int rows, int k, int sms, cudaStream_t stream) {
+    a.rows = rows;
+    a.k = k;
+    a.tiles = Product::kPairs ? 4 * ((a.dim + 127) / 128) : 8 * ((a.inner + 127) / 128);
+    const int smem = shape(&a, Product::kPairs);
+    if (smem == 0) return cudaErrorInvalidValue;
+    return a.passes_rows == 8 ? launch<Product, 1>(a, smem, sms, stream) : launch<Product, 2>(a, smem, sms, stream);
+}
+
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
+
+// Sizes that the kernels take: what they need of shared memory decides.
+bool sizes_ok(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim, int64_t inner) {
+    if (tokens < 0 || tokens > MXFP4_EXPERTS_MAX_TOKENS || experts < 1 || experts > MXFP4_MAX_GROUPS || top_k < 1 ||
+        top_k > MXFP4_EXPERTS_MAX_TOP_K || top_k > experts || dim < 1 || dim > 65536 || inner < 1 || inner > 65536)
+        return false;
+    ExpertsArgs a = {};
+    a.experts = static_cast<int32_t>(experts);
+    a.tokens = static_cast<int32_t>(tokens > 0 ? tokens : 1);
+    a.top_k = static_cast<int32_t>(top_k);
+    a.k = static_cast<int32_t>(dim);
+    if (shape(&a, false) == 0) return false;
+    a.k = static_cast<int32_t>(inner);
+    return shape(&a, true) != 0;
+}
+
+int64_t counters_bytes(int64_t dim) { return align256((dim + 127) / 128 * 16); }
+
+}  // namespace
+}  // namespace mxfp4
+
+extern "C" {
+
+mxfp4_status mxfp4_experts_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim, int64_t inner, size_t* bytes) {
+    if (!mxfp4::sizes_ok(tokens, experts, top_k, dim, inner) || bytes == nullptr) return MXFP4_ERR_INVALID_ARG;
+    *bytes = static_cast<size_t>(mxfp4::counters_bytes(dim) + mxfp4::align256(4 * tokens * top_k * inner) +
+                                 mxfp4::align256(4 * tokens * top_k * dim));
+    return MXFP4_OK;
+}
+
+mxfp4_status mxfp4_experts_forward(const void* x, int64_t tokens, int64_t ldx, const void* logits, int64_t ldl, int64_t experts,
+                                   int64_t top_k, int64_t dim, int64_t inner, const void* up_q, const void* up_s,
+                                   const void* down_q, const void* down_s, void* y, int64_t ldy, int32_t flags, void* workspace,
+                                   size_t workspace_bytes, mxfp4_stream_t stream) {
+    size_t need = 0;
+    if (mxfp4_experts_workspace_bytes(tokens, experts, top_k, dim, inner, &need) != MXFP4_OK || (flags & ~3))
+        return MXFP4_ERR_INVALID_ARG;
+    const int64_t most = int64_t{1} << 40;
+    if (tokens > 0 && (!x || !logits || !up_q || !up_s || !down_q || !down_s || !y || !workspace || workspace_bytes < need ||
+                       (tokens > 1 && (ldx < dim || ldl < experts || ldy < dim || ldx > most || ldl > most || ldy > most))))
+        return MXFP4_ERR_INVALID_ARG;
+    if (!mxfp4::aligned_to(x, 2) || !mxfp4::aligned_to(y, 2) || !mxfp4::aligned_to(logits, flags & MXFP4_EXPERTS_LOGITS_F32 ? 4 : 2) ||
+        !mxfp4::aligned_to(up_q, 16) || !mxfp4::aligned_to(up_s, 16) || !mxfp4::aligned_to(down_q, 16) ||
+        !mxfp4::aligned_to(down_s, 16) || !mxfp4::aligned_to(workspace, 256))
+        return MXFP4_ERR_MISALIGNED;
+    int sms = 0;
+    uint32_t* err = nullptr;
+    const int st = mxfp4::device_info(&sms, &err);
+    if (st != MXFP4_OK || tokens == 0) return static_cast<mxfp4_status>(st);
+    mxfp4::ExpertsArgs a = {};
+    uint8_t* const w = static_cast<uint8_t*>(workspace);
+    a.x = static_cast<const uint16_t*>(x);
+    a.ldx = tokens > 1 ? ldx : 0;
+    a.logits = logits;
+    a.ldl = tokens > 1 ? ldl : 0;
+    a.done = reinterpret_cast<uint32_t*>(w);
+    a.h = reinterpret_cast<float*>(w + mxfp4::counters_bytes(dim));
+    a.part = reinterpret_cast<float*>(w + mxfp4::counters_bytes(dim) + mxfp4::align256(4 * tokens * top_k * inner));
+    a.y = static_cast<uint16_t*>(y);
+    a.ldy = tokens > 1 ? ldy : 0;
+    a.tokens = static_cast<int32_t>(tokens);
+    a.experts = static_cast<int32_t>(experts);
+    a.top_k = static_cast<int32_t>(top_k);
+    a.dim = static_cast<int32_t>(dim);
+    a.inner = static_cast<int32_t>(inner);
+    a.logits_f32 = flags & MXFP4_EXPERTS_LOGITS_F32 ? 1 : 0;
+    a.normalize = flags & MXFP4_EXPERTS_NORMALIZE ? 1 : 0;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    a.q = static_cast<const uint8_t*>(up_q);
+    a.s = static_cast<const uint8_t*>(up_s);
+    if (mxfp4::launch<mxfp4::Up>(a, 2 * a.inner, a.dim, sms, s) != cudaSuccess) return MXFP4_ERR_CUDA;
+    a.q = static_cast<const uint8_t*>(down_q);
+    a.s = static_cast<const uint8_t*>(down_s);
+    return mxfp4::launch<mxfp4::Down>(a, a.dim, a.inner, sms, s) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+}
+
+}  // extern "C"
