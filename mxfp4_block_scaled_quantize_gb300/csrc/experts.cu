@@ -16,14 +16,17 @@
 // multiplied by its scale in fp32, as all sums are.  y is rounded once.
 //
 // Work.  A unit is 32 rows of an expert's weights (16 of g and the same 16 of u) against a pass of its routed rows.  A CTA, one
-// an SM, takes a range of consecutive units, so it stages an expert's activations in shared memory once.  A unit's length is cut
-// into slices of 128 elements (2 KB of codes), dealt round the CTA's 16 warps without regard to where a unit ends; each warp has
-// several slices on their way to shared memory by asynchronous copies of its own, and meets the others only to add up a unit.
+// an SM, takes a range of consecutive units, so it stages an expert's activations in shared memory once.  Its 16 warps take
+// 16 units of one expert at a time, a whole unit each, and meet nobody; of the n < 16 that are left they take 8, 4, 2 and 1, as n
+// has them, with 2, 4, 8 and 16 warps to a unit, each with its part of the row's length: so all warps do the same whatever n is.
+// (All units dealt out in slices of 128 elements to 16 warps, which met after each one: 171 instructions for 32 x 32 weights, and
+// 255 us where it is now ##.)  Each warp has several slices (2 KB of codes) on their way to shared memory by asynchronous
+// copies of its own, across the ends of its units.
 //   Rows of a unit: 32 q + i for q = 0 .. 3 and a few consecutive i of a group of 128, so that their scales (16 bytes for the
 //   four q of one i in the scale layout) are consecutive too.
-//   The sum over experts: each unit of the second product leaves its rows, weighted, in fp32; the CTA that
+//   The sum over experts: each unit of the second product leaves its rows, weighted, in fp32; the warp that
 //   leaves the last one for 32 columns adds them up in the order of the tokens' choices.  No CTA waits for another, and the
-//   order of additions is fixed.
+//   order of additions is fixed by the call's routing.
 //
 // The routing is so little work (64 tokens of 64 experts: 1 us) that every CTA does it for itself; the second kernel does
 // it, and asks for its first weights, while the first one is still at work.
@@ -58,10 +61,8 @@ struct Row {           // of a pass
 // the activations, the unit's sums and the warps' stages.
 struct Head {
     Row rows[kMaxPass];
-    int32_t used;
     int32_t units;     // (expert, pass) pairs
-    int32_t last;
-    int32_t pad;
+    int32_t wide;      // the pass has more than 8 rows
 };
 
 __host__ __device__ inline int align16(int n) { return (n + 15) & ~15; }
@@ -77,7 +78,7 @@ struct Layout {
         // an expert's passes: one, and one more for every further pass_rows of its tokens
         acts = list + align16(4 * ((experts < choices ? experts : choices) + choices / pass_rows));
         sums = acts + pass_rows * pitch(k) * (pairs ? 2 : 1);
-        stages = sums + (kWarps / 2) * kUnitRows * pass_rows * 4;
+        stages = sums + kWarps / 2 * kUnitRows * kMaxPass * 4;
         total = stages + kWarps * stage_count * kStageBytes;
     }
     // Bytes from one row of the activations to the next: 64 more than a multiple of 128, so that the 16-byte
@@ -113,6 +114,12 @@ __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // 2^(byte - 127) for byte b of w.
@@ -257,52 +264,89 @@ struct Down {
     }
 };
 
-// A warp's stream of slices: item i is slice i % slices of unit i / slices of the CTA's range.
+// A warp's way through the CTA's units, round by round: 16 units of one expert and pass with a warp each, or the 8, 4, 2 or 1
+// that are left with more warps to each.
+struct Rounds {
+    int end, tiles, slices, warp;
+    int base;              // first unit of the round
+    int next;              // and of the one after it
+    int pair;              // the round's place in the list of (expert, pass)
+    int parts;             // warps of a unit
+    int unit, part;        // this warp's
+    int slice, last;       // its slices: from, to
+
+    // Before the first round.
+    __device__ __forceinline__ Rounds(int from, int to, int tiles_, int slices_)
+        : end(to), tiles(tiles_), slices(slices_), warp(threadIdx.x >> 5), base(from), next(from), pair(-1), parts(1), unit(0), part(0),
+          slice(0), last(0) {}
+    __device__ __forceinline__ bool advance() {
+        if (next >= end) return false;
+        base = next;
+        pair = base / tiles;
+        const int left = min(end, (pair + 1) * tiles) - base;
+        const int shift = left >= kWarps ? 0 : __clz(left) - (31 - 4);   // kWarps = 2^4
+        parts = 1 << shift;
+        unit = base + (warp >> shift);
+        part = warp & (parts - 1);
+        slice = (slices * part) >> shift;
+        last = (slices * (part + 1)) >> shift;
+        next = base + (kWarps >> shift);
+        return true;
+    }
+};
+
+// A warp's slices on their way to shared memory, in the order in which it takes them.
 template <typename Product>
 struct Stream {
     const ExpertsArgs& a;
     const uint32_t* list;
-    uint32_t to;             // the warp's stages
-    int first, slices, items;
-    int item, unit, stage;   // next to be asked for
-    int64_t at[4];           // this lane's four rows of the unit: their codes' place, or -1
-    int64_t scale;           // and the place of its row's scales
+    uint32_t to, end_to, d;   // the warp's stages, and the next one to be filled
+    Rounds r;
+    bool more;
+    const uint8_t* q[4];      // this lane's piece of four rows
+    const uint8_t* s;         // and its row's scales
+    uint32_t there;           // which of the rows there are; bit 4: the scales' row
 
-    __device__ __forceinline__ Stream(const ExpertsArgs& args, const uint32_t* l, uint32_t stages, int first_unit, int units)
-        : a(args), list(l), to(stages), first(first_unit), slices((args.k + kSlice - 1) / kSlice), items(units * slices),
-          item(threadIdx.x >> 5), unit(-1), stage(0) {}
-
-    __device__ __forceinline__ void place(int u) {
-        unit = u;
-        const int pair = (first + u) / a.tiles, tile = (first + u) - pair * a.tiles;
-        const int64_t e = list[pair] & 0xFFFFu;
-        const int lane = static_cast<int>(lane_id());
-        const int64_t pitch = static_cast<int64_t>(slices) * (kSlice / 2);
+    __device__ __forceinline__ Stream(const ExpertsArgs& args, const uint32_t* l, uint32_t stages, const Rounds& rounds)
+        : a(args), list(l), to(stages), end_to(stages + args.stages * kStageBytes), d(stages), r(rounds) {
+        advance();
+    }
+    // To the next round with slices for this warp.
+    __device__ __forceinline__ void advance() {
+        do more = r.advance();
+        while (more && r.slice >= r.last);
+        if (!more) return;
+        const int tile = r.unit - r.pair * a.tiles, lane = static_cast<int>(lane_id());
+        const int64_t e = list[r.pair] & 0xFFFFu;
+        const int64_t pitch = static_cast<int64_t>(r.slices) * (kSlice / 2);
+        there = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = Product::row(a, tile, 8 * i + (lane >> 2));
-            at[i] = r < 0 ? -1 : (e * a.rows + r) * pitch + (lane & 3) * 16;
+            const int row = Product::row(a, tile, 8 * i + (lane >> 2));
+            if (row >= 0) there |= 1u << i;
+            q[i] = a.q + (row < 0 ? 0 : (e * a.rows + row) * pitch + r.slice * (kSlice / 2) + (lane & 3) * 16);
         }
-        const int r = Product::row(a, tile, lane);
-        const int64_t atom = (e * ((a.rows + 127) / 128) + r / 128) * slices;
-        scale = r < 0 ? -1 : atom * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+        const int row = Product::row(a, tile, lane);
+        const int64_t atom = (e * ((a.rows + 127) / 128) + row / 128) * r.slices + r.slice;
+        if (row >= 0) there |= 16u;
+        s = a.s + (row < 0 ? 0 : atom * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4);
     }
-    // Asks for the next item, or for nothing: a group of copies either way.
+    // Asks for the next slice, or for nothing: a group of copies either way.
     __device__ __forceinline__ void ask() {
-        if (item < items) {
-            const int u = item / slices, s = item - u * slices;
-            if (u != unit) place(u);
+        if (more) {
             const int lane = static_cast<int>(lane_id());
-            const uint32_t d = to + static_cast<uint32_t>(stage * kStageBytes);
+            // row 8 i + lane / 4 at 64 bytes of it, its 16-byte pieces turned by (row / 2) % 4
+            const uint32_t at = d + static_cast<uint32_t>((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + (lane >> 2);
-                copy16(d + static_cast<uint32_t>(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)),
-                       a.q + (at[i] < 0 ? 0 : at[i] + s * (kSlice / 2)), at[i] >= 0);
+                copy16(at + 512 * i, q[i], there >> i & 1u);
+                q[i] += there >> i & 1u ? kSlice / 2 : 0;
             }
-            copy4(d + static_cast<uint32_t>(kSliceBytes + 4 * lane), a.s + (scale < 0 ? 0 : scale + s * 512), scale >= 0);
-            item += kWarps;
-            if (++stage == a.stages) stage = 0;
+            copy4(d + static_cast<uint32_t>(kSliceBytes + 4 * lane), s, there >> 4 & 1u);
+            s += there >> 4 & 1u ? 512 : 0;
+            d += kStageBytes;
+            if (d == end_to) d = to;
+            if (++r.slice == r.last) advance();
         }
         copies_commit();
     }
@@ -311,7 +355,7 @@ struct Stream {
 // The unit's sums so far += one slice.  acts: this lane's place in the activations (row g, 16 bytes t of the slice's first
 // block), `low` bytes further their low parts.
 template <int kCols, bool kPairs>
-__device__ __forceinline__ void multiply(const uint8_t* stage, const uint8_t* acts, int pitch, int low, float (*acc)[kCols][4]) {
+__device__ __forceinline__ void multiply(const uint8_t* stage, const uint8_t* acts, int pitch, int low, float (*acc)[kMaxPass / 8][4]) {
     const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
     const uint32_t* const words = reinterpret_cast<const uint32_t*>(stage + kSliceBytes);
     uint32_t sw[2][2];
@@ -338,8 +382,8 @@ __device__ __forceinline__ void multiply(const uint8_t* stage, const uint8_t* ac
             const float s0 = scale_of(sw[m][0], b), s1 = scale_of(sw[m][1], b);
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
-                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma(p, lo[0], hi[0], lo[1], hi[1], x[n].x, x[n].y);
+                float p[4];
+                mma_first(p, lo[0], hi[0], lo[1], hi[1], x[n].x, x[n].y);
                 mma(p, lo[2], hi[2], lo[3], hi[3], x[n].z, x[n].w);
                 if (kPairs) {
                     mma(p, lo[0], hi[0], lo[1], hi[1], xl[n].x, xl[n].y);
@@ -430,6 +474,7 @@ __device__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, cons
         head->rows[n].token = token;
         head->rows[n].slot = slot;
         head->rows[n].weight = slot >= 0 ? weights[slot] : 0.0f;
+        if (n == rows - 1) head->wide = rows > 8 && (all ? a.tokens : __popcll(masks[e]) - pass * rows) > 8;
     }
     __syncthreads();
     if (!staged) {
@@ -482,57 +527,66 @@ __device__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, cons
     __syncthreads();
 }
 
-// What becomes of a unit's sums, in shared memory as [kWarps / 2][kUnitRows][columns].
-__device__ __forceinline__ float unit_sum(const float* sums, int cols, int row, int n) {
-    float v = 0.0f;
+// What becomes of a unit's sums, in the registers of one warp: element (row 16 m + 8 h + g, column 8 n + 2 t + c) of the
+// unit in acc[m][n][2 h + c].
+__device__ __forceinline__ void finish(Up, const ExpertsArgs& a, const Head* head, const float*, int tile, int cols,
+                                       const float (*acc)[kMaxPass / 8][4]) {
+    const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
 #pragma unroll
-    for (int w = 0; w < kWarps / 2; ++w) v += sums[(w * kUnitRows + row) * cols + n];
-    return v;
-}
-
-__device__ __forceinline__ void finish(Up, const ExpertsArgs& a, Head* head, const float* sums, const float*, const uint16_t*,
-                                       int tile, int cols) {
-    for (int i = threadIdx.x; i < 16 * cols; i += kThreads) {
-        const int m = i / cols, n = i - m * cols, r = Up::hidden(tile, m);
-        const Row& row = head->rows[n];
-        if (row.slot < 0 || r >= a.inner) continue;
-        const float g = unit_sum(sums, cols, m, n) * row.back, u = unit_sum(sums, cols, 16 + m, n) * row.back;
-        a.h[static_cast<int64_t>(row.slot) * a.inner + r] = g / (1.0f + expf(-g)) * u;
-    }
-}
-
-__device__ __forceinline__ void finish(Down, const ExpertsArgs& a, Head* head, const float* sums, const float* weights, const uint16_t*,
-                                       int tile, int cols) {
-    for (int i = threadIdx.x; i < kUnitRows * cols; i += kThreads) {
-        const int lr = i / cols, n = i - lr * cols, r = Down::row(a, tile, lr);
-        const Row& row = head->rows[n];
-        if (row.slot < 0 || r < 0) continue;
-        __stcg(a.part + static_cast<int64_t>(row.slot) * a.dim + r, unit_sum(sums, cols, lr, n) * row.back * row.weight);
-    }
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        head->last = atomicAdd(a.done + tile, 1u) == static_cast<uint32_t>(head->units) - 1u;
-    }
-    __syncthreads();
-    if (!head->last) return;
-    __threadfence();
-    for (int i = threadIdx.x; i < a.tokens * kUnitRows; i += kThreads) {
-        const int t = i / kUnitRows, r = Down::row(a, tile, i % kUnitRows);
-        if (r < 0) continue;
-        float v = 0.0f;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int slot = t * a.top_k + j;
-            if (weights[slot] != 0.0f) v += __ldcg(a.part + static_cast<int64_t>(slot) * a.dim + r);
+    for (int n = 0; n < kMaxPass / 8; ++n) {
+        if (n >= cols) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const Row row = head->rows[8 * n + 2 * t + c];
+            if (row.slot < 0) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = Up::hidden(tile, 8 * h + g);
+                const float x = acc[0][n][2 * h + c] * row.back, u = acc[1][n][2 * h + c] * row.back;
+                if (r < a.inner) a.h[static_cast<int64_t>(row.slot) * a.inner + r] = x / (1.0f + expf(-x)) * u;
+            }
         }
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        a.y[t * a.ldy + r] = *reinterpret_cast<const uint16_t*>(&h);
     }
-    if (threadIdx.x == 0) a.done[tile] = 0u;
 }
 
-template <typename Product, int kCols>
+__device__ __forceinline__ void finish(Down, const ExpertsArgs& a, const Head* head, const float* weights, int tile, int cols,
+                                       const float (*acc)[kMaxPass / 8][4]) {
+    const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < kMaxPass / 8; ++n) {
+        if (n >= cols) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const Row row = head->rows[8 * n + 2 * t + c];
+            if (row.slot < 0) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = Down::row(a, tile, 8 * i + g);
+                if (r >= 0) __stcg(a.part + static_cast<int64_t>(row.slot) * a.dim + r, acc[i >> 1][n][2 * (i & 1) + c] * row.back * row.weight);
+            }
+        }
+    }
+    __threadfence();
+    __syncwarp();
+    uint32_t before = 0;
+    if (lane == 0) before = atomicAdd(a.done + tile, 1u);
+    if (__shfl_sync(0xFFFFFFFFu, before, 0) != static_cast<uint32_t>(head->units) - 1u) return;
+    __threadfence();
+    const int r = Down::row(a, tile, lane);
+    if (r >= 0)
+        for (int64_t at = 0; at < a.tokens; ++at) {
+            float v = 0.0f;
+            for (int j = 0; j < a.top_k; ++j) {
+                const int64_t slot = at * a.top_k + j;
+                if (weights[slot] != 0.0f) v += __ldcg(a.part + slot * a.dim + r);
+            }
+            const __nv_bfloat16 h = __float2bfloat16_rn(v);
+            a.y[at * a.ldy + r] = *reinterpret_cast<const uint16_t*>(&h);
+        }
+    if (lane == 0) a.done[tile] = 0u;
+}
+
+template <typename Product>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a) {
     extern __shared__ __align__(16) uint8_t shared[];
     const Layout at(a.experts, a.tokens, a.top_k, a.k, a.passes_rows, Product::kPairs, a.stages);
@@ -542,18 +596,19 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     uint16_t* const ids = reinterpret_cast<uint16_t*>(shared + at.ids);
     uint32_t* const list = reinterpret_cast<uint32_t*>(shared + at.list);
     uint8_t* const acts = shared + at.acts;
-    float* const sums = reinterpret_cast<float*>(shared + at.sums);
     const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
 
     // The second kernel starts when every CTA of the first has passed its wait: what came before the call is complete.
     if (!Product::kPairs) grid_wait_prerequisites();
     grid_launch_dependents();
     route(a, head, masks, weights, ids, list);
-    const int all_units = head->units * a.tiles;
-    const int from = static_cast<int>(static_cast<int64_t>(all_units) * blockIdx.x / gridDim.x);
-    const int units = static_cast<int>(static_cast<int64_t>(all_units) * (blockIdx.x + 1) / gridDim.x) - from;
+    const int64_t all_units = static_cast<int64_t>(head->units) * a.tiles;
+    const int slices = (a.k + kSlice - 1) / kSlice;
+    Rounds round(static_cast<int>(all_units * blockIdx.x / gridDim.x), static_cast<int>(all_units * (blockIdx.x + 1) / gridDim.x),
+                 a.tiles, slices);
     uint8_t* const own = shared + at.stages + warp * a.stages * kStageBytes;
-    Stream<Product> stream(a, list, smem_addr(own), from, units);
+    const uint8_t *stage = own, *const last_stage = own + a.stages * kStageBytes;
+    Stream<Product> stream(a, list, smem_addr(own), round);
     for (int i = 0; i < a.stages; ++i) stream.ask();
     if (Product::kPairs) grid_wait_prerequisites();
     if (Product::kPairs && all_units == 0)   // nobody chose anything
@@ -561,61 +616,62 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
              i += static_cast<int64_t>(gridDim.x) * kThreads)
             a.y[i / a.dim * a.ldy + i % a.dim] = 0;
 
-    const int slices = stream.slices, pitch = Layout::pitch(a.k), low = a.passes_rows * pitch;
+    const int pitch = Layout::pitch(a.k), low = a.passes_rows * pitch;
     const bool all = !Product::kPairs && a.tokens <= a.passes_rows;
-    int item = warp, stage = 0, pair = -1;
-    bool staged = false;
-    for (int u = 0; u < units; ++u) {
-        const int p = (from + u) / a.tiles, tile = from + u - p * a.tiles;
-        if (p != pair) {
-            stage_rows<Product>(a, head, acts, masks, weights, ids, list[p], all, staged);
-            pair = p;
-            staged = all;
+    int pair = -1;
+    while (round.advance()) {
+        if (round.pair != pair) {
+            stage_rows<Product>(a, head, acts, masks, weights, ids, list[round.pair], all, all && pair >= 0);
+            pair = round.pair;
         }
-        float acc[2][kCols][4];
+        const bool wide = head->wide != 0;
+        float acc[2][kMaxPass / 8][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int n = 0; n < kCols; ++n)
+            for (int n = 0; n < kMaxPass / 8; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-        for (; item < (u + 1) * slices; item += kWarps) {
+        const uint8_t* x = acts + g * pitch + t * 16 + round.slice * (kSlice * 2);
+        for (int i = round.slice; i < round.last; ++i) {
             copies_wait(a.stages - 1);
             __syncwarp();
-            multiply<kCols, Product::kPairs>(own + stage * kStageBytes, acts + g * pitch + t * 16 + (item - u * slices) * (kSlice * 2),
-                                             pitch, low, acc);
+            if (wide) multiply<2, Product::kPairs>(stage, x, pitch, low, acc);
+            else multiply<1, Product::kPairs>(stage, x, pitch, low, acc);
             __syncwarp();
             stream.ask();
-            if (++stage == a.stages) stage = 0;
+            x += kSlice * 2;
+            stage += kStageBytes;
+            if (stage == last_stage) stage = own;
         }
-        // A warp's place is that of its slices in the unit, so that what a token's sums add up in what order does not
-        // depend on the tokens beside it.  The upper half, then the lower half with it, then the sum over eight.
-        constexpr int kWide = 8 * kCols;
-        const int place = (warp - u * slices) & (kWarps - 1);
-        float* const mine = sums + (place & (kWarps / 2 - 1)) * kUnitRows * kWide;
-#pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            if ((place >= kWarps / 2) == (half == 1)) {
+        const int cols = wide ? 2 : 1;
+        // A unit's first warp gets what the others have: at once, or in halves where 16 columns leave room for 8 warps' sums.
+        float* const sums = reinterpret_cast<float*>(shared + at.sums) + lane;
+        for (int span = round.parts; span > 1;) {
+            const int keep = wide ? span / 2 : 1, first = (warp / round.parts) * (span - keep);
+            __syncthreads();   // what was here before has been added up
+            if (round.part >= keep && round.part < span)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int n = 0; n < kCols; ++n)
+                    for (int n = 0; n < kMaxPass / 8; ++n)
+                        if (n < cols)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float2* const d = reinterpret_cast<float2*>(mine + (16 * m + 8 * h + g) * kWide + 8 * n + 2 * t);
-                            float2 v = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
-                            if (half == 0) {
-                                const float2 w = *d;
-                                v.x += w.x;
-                                v.y += w.y;
-                            }
-                            *d = v;
-                        }
-            }
+                            for (int i = 0; i < 4; ++i) sums[(((first + round.part - keep) * cols + n) * 8 + m * 4 + i) * 32] = acc[m][n][i];
             __syncthreads();
+            if (round.part < keep)
+                for (int p = round.part + keep; p < span; p += keep)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int n = 0; n < kMaxPass / 8; ++n)
+                            if (n < cols)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[m][n][i] += sums[(((first + p - keep) * cols + n) * 8 + m * 4 + i) * 32];
+            span = keep;
         }
-        finish(Product(), a, head, sums, weights, ids, tile, kWide);
-        __syncthreads();
+        if (round.part != 0) continue;
+        finish(Product(), a, head, weights, round.unit - round.pair * a.tiles, cols, acc);
     }
     copies_wait(0);
 }
@@ -632,9 +688,14 @@ int shape(ExpertsArgs* a, bool pairs) {
     return 0;
 }
 
-template <typename Product, int kCols>
-cudaError_t launch(const ExpertsArgs& a, int smem, int sms, cudaStream_t stream) {
-    const auto kernel = experts_kernel<Product, kCols>;
+template <typename Product>
+cudaError_t launch(ExpertsArgs a, int rows, int k, int sms, cudaStream_t stream) {
+    a.rows = rows;
+    a.k = k;
+    a.tiles = Product::kPairs ? 4 * ((a.dim + 127) / 128) : 8 * ((a.inner + 127) / 128);
+    const int smem = shape(&a, Product::kPairs);
+    if (smem == 0) return cudaErrorInvalidValue;
+    const auto kernel = experts_kernel<Product>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -648,16 +709,6 @@ cudaError_t launch(const ExpertsArgs& a, int smem, int sms, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
-template <typename Product>
-cudaError_t launch(ExpertsArgs a, int rows, int k, int sms, cudaStream_t stream) {
-    a.rows = rows;
-    a.k = k;
-    a.tiles = Product::kPairs ? 4 * ((a.dim + 127) / 128) : 8 * ((a.inner + 127) / 128);
-    const int smem = shape(&a, Product::kPairs);
-    if (smem == 0) return cudaErrorInvalidValue;
-    return a.passes_rows == 8 ? launch<Product, 1>(a, smem, sms, stream) : launch<Product, 2>(a, smem, sms, stream);
 }
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

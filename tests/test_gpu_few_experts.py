@@ -232,13 +232,13 @@ def test_fewer_tokens_than_the_layer_takes(used):
     assert layer.forward(p.x[:0], p.logits[:0], *p.up, *p.down).shape == (0, 256)
 
 
-def test_a_tokens_output_does_not_depend_on_the_batch():
-    # a token's products are summed in the same order whoever is beside it, as long as the pass is as wide
+def test_a_token_alone_and_in_its_batch():
     p = Problem(8, 10, 3, 256, 128, seed=21)
     layer = p.layer()
-    y = p.run(layer).clone()
-    for t in range(8):
-        assert torch.equal(layer.forward(p.x[t:t + 1], p.logits[t:t + 1], *p.up, *p.down), y[t:t + 1])
+    want, tol = p.want()
+    for t in range(8):   # the sums' order goes by the batch, the value does not
+        err = np.abs(f64(layer.forward(p.x[t:t + 1], p.logits[t:t + 1], *p.up, *p.down)) - want[t:t + 1])
+        assert np.all(err <= tol[t] + 2.0 ** -8 * (np.abs(want[t]) + tol[t]))
 
 
 @pytest.mark.parametrize("tokens", [1, 24])
