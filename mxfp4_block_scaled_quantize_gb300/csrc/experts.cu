@@ -24,8 +24,8 @@
 // copies of its own, across the ends of its units.
 //   Rows of a unit: 32 q + i for q = 0 .. 3 and a few consecutive i of a group of 128, so that their scales (16 bytes for the
 //   four q of one i in the scale layout) are consecutive too.
-//   The sum over experts: each unit of the second product leaves its rows, weighted, in fp32; the warp that
-//   leaves the last one for 32 columns adds them up in the order of the tokens' choices.  No CTA waits for another, and the
+//   The sum over experts: each unit of the second product leaves its rows, weighted, in fp32; the CTA that
+//   leaves the last one for 32 columns adds them up in the order of the tokens' choices, when it is done with its units.  No CTA waits for another, and the
 //   order of additions is fixed by the call's routing.
 //
 // The routing is so little work (64 tokens of 64 experts: 1 us) that every CTA does it for itself; the second kernel does
@@ -46,7 +46,6 @@ constexpr int kUnitRows = 32;
 constexpr int kSlice = 128;                              // elements of a row
 constexpr int kSliceBytes = kUnitRows * kSlice / 2;      // codes
 constexpr int kStageBytes = kSliceBytes + 4 * kUnitRows; // and a word of four scales for each row
-constexpr int kMaxStages = 4;
 constexpr int kMaxPass = 16;                             // routed rows of a pass
 constexpr int kSharedMost = 227 * 1024;
 
@@ -57,28 +56,34 @@ struct Row {           // of a pass
     float weight;
 };
 
-// Shared memory: this head, then [experts] masks, [tokens * top_k] weights and experts, [experts] used experts,
-// the activations, the unit's sums and the warps' stages.
+// Shared memory: this head, then [experts] masks, [tokens * top_k] weights and experts, the list of (expert, pass),
+// [tiles] the queue of finished tiles, the activations, the units' sums, the warps' scales and their stages.
 struct Head {
     Row rows[kMaxPass];
-    int32_t units;     // (expert, pass) pairs
+    int32_t narrow;    // (expert, pass) pairs of up to 8 rows,
+    int32_t pairs;     // and all of them
     int32_t wide;      // the pass has more than 8 rows
+    int32_t queued;    // of the tiles whose last unit one of this CTA's warps left
+    uint32_t top[kMaxPass];   // largest magnitudes of the pass's activations, as bits
 };
 
 __host__ __device__ inline int align16(int n) { return (n + 15) & ~15; }
 
 struct Layout {
-    int masks, weights, ids, list, acts, sums, stages, total;
-    __host__ __device__ Layout(int experts, int tokens, int top_k, int k, int pass_rows, bool pairs, int stage_count) {
+    int masks, weights, ids, list, list_size, queue, acts, sums, scales, stages, total;
+    __host__ __device__ Layout(int experts, int tokens, int top_k, int k, int tiles, int pass_rows, bool pairs, int stage_count) {
         const int choices = tokens * top_k;
         masks = align16(sizeof(Head));
         weights = masks + align16(8 * experts);
         ids = weights + align16(4 * choices);
         list = ids + align16(2 * choices);
         // an expert's passes: one, and one more for every further pass_rows of its tokens
-        acts = list + align16(4 * ((experts < choices ? experts : choices) + choices / pass_rows));
+        list_size = (experts < choices ? experts : choices) + choices / pass_rows;
+        queue = list + align16(4 * list_size);
+        acts = queue + (pairs ? align16(2 * tiles) : 0);
         sums = acts + pass_rows * pitch(k) * (pairs ? 2 : 1);
-        stages = sums + kWarps / 2 * kUnitRows * kMaxPass * 4;
+        scales = sums + kWarps / 2 * kUnitRows * kMaxPass * 4;
+        stages = scales + kWarps * kUnitRows * 16;
         total = stages + kWarps * stage_count * kStageBytes;
     }
     // Bytes from one row of the activations to the next: 64 more than a multiple of 128, so that the 16-byte
@@ -86,19 +91,18 @@ struct Layout {
     __host__ __device__ static int pitch(int k) { return 2 * ((k + kSlice - 1) / kSlice * kSlice) + 64; }
 };
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+// Of the 16 (4) bytes that these write, the first `bytes` are read, the others zero.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Until at most `left` (0 .. 3) of this thread's groups are under way.
-__device__ __forceinline__ void copies_wait(int left) {
-    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+// Until at most kLeft of this thread's groups are under way.
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // Eight codes as four pairs of fp16.
@@ -122,10 +126,9 @@ __device__ __forceinline__ void mma_first(float* c, uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// 2^(byte - 127) for byte b of w.
-__device__ __forceinline__ float scale_of(uint32_t w, int b) {
-    const uint32_t e = (b < 3 ? w << (23 - 8 * b) : w >> 1) & 0x7F800000u;
-    return __uint_as_float(e > 0x00400000u ? e : 0x00400000u);
+// 2^(byte - 127) for byte b of w, as bits.
+__device__ __forceinline__ uint32_t scale_of(uint32_t w, int b) {
+    return max((b < 3 ? w << (23 - 8 * b) : w >> 1) & 0x7F800000u, 0x00400000u);
 }
 
 __device__ __forceinline__ uint32_t max_all(uint32_t v) {
@@ -150,34 +153,43 @@ __device__ __forceinline__ float logit_of(const ExpertsArgs& a, int64_t t, int e
                         : __uint_as_float(static_cast<uint32_t>(__ldcg(static_cast<const uint16_t*>(a.logits) + i)) << 16);
 }
 
-// The choices of a warp's tokens.  kPer: 32 kPer experts at most.  Order: value, then lowest index; a NaN is
-// above all values, as in a sort.
-template <int kPer>
-__device__ void choose(const ExpertsArgs& a, unsigned long long* masks, float* weights, uint16_t* ids) {
+// The choices of kTokens tokens from t on (those below a.tokens).  kPer: 32 kPer experts at most.  Order: value, then lowest
+// index; a NaN is above all values, as in a sort.  Several tokens' chains of warp-wide steps run beside each other.
+template <int kPer, int kTokens>
+__device__ __forceinline__ void choose(const ExpertsArgs& a, int t, unsigned long long* masks, float* weights, uint16_t* ids) {
     const int lane = static_cast<int>(lane_id());
-    for (int t = threadIdx.x >> 5; t < a.tokens; t += kWarps) {
-        float v[kPer];
-        uint32_t key[kPer];
+    const float none = __int_as_float(0xFF800000);
+    float v[kTokens][kPer];
+    uint32_t key[kTokens][kPer];
+#pragma unroll
+    for (int x = 0; x < kTokens; ++x)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = i * 32 + lane;
-            v[i] = e < a.experts ? logit_of(a, t, e) : 0.0f;
+            v[x][i] = e < a.experts && t + x < a.tokens ? logit_of(a, t + x, e) : 0.0f;
         }
 #pragma unroll
+    for (int x = 0; x < kTokens; ++x)
+#pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const uint32_t u = __float_as_uint(v[i] + 0.0f);   // one zero
-            key[i] = v[i] != v[i] ? 0xFFFFFFFFu : u & 0x80000000u ? ~u : u | 0x80000000u;
-            if (i * 32 + lane >= a.experts) key[i] = 0u;       // below every value
+            const uint32_t u = __float_as_uint(v[x][i] + 0.0f);   // one zero
+            key[x][i] = v[x][i] != v[x][i] ? 0xFFFFFFFFu : u & 0x80000000u ? ~u : u | 0x80000000u;
+            if (i * 32 + lane >= a.experts) key[x][i] = 0u;       // below every value
         }
-        float mine = 0.0f, top = 0.0f;   // lane j: the value of choice j
-        int id = 0;
-        for (int j = 0; j < a.top_k; ++j) {
+    float mine[kTokens], top[kTokens];   // lane j: the value of choice j
+    int id[kTokens];
+#pragma unroll
+    for (int x = 0; x < kTokens; ++x) mine[x] = top[x] = 0.0f, id[x] = 0;
+#pragma unroll 1
+    for (int j = 0; j < a.top_k; ++j)
+#pragma unroll
+        for (int x = 0; x < kTokens; ++x) {
             uint32_t best = 0u;
             int at = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                if (key[i] > best) {
-                    best = key[i];
+                if (key[x][i] > best) {
+                    best = key[x][i];
                     at = i;
                 }
             const uint32_t most = max_all(best);
@@ -186,63 +198,95 @@ __device__ void choose(const ExpertsArgs& a, unsigned long long* masks, float* w
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 if (i * 32 + lane == e) {
-                    key[i] = 0u;
-                    value = v[i];
+                    key[x][i] = 0u;
+                    value = v[x][i];
                 }
             value = __shfl_sync(0xFFFFFFFFu, value, e & 31);
-            if (j == 0) top = value;
+            if (j == 0) top[x] = value;
             if (lane == j) {
-                mine = value;
-                id = e;
+                mine[x] = value;
+                id[x] = e;
             }
         }
-        const float none = __int_as_float(0xFF800000);
-        const float p = lane < a.top_k && mine != none ? expf(mine - top) : 0.0f;
+#pragma unroll
+    for (int x = 0; x < kTokens; ++x) {
+        const float p = lane < a.top_k && mine[x] != none ? expf(mine[x] - top[x]) : 0.0f;
         float sum = p;
         if (!a.normalize) {
             sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                if (i * 32 + lane < a.experts && v[i] != none) sum += expf(v[i] - top);
+                if (i * 32 + lane < a.experts && v[x][i] != none) sum += expf(v[x][i] - top[x]);
         }
         sum = sum_all(sum);
-        if (lane < a.top_k) {
+        if (lane < a.top_k && t + x < a.tokens) {
             const float w = sum == 0.0f ? 0.0f : p / sum;   // 0: every logit is -inf
-            weights[t * a.top_k + lane] = w;
-            ids[t * a.top_k + lane] = static_cast<uint16_t>(id);
-            if (w != 0.0f) atomicOr(&masks[id], 1ull << t);   // not where it changes nothing
+            weights[(t + x) * a.top_k + lane] = w;
+            ids[(t + x) * a.top_k + lane] = static_cast<uint16_t>(id[x]);
+            if (w != 0.0f) atomicOr(&masks[id[x]], 1ull << (t + x));   // not where it changes nothing
         }
     }
 }
 
-// The routing: each expert's tokens, and the list of (expert, pass) pairs that have any.
-__device__ void route(const ExpertsArgs& a, Head* head, unsigned long long* masks, float* weights, uint16_t* ids, uint32_t* list) {
+// The routing: each expert's tokens, and the list of (expert, pass) pairs that have any: those of up to 8 rows from its front
+// on, the others from its back on.
+__device__ void route(const ExpertsArgs& a, Head* head, unsigned long long* masks, float* weights, uint16_t* ids, uint32_t* list, int list_size) {
     for (int e = threadIdx.x; e < a.experts; e += kThreads) masks[e] = 0ull;
     __syncthreads();
-    if (a.experts <= 64) choose<2>(a, masks, weights, ids);
-    else if (a.experts <= 256) choose<8>(a, masks, weights, ids);
-    else choose<32>(a, masks, weights, ids);
+    const int warp = threadIdx.x >> 5;
+    if (a.experts <= 64) {
+        if (a.tokens <= kWarps) {
+            if (warp < a.tokens) choose<2, 1>(a, warp, masks, weights, ids);
+        } else {
+#pragma unroll 1
+            for (int t = 2 * warp; t < a.tokens; t += 2 * kWarps) choose<2, 2>(a, t, masks, weights, ids);
+        }
+    } else if (a.experts <= 256) {
+#pragma unroll 1
+        for (int t = warp; t < a.tokens; t += kWarps) choose<8, 1>(a, t, masks, weights, ids);
+    } else {
+#pragma unroll 1
+        for (int t = warp; t < a.tokens; t += kWarps) choose<32, 1>(a, t, masks, weights, ids);
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = static_cast<int>(lane_id());
-        int units = 0;
+        if (lane == 0) head->queued = 0;
+        int before = 0;   // pairs of the experts before: narrow ones, and 2^16 times the wide ones
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
             const int e = e0 + lane;
             const int n = e < a.experts ? __popcll(masks[e]) : 0;
-            const int passes = (n + a.passes_rows - 1) / a.passes_rows;
-            int before = passes;   // inclusive sum over the lanes
+            const int full = n / a.passes_rows, rest = n - full * a.passes_rows;
+            const int wide = a.passes_rows > 8 ? full + (rest > 8) : 0;
+            const int mine = (full + (rest > 0) - wide) | wide << 16;
+            int sum = mine;   // inclusive over the lanes
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int up = __shfl_up_sync(0xFFFFFFFFu, before, d);
-                if (lane >= d) before += up;
+                const int up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d) sum += up;
             }
-            for (int p = 0; p < passes; ++p) list[units + before - passes + p] = static_cast<uint32_t>(e) | static_cast<uint32_t>(p) << 16;
-            units += __shfl_sync(0xFFFFFFFFu, before, 31);
+            int at = before + sum - mine;
+            for (int p = 0; p < full + (rest > 0); ++p) {
+                const bool is_wide = p < wide;   // full passes first, the one with the rest last
+                list[is_wide ? list_size - 1 - (at >> 16) : at & 0xFFFF] = static_cast<uint32_t>(e) | static_cast<uint32_t>(p) << 16;
+                at += is_wide ? 1 << 16 : 1;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
-        if (lane == 0) head->units = units;
+        if (lane == 0) {
+            head->narrow = before & 0xFFFF;
+            head->pairs = (before & 0xFFFF) + (before >> 16);
+        }
     }
     __syncthreads();
 }
+
+// Pair p of the list, those of up to 8 rows first.
+struct Pairs {
+    const uint32_t* list;
+    int size, narrow;
+    __device__ __forceinline__ uint32_t operator[](int p) const { return list[p < narrow ? p : size - 1 - (p - narrow)]; }
+};
 
 // What each of the two kernels multiplies.
 struct Up {
@@ -296,19 +340,19 @@ struct Rounds {
 };
 
 // A warp's slices on their way to shared memory, in the order in which it takes them.
-template <typename Product>
+template <typename Product, int kStages>
 struct Stream {
     const ExpertsArgs& a;
-    const uint32_t* list;
+    Pairs list;
     uint32_t to, end_to, d;   // the warp's stages, and the next one to be filled
     Rounds r;
     bool more;
     const uint8_t* q[4];      // this lane's piece of four rows
     const uint8_t* s;         // and its row's scales
-    uint32_t there;           // which of the rows there are; bit 4: the scales' row
+    int bytes[5];             // to copy of each: none where there is no row
 
-    __device__ __forceinline__ Stream(const ExpertsArgs& args, const uint32_t* l, uint32_t stages, const Rounds& rounds)
-        : a(args), list(l), to(stages), end_to(stages + args.stages * kStageBytes), d(stages), r(rounds) {
+    __device__ __forceinline__ Stream(const ExpertsArgs& args, const Pairs& l, uint32_t stages, const Rounds& rounds)
+        : a(args), list(l), to(stages), end_to(stages + kStages * kStageBytes), d(stages), r(rounds) {
         advance();
     }
     // To the next round with slices for this warp.
@@ -319,16 +363,15 @@ struct Stream {
         const int tile = r.unit - r.pair * a.tiles, lane = static_cast<int>(lane_id());
         const int64_t e = list[r.pair] & 0xFFFFu;
         const int64_t pitch = static_cast<int64_t>(r.slices) * (kSlice / 2);
-        there = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = Product::row(a, tile, 8 * i + (lane >> 2));
-            if (row >= 0) there |= 1u << i;
+            bytes[i] = row < 0 ? 0 : 16;
             q[i] = a.q + (row < 0 ? 0 : (e * a.rows + row) * pitch + r.slice * (kSlice / 2) + (lane & 3) * 16);
         }
         const int row = Product::row(a, tile, lane);
         const int64_t atom = (e * ((a.rows + 127) / 128) + row / 128) * r.slices + r.slice;
-        if (row >= 0) there |= 16u;
+        bytes[4] = row < 0 ? 0 : 4;
         s = a.s + (row < 0 ? 0 : atom * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4);
     }
     // Asks for the next slice, or for nothing: a group of copies either way.
@@ -339,11 +382,11 @@ struct Stream {
             const uint32_t at = d + static_cast<uint32_t>((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                copy16(at + 512 * i, q[i], there >> i & 1u);
-                q[i] += there >> i & 1u ? kSlice / 2 : 0;
+                copy16(at + 512 * i, q[i], bytes[i]);
+                q[i] += kSlice / 2;
             }
-            copy4(d + static_cast<uint32_t>(kSliceBytes + 4 * lane), s, there >> 4 & 1u);
-            s += there >> 4 & 1u ? 512 : 0;
+            copy4(d + static_cast<uint32_t>(kSliceBytes + 4 * lane), s, bytes[4]);
+            s += 512;
             d += kStageBytes;
             if (d == end_to) d = to;
             if (++r.slice == r.last) advance();
@@ -354,16 +397,25 @@ struct Stream {
 
 // The unit's sums so far += one slice.  acts: this lane's place in the activations (row g, 16 bytes t of the slice's first
 // block), `low` bytes further their low parts.
-template <int kCols, bool kPairs>
-__device__ __forceinline__ void multiply(const uint8_t* stage, const uint8_t* acts, int pitch, int low, float (*acc)[kMaxPass / 8][4]) {
-    const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
-    const uint32_t* const words = reinterpret_cast<const uint32_t*>(stage + kSliceBytes);
-    uint32_t sw[2][2];
+template <int kCols, bool kPairs, int kMost>
+__device__ __forceinline__ void multiply(const uint8_t* stage, float4* scales, const uint8_t* acts, int pitch, int low,
+                                         float (*acc)[kMost][4]) {
+    const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+    // each lane turns one row's four bytes into factors, for all (48 instructions less than each for itself)
+    const uint32_t w = reinterpret_cast<const uint32_t*>(stage + kSliceBytes)[lane];
+    reinterpret_cast<uint4*>(scales)[lane] = make_uint4(scale_of(w, 0), scale_of(w, 1), scale_of(w, 2), scale_of(w, 3));
+    __syncwarp();
+    float by[2][2][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        sw[m][0] = words[16 * m + g];
-        sw[m][1] = words[16 * m + g + 8];
-    }
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 f = scales[16 * m + 8 * h + g];
+            by[m][h][0] = f.x;
+            by[m][h][1] = f.y;
+            by[m][h][2] = f.z;
+            by[m][h][3] = f.w;
+        }
     const uint8_t* const codes = stage + g * 64 + t * 4;
     const int turn = ((g >> 1) & 3) << 4;
 #pragma unroll
@@ -379,7 +431,7 @@ __device__ __forceinline__ void multiply(const uint8_t* stage, const uint8_t* ac
             uint32_t lo[4], hi[4];
             decode8(*reinterpret_cast<const uint32_t*>(codes + 1024 * m + ((b << 4) ^ turn)), lo);
             decode8(*reinterpret_cast<const uint32_t*>(codes + 1024 * m + 512 + ((b << 4) ^ turn)), hi);
-            const float s0 = scale_of(sw[m][0], b), s1 = scale_of(sw[m][1], b);
+            const float s0 = by[m][0][b], s1 = by[m][1][b];
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
                 float p[4];
@@ -474,54 +526,82 @@ __device__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, cons
         head->rows[n].token = token;
         head->rows[n].slot = slot;
         head->rows[n].weight = slot >= 0 ? weights[slot] : 0.0f;
+        if (!staged) head->top[n] = 0u;
         if (n == rows - 1) head->wide = rows > 8 && (all ? a.tokens : __popcll(masks[e]) - pass * rows) > 8;
     }
     __syncthreads();
     if (!staged) {
-        const int lane = static_cast<int>(lane_id());
-        for (int n = threadIdx.x >> 5; n < rows; n += kWarps) {
+        // All threads over the rows' groups of 8: the largest magnitudes (whose order does not matter), then the values, with up
+        // to kHeld groups of a thread in registers in between; those beyond are read twice.
+        constexpr int kHeld = Product::kPairs ? 2 : 4;
+        const int groups = (pitch - 64) / 16;
+        int last = rows;   // rows that there are: what the others' columns give is not used
+        if (!all) last = min(rows, __popcll(masks[e]) - pass * rows);
+        else last = a.tokens;
+        const int all_groups = last * groups;
+        auto load = [&](int i, float* f) {
+            const int n = i / groups, c = 8 * (i - n * groups);
             const int64_t row = Product::kPairs ? head->rows[n].slot : head->rows[n].token;
-            uint4* const to = reinterpret_cast<uint4*>(acts + n * pitch);
-            const int groups = (pitch - 64) / 16;   // of 8 elements
-            if (row < 0) {
-                for (int c = lane; c < groups; c += 32) {
-                    to[c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (Product::kPairs) to[rows * pitch / 16 + c] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                if (lane == 0) head->rows[n].back = 0.0f;
-                continue;
-            }
-            const bool wide = Product::kPairs
-                                  ? a.inner % 8 == 0
-                                  : a.k % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.x + row * a.ldx)) & 15u) == 0;
-            float top = 0.0f, f[8];
-            for (int c = lane; c < groups; c += 32) {
-                if (Product::kPairs) h8(a, row, 8 * c, wide, f);
-                else x8(a, row, 8 * c, wide, f);
+            if (Product::kPairs) h8(a, row, c, a.inner % 8 == 0, f);
+            else x8(a, row, c, a.k % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x + row * a.ldx) & 15u) == 0, f);
+        };
+        auto largest = [&](int i, const float* f) {
+            float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_or_zero(f[i]));
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_or_zero(f[j]));
+            uint32_t bits = __float_as_uint(top);
+            if (groups % 32 == 0) {   // a warp's groups are of one row
+                bits = max_all(bits);
+                if (lane_id() != 0) return;
             }
-            top = __uint_as_float(max_all(__float_as_uint(top)));
+            atomicMax(&head->top[i / groups], bits);
+        };
+        auto place = [&](int i, const float* f) {
+            const int n = i / groups;
             float back;
-            const float up = lift(top, &back);
-            if (lane == 0) head->rows[n].back = back;
-            for (int c = lane; c < groups; c += 32) {
-                if (Product::kPairs) h8(a, row, 8 * c, wide, f);
-                else x8(a, row, 8 * c, wide, f);
-                uint32_t w[4], l[4];
+            const float up = lift(__uint_as_float(head->top[n]), &back);
+            uint32_t w[4], l[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = f[2 * i] * up, q = f[2 * i + 1] * up;
-                    w[i] = half2_of(p, q);
-                    if (Product::kPairs) {
-                        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                        const float inf = __int_as_float(0x7F800000);
-                        l[i] = half2_of(fabsf(h.x) < inf ? p - h.x : 0.0f, fabsf(h.y) < inf ? q - h.y : 0.0f);
-                    }
+            for (int j = 0; j < 4; ++j) {
+                const float p = f[2 * j] * up, q = f[2 * j + 1] * up;
+                w[j] = half2_of(p, q);
+                if (Product::kPairs) {
+                    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                    const float inf = __int_as_float(0x7F800000);
+                    l[j] = half2_of(fabsf(h.x) < inf ? p - h.x : 0.0f, fabsf(h.y) < inf ? q - h.y : 0.0f);
                 }
-                to[c] = make_uint4(w[0], w[1], w[2], w[3]);
-                if (Product::kPairs) to[rows * pitch / 16 + c] = make_uint4(l[0], l[1], l[2], l[3]);
             }
+            uint4* const to = reinterpret_cast<uint4*>(acts + n * pitch) + (i - n * groups);
+            *to = make_uint4(w[0], w[1], w[2], w[3]);
+            if (Product::kPairs) to[rows * pitch / 16] = make_uint4(l[0], l[1], l[2], l[3]);
+        };
+        float held[kHeld][8];
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (threadIdx.x + h * kThreads < all_groups) load(threadIdx.x + h * kThreads, held[h]);
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (threadIdx.x + h * kThreads < all_groups) largest(threadIdx.x + h * kThreads, held[h]);
+#pragma unroll 1
+        for (int i = threadIdx.x + kHeld * kThreads; i < all_groups; i += kThreads) {
+            float f[8];
+            load(i, f);
+            largest(i, f);
+        }
+        __syncthreads();
+        if (threadIdx.x < static_cast<unsigned>(rows)) {
+            float back;
+            lift(__uint_as_float(head->top[threadIdx.x]), &back);
+            head->rows[threadIdx.x].back = back;
+        }
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (threadIdx.x + h * kThreads < all_groups) place(threadIdx.x + h * kThreads, held[h]);
+#pragma unroll 1
+        for (int i = threadIdx.x + kHeld * kThreads; i < all_groups; i += kThreads) {
+            float f[8];
+            load(i, f);
+            place(i, f);
         }
     }
     __syncthreads();
@@ -529,11 +609,12 @@ __device__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, cons
 
 // What becomes of a unit's sums, in the registers of one warp: element (row 16 m + 8 h + g, column 8 n + 2 t + c) of the
 // unit in acc[m][n][2 h + c].
-__device__ __forceinline__ void finish(Up, const ExpertsArgs& a, const Head* head, const float*, int tile, int cols,
-                                       const float (*acc)[kMaxPass / 8][4]) {
+template <int kMost>
+__device__ __forceinline__ void finish(Up, const ExpertsArgs& a, Head* head, uint16_t*, int tile, int cols,
+                                       const float (*acc)[kMost][4]) {
     const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
 #pragma unroll
-    for (int n = 0; n < kMaxPass / 8; ++n) {
+    for (int n = 0; n < kMost; ++n) {
         if (n >= cols) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -549,11 +630,12 @@ __device__ __forceinline__ void finish(Up, const ExpertsArgs& a, const Head* hea
     }
 }
 
-__device__ __forceinline__ void finish(Down, const ExpertsArgs& a, const Head* head, const float* weights, int tile, int cols,
-                                       const float (*acc)[kMaxPass / 8][4]) {
+template <int kMost>
+__device__ __forceinline__ void finish(Down, const ExpertsArgs& a, Head* head, uint16_t* queue, int tile, int cols,
+                                       const float (*acc)[kMost][4]) {
     const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < kMaxPass / 8; ++n) {
+    for (int n = 0; n < kMost; ++n) {
         if (n >= cols) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -568,50 +650,87 @@ __device__ __forceinline__ void finish(Down, const ExpertsArgs& a, const Head* h
     }
     __threadfence();
     __syncwarp();
-    uint32_t before = 0;
-    if (lane == 0) before = atomicAdd(a.done + tile, 1u);
-    if (__shfl_sync(0xFFFFFFFFu, before, 0) != static_cast<uint32_t>(head->units) - 1u) return;
-    __threadfence();
-    const int r = Down::row(a, tile, lane);
-    if (r >= 0)
-        for (int64_t at = 0; at < a.tokens; ++at) {
-            float v = 0.0f;
-            for (int j = 0; j < a.top_k; ++j) {
-                const int64_t slot = at * a.top_k + j;
-                if (weights[slot] != 0.0f) v += __ldcg(a.part + slot * a.dim + r);
-            }
-            const __nv_bfloat16 h = __float2bfloat16_rn(v);
-            a.y[at * a.ldy + r] = *reinterpret_cast<const uint16_t*>(&h);
-        }
-    if (lane == 0) a.done[tile] = 0u;
+    if (lane == 0 && atomicAdd(a.done + tile, 1u) == static_cast<uint32_t>(head->pairs) - 1u) {
+        __threadfence();
+        queue[atomicAdd(&head->queued, 1)] = static_cast<uint16_t>(tile);
+    }
 }
 
-template <typename Product>
+// The sums over the experts for the tiles in the queue: a warp for four of a tile's tokens, a lane for each of its columns.
+__device__ __forceinline__ void join(const ExpertsArgs& a, const Head* head, const uint16_t* queue, const float* weights) {
+    constexpr int kTogether = 4;
+    const int lane = static_cast<int>(lane_id()), fours = (a.tokens + kTogether - 1) / kTogether;
+#pragma unroll 1
+    for (int i = threadIdx.x >> 5; i < head->queued * fours; i += kWarps) {
+        const int tile = queue[i / fours], t = i % fours * kTogether, r = Down::row(a, tile, lane);
+        if (t == 0 && lane == 0) a.done[tile] = 0u;
+        if (r < 0) continue;
+        const int choices = min(kTogether, a.tokens - t) * a.top_k;
+        const float* const p = a.part + static_cast<int64_t>(t) * a.top_k * a.dim + r;
+        const float* const w = weights + t * a.top_k;
+        float sum[kTogether] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int j = 0; j < a.top_k; j += 4) {
+            float v[4][kTogether];   // all under way together; what no warp has left is not read
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int x = 0; x < kTogether; ++x) {
+                    const int c = x * a.top_k + j + q;
+                    v[q][x] = j + q < a.top_k && c < choices && w[c] != 0.0f ? __ldcg(p + static_cast<int64_t>(c) * a.dim) : 0.0f;
+                }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int x = 0; x < kTogether; ++x) sum[x] += v[q][x];
+        }
+#pragma unroll
+        for (int x = 0; x < kTogether; ++x) {
+            const __nv_bfloat16 h = __float2bfloat16_rn(sum[x]);
+            if (t + x < a.tokens) a.y[(t + x) * a.ldy + r] = *reinterpret_cast<const uint16_t*>(&h);
+        }
+    }
+}
+
+// A wide unit takes 1.6 times as long as one of up to 8 rows.
+constexpr uint32_t kNarrowCost = 5, kWideCost = 8;
+
+// The unit at which CTA `cta` starts, so that all have the same to do.
+__device__ __forceinline__ int range_start(const Head* head, int tiles, uint32_t cta) {
+    const uint32_t narrow = static_cast<uint32_t>(head->narrow * tiles), all = static_cast<uint32_t>(head->pairs * tiles);
+    // below 2^32: at most 2^11 pairs of 300 tiles on 152 SMs
+    const uint32_t at = (narrow * kNarrowCost + (all - narrow) * kWideCost) * cta / gridDim.x;
+    return static_cast<int>(at < narrow * kNarrowCost ? at / kNarrowCost : narrow + (at - narrow * kNarrowCost) / kWideCost);
+}
+
+// kMost: 8 kMost rows in a pass at most.
+template <typename Product, int kStages, int kMost>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a) {
     extern __shared__ __align__(16) uint8_t shared[];
-    const Layout at(a.experts, a.tokens, a.top_k, a.k, a.passes_rows, Product::kPairs, a.stages);
+    const Layout at(a.experts, a.tokens, a.top_k, a.k, a.tiles, a.passes_rows, Product::kPairs, kStages);
     Head* const head = reinterpret_cast<Head*>(shared);
     unsigned long long* const masks = reinterpret_cast<unsigned long long*>(shared + at.masks);
     float* const weights = reinterpret_cast<float*>(shared + at.weights);
     uint16_t* const ids = reinterpret_cast<uint16_t*>(shared + at.ids);
     uint32_t* const list = reinterpret_cast<uint32_t*>(shared + at.list);
+    uint16_t* const queue = reinterpret_cast<uint16_t*>(shared + at.queue);
     uint8_t* const acts = shared + at.acts;
     const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+    float4* const scales = reinterpret_cast<float4*>(shared + at.scales) + warp * kUnitRows;
+    uint8_t* const own = shared + at.stages + warp * kStages * kStageBytes;
+    const uint8_t *stage = own, *const last_stage = own + kStages * kStageBytes;
 
     // The second kernel starts when every CTA of the first has passed its wait: what came before the call is complete.
     if (!Product::kPairs) grid_wait_prerequisites();
     grid_launch_dependents();
-    route(a, head, masks, weights, ids, list);
-    const int64_t all_units = static_cast<int64_t>(head->units) * a.tiles;
-    const int slices = (a.k + kSlice - 1) / kSlice;
-    Rounds round(static_cast<int>(all_units * blockIdx.x / gridDim.x), static_cast<int>(all_units * (blockIdx.x + 1) / gridDim.x),
-                 a.tiles, slices);
-    uint8_t* const own = shared + at.stages + warp * a.stages * kStageBytes;
-    const uint8_t *stage = own, *const last_stage = own + a.stages * kStageBytes;
-    Stream<Product> stream(a, list, smem_addr(own), round);
-    for (int i = 0; i < a.stages; ++i) stream.ask();
+    route(a, head, masks, weights, ids, list, at.list_size);
+    Rounds round(range_start(head, a.tiles, blockIdx.x), range_start(head, a.tiles, blockIdx.x + 1), a.tiles, (a.k + kSlice - 1) / kSlice);
+    const Pairs pairs{list, at.list_size, head->narrow};
+    Stream<Product, kStages> stream(a, pairs, smem_addr(own), round);
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) stream.ask();
     if (Product::kPairs) grid_wait_prerequisites();
-    if (Product::kPairs && all_units == 0)   // nobody chose anything
+    if (Product::kPairs && head->pairs == 0)   // nobody chose anything
         for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<int64_t>(a.tokens) * a.dim;
              i += static_cast<int64_t>(gridDim.x) * kThreads)
             a.y[i / a.dim * a.ldy + i % a.dim] = 0;
@@ -621,32 +740,34 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     int pair = -1;
     while (round.advance()) {
         if (round.pair != pair) {
-            stage_rows<Product>(a, head, acts, masks, weights, ids, list[round.pair], all, all && pair >= 0);
+            stage_rows<Product>(a, head, acts, masks, weights, ids, pairs[round.pair], all, all && pair >= 0);
             pair = round.pair;
         }
-        const bool wide = head->wide != 0;
-        float acc[2][kMaxPass / 8][4];
+        const bool wide = kMost > 1 && head->wide != 0;
+        float acc[2][kMost][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int n = 0; n < kMaxPass / 8; ++n)
+            for (int n = 0; n < kMost; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
         const uint8_t* x = acts + g * pitch + t * 16 + round.slice * (kSlice * 2);
+#pragma unroll 1
         for (int i = round.slice; i < round.last; ++i) {
-            copies_wait(a.stages - 1);
+            copies_wait<kStages - 1>();
             __syncwarp();
-            if (wide) multiply<2, Product::kPairs>(stage, x, pitch, low, acc);
-            else multiply<1, Product::kPairs>(stage, x, pitch, low, acc);
+            if (wide) multiply<kMost, Product::kPairs>(stage, scales, x, pitch, low, acc);
+            else multiply<1, Product::kPairs>(stage, scales, x, pitch, low, acc);
             __syncwarp();
             stream.ask();
             x += kSlice * 2;
             stage += kStageBytes;
             if (stage == last_stage) stage = own;
         }
-        const int cols = wide ? 2 : 1;
+        const int cols = wide ? kMost : 1;
         // A unit's first warp gets what the others have: at once, or in halves where 16 columns leave room for 8 warps' sums.
         float* const sums = reinterpret_cast<float*>(shared + at.sums) + lane;
+#pragma unroll 1
         for (int span = round.parts; span > 1;) {
             const int keep = wide ? span / 2 : 1, first = (warp / round.parts) * (span - keep);
             __syncthreads();   // what was here before has been added up
@@ -654,48 +775,56 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int n = 0; n < kMaxPass / 8; ++n)
+                    for (int n = 0; n < kMost; ++n)
                         if (n < cols)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) sums[(((first + round.part - keep) * cols + n) * 8 + m * 4 + i) * 32] = acc[m][n][i];
             __syncthreads();
             if (round.part < keep)
+#pragma unroll 1
                 for (int p = round.part + keep; p < span; p += keep)
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int n = 0; n < kMaxPass / 8; ++n)
+                        for (int n = 0; n < kMost; ++n)
                             if (n < cols)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) acc[m][n][i] += sums[(((first + p - keep) * cols + n) * 8 + m * 4 + i) * 32];
             span = keep;
         }
         if (round.part != 0) continue;
-        finish(Product(), a, head, weights, round.unit - round.pair * a.tiles, cols, acc);
+        finish<kMost>(Product(), a, head, queue, round.unit - round.pair * a.tiles, cols, acc);
     }
-    copies_wait(0);
+    copies_wait<0>();
+    if (Product::kPairs) {
+        __syncthreads();
+        join(a, head, queue, weights);
+    }
 }
 
 // Sets passes and stages for the kernel of `a`, and gives its shared memory, or 0 where it does not fit.
 int shape(ExpertsArgs* a, bool pairs) {
     for (int cols = a->tokens <= 8 ? 1 : 2; cols >= 1; --cols) {
         a->passes_rows = 8 * cols;
-        for (a->stages = kMaxStages; a->stages >= 2; --a->stages) {
-            const Layout l(a->experts, a->tokens, a->top_k, a->k, a->passes_rows, pairs, a->stages);
+        for (a->stages = 4; a->stages >= 2; a->stages -= 2) {
+            const Layout l(a->experts, a->tokens, a->top_k, a->k, a->tiles, a->passes_rows, pairs, a->stages);
             if (l.total <= kSharedMost) return l.total;
         }
     }
     return 0;
 }
 
+inline int tiles_of(int columns, bool pairs) { return (pairs ? 4 : 8) * ((columns + 127) / 128); }
+
 template <typename Product>
 cudaError_t launch(ExpertsArgs a, int rows, int k, int sms, cudaStream_t stream) {
     a.rows = rows;
     a.k = k;
-    a.tiles = Product::kPairs ? 4 * ((a.dim + 127) / 128) : 8 * ((a.inner + 127) / 128);
+    a.tiles = tiles_of(Product::kPairs ? a.dim : a.inner, Product::kPairs);
     const int smem = shape(&a, Product::kPairs);
     if (smem == 0) return cudaErrorInvalidValue;
-    const auto kernel = experts_kernel<Product>;
+    const auto kernel = a.passes_rows == 8 ? (a.stages == 4 ? experts_kernel<Product, 4, 1> : experts_kernel<Product, 2, 1>)
+                                           : (a.stages == 4 ? experts_kernel<Product, 4, 2> : experts_kernel<Product, 2, 2>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -726,6 +855,7 @@ bool sizes_ok(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim, int64
     a.k = static_cast<int32_t>(dim);
     if (shape(&a, false) == 0) return false;
     a.k = static_cast<int32_t>(inner);
+    a.tiles = tiles_of(static_cast<int>(dim), true);
     return shape(&a, true) != 0;
 }
 

@@ -33,7 +33,7 @@ struct ExpertsArgs {
     int32_t k;                 // their length,
     int32_t tiles;             // units in an expert's rows,
     int32_t passes_rows;       // routed rows that one pass over the weights takes
-    int32_t stages;            // slices on their way to shared memory, for each warp
+    int32_t stages;            // slices on their way to shared memory, for each warp: 2 or 4
 };
 
 }  // namespace mxfp4
