@@ -499,10 +499,10 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const voi
 
 /* ---- a layer of experts for a few tokens --------------------------------------------------
  * y_t = sum over token t's chosen experts e of w_e W2_e . (silu(g) u), [g; u] = W1_e . x_t, silu(g) = g / (1 + exp(-g)), in
- * two kernels: the top_k experts with the largest logits (equal ones: the lowest index first; a NaN counts as the
- * largest), w_e = softmax(logits)_e, divided by the sum of the chosen ones with MXFP4_EXPERTS_NORMALIZE.  An expert whose
- * weight is zero (a logit of -inf, or far enough below the largest) is not computed and adds nothing; a token whose
- * logits are all -inf (a row that pads a batch) gets zeros.
+ * one kernel (a cooperative launch): the top_k experts with the largest logits (equal ones: the lowest index first; a NaN
+ * counts as the largest), w_e = softmax(logits)_e, divided by the sum of the chosen ones with MXFP4_EXPERTS_NORMALIZE.  An
+ * expert whose weight is zero (a logit of -inf, or far enough below the largest) is not computed and adds nothing; a token
+ * whose logits are all -inf (a row that pads a batch) gets zeros.
  *   x, y       bf16 [tokens, dim], row pitches ldx, ldy (>= dim), tokens 0 .. MXFP4_EXPERTS_MAX_TOKENS; y must not overlap x
  *   logits     [tokens, experts], bf16 or (MXFP4_EXPERTS_LOGITS_F32) fp32, row pitch ldl (>= experts)
  *              x, y and logits aligned to their elements; of one row the pitches are not read
@@ -512,7 +512,7 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const voi
  *   sizes      experts 1 .. MXFP4_MAX_GROUPS, top_k 1 .. min(experts, MXFP4_EXPERTS_MAX_TOP_K); dim and inner as far as the
  *              activations of 8 routed rows fit the shared memory: up to 7500 and 4000 whatever the rest
  *              (mxfp4_experts_workspace_bytes tells: it refuses what the call refuses)
- *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned; its first 4 * ceil(dim / 128) words are zero before the first use
+ *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned; its first 256 bytes are zero before the first use
  *              (a call leaves them zero); calls that share one are ordered one after the other, as are replays of
  *              graphs that hold them
  * x, the weights and the sums are not rounded on the way: the products are those of the values that the blobs stand for, in

@@ -1,5 +1,5 @@
 // launch_experts.h -- internal interface of the few tokens' layer of experts between its C entry and its
-// kernels.
+// kernel.
 #pragma once
 
 #include <cstdint>
@@ -9,18 +9,32 @@
 
 namespace mxfp4 {
 
+// Head of the workspace: where the grid meets, zero between calls.
+struct ExpertsSync {
+    uint32_t arrived[3];
+    uint32_t left;
+};
+
 struct ExpertsArgs {
     const uint16_t* x;         // bf16 [tokens, dim], row pitch ldx
     int64_t ldx;
     const void* logits;        // [tokens, experts], row pitch ldl
     int64_t ldl;
-    const uint8_t* q;          // codes of this kernel's weights,
-    const uint8_t* s;          // and their scales
-    float* h;                  // [tokens * top_k, inner]: the activations between the two products
-    float* part;               // [tokens * top_k, dim]: the second product's rows, weighted
-    uint32_t* done;            // a counter for each 32 columns of y, zero between calls
+    const uint8_t* up_q;       // codes and scales of W1,
+    const uint8_t* up_s;
+    const uint8_t* down_q;     // and of W2
+    const uint8_t* down_s;
     uint16_t* y;               // bf16 [tokens, dim], row pitch ldy
     int64_t ldy;
+    ExpertsSync* sync;
+    float* weights;            // [tokens * top_k]: of the choices,
+    uint16_t* ids;             // and which experts they are
+    uint16_t* lowered;         // fp16 [tokens, dim rounded up to 128]: x times a power of two for each row,
+    float* backs;              // [tokens]: which undoes it
+    float* h;                  // [tokens * top_k, inner]: the activations between the two products,
+    uint32_t* tops;            // [tokens * top_k]: their largest finite magnitudes, as bits
+    float* part;               // [tokens * top_k, dim]: the second product's rows, weighted
+    uint32_t* err;
     int32_t tokens;
     int32_t experts;
     int32_t top_k;
@@ -28,12 +42,8 @@ struct ExpertsArgs {
     int32_t inner;
     int32_t logits_f32;
     int32_t normalize;
-    // of this kernel's product
-    int32_t rows;              // rows of an expert's weights,
-    int32_t k;                 // their length,
-    int32_t tiles;             // units in an expert's rows,
-    int32_t passes_rows;       // routed rows that one pass over the weights takes
-    int32_t stages;            // slices on their way to shared memory, for each warp: 2 or 4
+    int32_t passes_rows;       // routed rows that one pass over the weights takes: 8 or 16
+    int32_t stages;            // slices on their way to shared memory, for each warp: 2 to 4
 };
 
 }  // namespace mxfp4

@@ -24,8 +24,9 @@ enum : uint32_t {
     kErrNonFinite = 1u << 7,   // not a wait: a tensorwise FP8 amax was NaN or inf
     kErrGroups = 1u << 8,      // not a wait: group offsets or a row index out of range
     kErrNorm = 1u << 9,
+    kErrExperts = 1u << 10,
 };
-constexpr uint32_t kErrWaitBits = (kErrNonFinite - 1) | kErrNorm;
+constexpr uint32_t kErrWaitBits = (kErrNonFinite - 1) | kErrNorm | kErrExperts;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -1,4 +1,4 @@
-"""A whole mixture-of-experts layer for a few tokens: routing, both products and the sum in two kernels.
+"""A whole mixture-of-experts layer for a few tokens: routing, both products and the sum in one kernel.
 
 What a decoding loop calls next to `MXFP4GroupedLinear`, which takes prompts and training steps.  From the router's
 logits it chooses each token's experts, and gives
