@@ -114,6 +114,14 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t* h) {
         : "r"(w));
 }
 
+// Words (row lane / 4, word lane % 4) of four matrices of 8 rows of 16 bytes; lane l brings the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void load_words4(uint32_t* w, uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
+}
+
 __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -485,7 +493,7 @@ struct Stream {
 // block), `low` bytes further their low parts.
 template <int kCols, bool kPairs, int kMost>
 __device__ __forceinline__ void multiply(uint8_t* shared, int stage, int scales, int acts, int pitch, int low, float (*acc)[kMost][4]) {
-    const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+    const int lane = static_cast<int>(lane_id()), g = lane >> 2;
     // each lane turns one row's four bytes into factors, for all (48 instructions less than each for itself)
     const uint32_t w = *reinterpret_cast<const uint32_t*>(shared + stage + kSliceBytes + 4 * lane);
     *reinterpret_cast<uint4*>(shared + scales + 16 * lane) = make_uint4(scale_of(w, 0), scale_of(w, 1), scale_of(w, 2), scale_of(w, 3));
@@ -501,7 +509,9 @@ __device__ __forceinline__ void multiply(uint8_t* shared, int stage, int scales,
             by[m][h][2] = f.z;
             by[m][h][3] = f.w;
         }
-    const int codes = stage + g * 64 + t * 4, turn = ((g >> 1) & 3) << 4;
+    // the block's words of rows g, g + 8, g + 16 and g + 24 of the unit: this lane's is the address of its row, lane, at the block
+    const uint32_t codes = smem_addr(shared + stage + 64 * lane);
+    const uint32_t turn = static_cast<uint32_t>((lane >> 1) & 3) << 4;
 #pragma unroll
     for (int b = 0; b < kSlice / 32; ++b) {
         uint4 x[kCols], xl[kCols];
@@ -510,11 +520,13 @@ __device__ __forceinline__ void multiply(uint8_t* shared, int stage, int scales,
             x[n] = *reinterpret_cast<const uint4*>(shared + acts + 8 * n * pitch + b * 64);
             if (kPairs) xl[n] = *reinterpret_cast<const uint4*>(shared + acts + low + 8 * n * pitch + b * 64);
         }
+        uint32_t word[4];
+        load_words4(word, codes + ((b << 4) ^ turn));
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             uint32_t lo[4], hi[4];
-            decode8(*reinterpret_cast<const uint32_t*>(shared + codes + 1024 * m + ((b << 4) ^ turn)), lo);
-            decode8(*reinterpret_cast<const uint32_t*>(shared + codes + 1024 * m + 512 + ((b << 4) ^ turn)), hi);
+            decode8(word[2 * m], lo);
+            decode8(word[2 * m + 1], hi);
             const float s0 = by[m][0][b], s1 = by[m][1][b];
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
@@ -810,7 +822,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 
 // Sets the rows of a pass and the stages, and gives the shared memory, or 0 where it does not fit.
 int shape(ExpertsArgs* a) {
-    for (int cols = a->tokens <= 8 ? 1 : 2; cols >= 1; --cols) {
+    // 16 rows where an expert has 8 on average, else 8: an expert with more than 8 is read twice then, but the others' stages
+    // have the room (64 tokens, 6 of 64, 4096 x 2048: ## us with 16, ## with 8; 2 of 8: ## and ##).
+    for (int cols = a->tokens > 8 && a->tokens * a->top_k >= 8 * a->experts ? 2 : 1; cols >= 1; --cols) {
         a->passes_rows = 8 * cols;
         for (a->stages = 4; a->stages >= 2; --a->stages) {
             const Layout l(a->experts, a->tokens, a->top_k, a->dim, a->inner, a->passes_rows, a->stages);
