@@ -45,7 +45,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kUnitRows = 32;
 constexpr int kSlice = 128;                              // elements of a row
 constexpr int kSliceBytes = kUnitRows * kSlice / 2;      // codes
-constexpr int kStageBytes = kSliceBytes + 4 * kUnitRows; // and a word of four scales for each row
+constexpr int kWordBytes = 4 * kUnitRows;                // and a word of four scales for each row
+constexpr int kMaxStages = 4;
 constexpr int kMaxPass = 16;                             // routed rows of a pass
 constexpr int kSharedMost = 227 * 1024;
 // A unit of a pass of more than 8 rows takes 1.6 times as long as one of up to 8.
@@ -59,19 +60,22 @@ struct Row {           // of a pass
 };
 
 // Shared memory: this head, then [experts] masks, [tokens * top_k] weights and experts, the list of (expert, pass),
-// the activations, the units' sums, the warps' scales and their stages.
+// the activations, the units' sums, the warps' scales, their words and (at a multiple of 512 bytes) their codes.
 struct Head {
     Row rows[kMaxPass];
     int32_t narrow;    // (expert, pass) pairs of up to 8 rows,
     int32_t pairs;     // and all of them
     int32_t wide;      // the pass has more than 8 rows
     uint32_t top;      // largest magnitude of a row of x, as bits
+    int32_t abort;     // a wait has run out
+    int32_t pad[3];
+    uint64_t full[kWarps][kMaxStages];
 };
 
 __host__ __device__ inline int align16(int n) { return (n + 15) & ~15; }
 
 struct Layout {
-    int masks, weights, ids, list, list_size, acts, sums, scales, stages, total;
+    int masks, weights, ids, list, list_size, acts, sums, scales, words, codes, total;
     __host__ __device__ Layout(int experts, int tokens, int top_k, int dim, int inner, int pass_rows, int stage_count) {
         const int choices = tokens * top_k, up = pass_rows * pitch(dim), down = 2 * pass_rows * pitch(inner);
         masks = align16(sizeof(Head));
@@ -83,8 +87,9 @@ struct Layout {
         acts = list + align16(4 * list_size);
         sums = acts + (up > down ? up : down);
         scales = sums + kWarps / 2 * kUnitRows * pass_rows * 4 * (pass_rows > 8 ? 1 : 2);
-        stages = scales + kWarps * kUnitRows * 16;
-        total = stages + kWarps * stage_count * kStageBytes;
+        words = scales + kWarps * kUnitRows * 16;
+        codes = (words + kWarps * stage_count * kWordBytes + 511) & ~511;
+        total = codes + kWarps * stage_count * kSliceBytes;
     }
     // Bytes from one row of the activations to the next: 64 more than a multiple of 128, so that the 16-byte
     // loads of two rows' four lanes each meet all banks once.
@@ -97,6 +102,10 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes)
 }
 __device__ __forceinline__ void copy4(uint32_t to, const void* from, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+// This thread's copies so far arrive at the barrier, as one of its expected arrivals, when they are done.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most kLeft of this thread's groups are under way.
@@ -373,30 +382,33 @@ struct Pairs {
 // What the two products multiply: `rows` rows of k elements for each expert, `tiles` units.
 struct Up {
     static constexpr bool kPairs = false;
-    static __device__ __forceinline__ const uint8_t* codes(const ExpertsArgs& a) { return a.up_q; }
     static __device__ __forceinline__ const uint8_t* scales(const ExpertsArgs& a) { return a.up_s; }
     static __device__ __forceinline__ int rows(const ExpertsArgs& a) { return 2 * a.inner; }
     static __device__ __forceinline__ int k(const ExpertsArgs& a) { return a.dim; }
-    static __device__ __forceinline__ int tiles(const ExpertsArgs& a) { return 8 * ((a.inner + 127) / 128); }
+    static __device__ __forceinline__ int tiles(const ExpertsArgs& a) { return (a.inner + 15) / 16; }
     // The weights' row for row lr of tile `tile`; -1: none.
     static __device__ __forceinline__ int row(const ExpertsArgs& a, int tile, int lr) {
-        const int r = hidden(tile, lr & 15);
+        const int r = 16 * tile + (lr & 15);
         return r < a.inner ? (lr < 16 ? r : a.inner + r) : -1;
     }
-    static __device__ __forceinline__ int hidden(int tile, int m) {
-        return 128 * (tile >> 3) + 32 * (m & 3) + 4 * (tile & 7) + (m >> 2);
+    // The codes of a slice of a unit: 16 rows of g and 16 of u; what lies behind either's end is of no use, and does no harm.
+    static __device__ __forceinline__ void load(const ExpertsArgs& a, uint32_t to, int x, int first, int tile, uint32_t bar) {
+        tma_load_2d(to, &a.up_map, x, first + 16 * tile, bar);
+        tma_load_2d(to + kSliceBytes / 2, &a.up_map, x, first + a.inner + 16 * tile, bar);
     }
 };
 struct Down {
     static constexpr bool kPairs = true;
-    static __device__ __forceinline__ const uint8_t* codes(const ExpertsArgs& a) { return a.down_q; }
     static __device__ __forceinline__ const uint8_t* scales(const ExpertsArgs& a) { return a.down_s; }
     static __device__ __forceinline__ int rows(const ExpertsArgs& a) { return a.dim; }
     static __device__ __forceinline__ int k(const ExpertsArgs& a) { return a.inner; }
-    static __device__ __forceinline__ int tiles(const ExpertsArgs& a) { return 4 * ((a.dim + 127) / 128); }
+    static __device__ __forceinline__ int tiles(const ExpertsArgs& a) { return (a.dim + 31) / 32; }
     static __device__ __forceinline__ int row(const ExpertsArgs& a, int tile, int lr) {
-        const int m = lr & 15, r = 128 * (tile >> 2) + 32 * (m & 3) + 8 * (tile & 3) + 4 * (lr >> 4) + (m >> 2);
+        const int r = 32 * tile + lr;
         return r < a.dim ? r : -1;
+    }
+    static __device__ __forceinline__ void load(const ExpertsArgs& a, uint32_t to, int x, int first, int tile, uint32_t bar) {
+        tma_load_2d(to, &a.down_map, x, first + 32 * tile, bar);
     }
 };
 
@@ -431,20 +443,24 @@ struct Rounds {
     }
 };
 
-// A warp's slices on their way to shared memory, in the order in which it takes them.
+// A warp's slices on their way to shared memory, in the order in which it takes them: the codes as boxes of a tensor copy, whose
+// 64-byte swizzle turns a row's four 16-byte pieces by (row / 2) % 4, the scales as a word for each lane's row; a barrier for each
+// stage counts both.  (All of it by 16-byte asynchronous copies from the lanes: 15 clocks of the load pipe for 512 bytes, 2.6 us
+// for the first four slices of 16 warps, ## us where this takes ##.)
 template <typename Product, int kStages>
 struct Stream {
     const ExpertsArgs& a;
     Pairs list;
-    uint32_t to, end_to, d;   // the warp's stages, and the next one to be filled
+    uint32_t codes, words, full;   // the warp's stages and their barriers
+    int stage;                     // the next one to be filled
     Rounds r;
     bool more;
-    const uint8_t* q[4];      // this lane's piece of four rows
-    const uint8_t* s;         // and its row's scales
-    int bytes[5];             // to copy of each: none where there is no row
+    int first, tile;               // of the unit: its expert's first row, and its place there
+    const uint8_t* s;              // this lane's row's scales,
+    int bytes;                     // to copy of them: none where there is no row
 
-    __device__ __forceinline__ Stream(const ExpertsArgs& args, const Pairs& l, uint32_t stages, uint32_t next, const Rounds& rounds)
-        : a(args), list(l), to(stages), end_to(stages + kStages * kStageBytes), d(next), r(rounds) {
+    __device__ __forceinline__ Stream(const ExpertsArgs& args, const Pairs& l, uint32_t c, uint32_t w, uint32_t f, int next, const Rounds& rounds)
+        : a(args), list(l), codes(c), words(w), full(f), stage(next), r(rounds) {
         advance();
     }
     // To the next round with slices for this warp.
@@ -452,50 +468,41 @@ struct Stream {
         do more = r.advance();
         while (more && r.slice >= r.last);
         if (!more) return;
-        const int tile = r.unit - r.pair * r.tiles, lane = static_cast<int>(lane_id());
-        const int64_t first = static_cast<int64_t>(list[r.pair] & 0xFFFFu) * Product::rows(a);
-        const int64_t pitch = static_cast<int64_t>(r.slices) * (kSlice / 2);
-        const uint8_t* const codes = Product::codes(a) + r.slice * (kSlice / 2) + (lane & 3) * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = Product::row(a, tile, 8 * i + (lane >> 2));
-            bytes[i] = row < 0 ? 0 : 16;
-            q[i] = row < 0 ? Product::codes(a) : codes + (first + row) * pitch;
-        }
-        const int row = Product::row(a, tile, lane);
-        const int64_t group = static_cast<int64_t>(list[r.pair] & 0xFFFFu) * ((Product::rows(a) + 127) / 128) + row / 128;
-        bytes[4] = row < 0 ? 0 : 4;
+        const int e = static_cast<int>(list[r.pair] & 0xFFFFu);
+        tile = r.unit - r.pair * r.tiles;
+        first = e * Product::rows(a);
+        const int row = Product::row(a, tile, static_cast<int>(lane_id()));
+        bytes = row < 0 ? 0 : 4;
         s = Product::scales(a);
-        if (row >= 0) s += (group * r.slices + r.slice) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
-    }
-    // Asks for the next slice, or for nothing: a group of copies either way.
-    __device__ __forceinline__ void ask() {
-        if (more) {
-            const int lane = static_cast<int>(lane_id());
-            // row 8 i + lane / 4 at 64 bytes of it, its 16-byte pieces turned by (row / 2) % 4
-            const uint32_t at = d + static_cast<uint32_t>((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                copy16(at + 512 * i, q[i], bytes[i]);
-                q[i] += kSlice / 2;
-            }
-            copy4(d + static_cast<uint32_t>(kSliceBytes + 4 * lane), s, bytes[4]);
-            s += 512;
-            d += kStageBytes;
-            if (d == end_to) d = to;
-            if (++r.slice == r.last) advance();
+        if (row >= 0) {
+            const int64_t group = static_cast<int64_t>(e) * ((Product::rows(a) + 127) / 128) + row / 128;
+            s += (group * r.slices + r.slice) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
         }
-        copies_commit();
+    }
+    // Asks for the next slice, if there is one.
+    __device__ __forceinline__ void ask() {
+        if (!more) return;
+        const uint32_t bar = full + 8 * stage;
+        copy4(words + stage * kWordBytes + 4 * lane_id(), s, bytes);
+        copies_arrive(bar);
+        s += 512;
+        if (lane_id() == 0) {
+            mbar_arrive_expect_tx(bar, kSliceBytes);
+            Product::load(a, codes + stage * kSliceBytes, r.slice * (kSlice / 2), first, tile, bar);
+        }
+        if (++stage == kStages) stage = 0;
+        if (++r.slice == r.last) advance();
     }
 };
 
 // The unit's sums so far += one slice.  All places in shared memory; acts: this lane's place in the activations (row g, 16 bytes t of the slice's first
 // block), `low` bytes further their low parts.
 template <int kCols, bool kPairs, int kMost>
-__device__ __forceinline__ void multiply(uint8_t* shared, int stage, int scales, int acts, int pitch, int low, float (*acc)[kMost][4]) {
+__device__ __forceinline__ void multiply(uint8_t* shared, int stage_codes, int stage_words, int scales, int acts, int pitch, int low,
+                                         float (*acc)[kMost][4]) {
     const int lane = static_cast<int>(lane_id()), g = lane >> 2;
     // each lane turns one row's four bytes into factors, for all (48 instructions less than each for itself)
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(shared + stage + kSliceBytes + 4 * lane);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(shared + stage_words + 4 * lane);
     *reinterpret_cast<uint4*>(shared + scales + 16 * lane) = make_uint4(scale_of(w, 0), scale_of(w, 1), scale_of(w, 2), scale_of(w, 3));
     __syncwarp();
     float by[2][2][4];
@@ -510,7 +517,7 @@ __device__ __forceinline__ void multiply(uint8_t* shared, int stage, int scales,
             by[m][h][3] = f.w;
         }
     // the block's words of rows g, g + 8, g + 16 and g + 24 of the unit: this lane's is the address of its row, lane, at the block
-    const uint32_t codes = smem_addr(shared + stage + 64 * lane);
+    const uint32_t codes = smem_addr(shared + stage_codes + 64 * lane);
     const uint32_t turn = static_cast<uint32_t>((lane >> 1) & 3) << 4;
 #pragma unroll
     for (int b = 0; b < kSlice / 32; ++b) {
@@ -632,7 +639,7 @@ __device__ __forceinline__ void finish(Up, const ExpertsArgs& a, const Head* hea
             if (row.slot >= 0)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int r = Up::hidden(tile, 8 * h + g);
+                    const int r = 16 * tile + 8 * h + g;
                     const float x = acc[0][n][2 * h + c] * row.back, u = acc[1][n][2 * h + c] * row.back;
                     const float v = x / (1.0f + expf(-x)) * u;
                     if (r < a.inner) {
@@ -702,15 +709,23 @@ __device__ __forceinline__ Rounds range_of(const ExpertsArgs& a, const Head* hea
     return Rounds(range_start(head, tiles, blockIdx.x), range_start(head, tiles, blockIdx.x + 1), tiles, (Product::k(a) + kSlice - 1) / kSlice);
 }
 
-// A product over the CTA's range.  `stage`: the stage that the stream's first slice goes to; becomes the one behind its last.
+// A warp's stages.
+struct Stages {
+    int codes, words;     // their places in shared memory
+    uint32_t full;        // their barriers
+    int next;             // the stage that is taken next, and the parity of its barrier's phase
+    uint32_t phase;
+};
+
+// A product over the CTA's range.
 template <typename Product, int kStages, int kMost>
 __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, uint8_t* shared, Stream<Product, kStages>& stream, const Pairs& pairs,
-                                        int* next_stage) {
+                                        Stages& st) {
     Head* const head = reinterpret_cast<Head*>(shared);
     const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
-    const int scales = at.scales + warp * kUnitRows * 16, own = at.stages + warp * kStages * kStageBytes;
+    const int scales = at.scales + warp * kUnitRows * 16;
     const int pitch = Layout::pitch(Product::k(a)), low = a.passes_rows * pitch;
-    int stage = *next_stage, pair = -1;
+    int pair = -1;
     Rounds round = range_of<Product>(a, head);
 #pragma unroll 1
     while (round.advance()) {
@@ -730,15 +745,17 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
         int x = at.acts + g * pitch + t * 16 + round.slice * (kSlice * 2);
 #pragma unroll 1
         for (int i = round.slice; i < round.last; ++i) {
-            copies_wait<kStages - 1>();
-            __syncwarp();
-            if (wide) multiply<kMost, Product::kPairs>(shared, stage, scales, x, pitch, low, acc);
-            else multiply<1, Product::kPairs>(shared, stage, scales, x, pitch, low, acc);
+            mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort);
+            const int codes = st.codes + st.next * kSliceBytes, words = st.words + st.next * kWordBytes;
+            if (wide) multiply<kMost, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
+            else multiply<1, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
             __syncwarp();
             stream.ask();
             x += kSlice * 2;
-            stage += kStageBytes;
-            if (stage == own + kStages * kStageBytes) stage = own;
+            if (++st.next == kStages) {
+                st.next = 0;
+                st.phase ^= 1u;
+            }
         }
         const int cols = wide ? kMost : 1;
         // A unit's first warp gets what the others have: at once, or in halves where 16 columns leave room for 8 warps' sums.
@@ -770,18 +787,25 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
         }
         if (round.part == 0) finish<kMost>(Product(), a, head, round.unit - round.pair * round.tiles, cols, acc);
     }
-    *next_stage = stage;
 }
 
 // kMost: 8 kMost rows in a pass at most.
 template <int kStages, int kMost>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a) {
-    extern __shared__ __align__(16) uint8_t shared[];
+    extern __shared__ __align__(1024) uint8_t shared[];   // the swizzle goes by addresses
     const Layout at(a.experts, a.tokens, a.top_k, a.dim, a.inner, a.passes_rows, kStages);
     Head* const head = reinterpret_cast<Head*>(shared);
     float* const weights = reinterpret_cast<float*>(shared + at.weights);
     uint32_t* const list = reinterpret_cast<uint32_t*>(shared + at.list);
-    const int warp = threadIdx.x >> 5, own = at.stages + warp * kStages * kStageBytes;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        head->abort = 0;
+        prefetch_tensormap(&a.up_map);
+        prefetch_tensormap(&a.down_map);
+    }
+    if (threadIdx.x < kWarps * kStages)   // 32 lanes' words, and the codes
+        mbar_init(smem_addr(&head->full[threadIdx.x / kStages][threadIdx.x % kStages]), 33);
+    fence_barrier_init();
 
 #pragma unroll 1
     for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
@@ -797,21 +821,26 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     list_pairs(a, head, reinterpret_cast<unsigned long long*>(shared + at.masks), weights, reinterpret_cast<uint16_t*>(shared + at.ids), list,
                at.list_size);
     const Pairs pairs{list, at.list_size, head->narrow};
-    int stage = own;
+    Stages st{at.codes + warp * kStages * kSliceBytes, at.words + warp * kStages * kWordBytes, smem_addr(head->full[warp]), 0, 0u};
+    const uint32_t codes = smem_addr(shared + st.codes), words = smem_addr(shared + st.words);
     {
-        Stream<Up, kStages> stream(a, pairs, smem_addr(shared + own), smem_addr(shared + stage), range_of<Up>(a, head));
+        Stream<Up, kStages> stream(a, pairs, codes, words, st.full, st.next, range_of<Up>(a, head));
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) stream.ask();
-        product<Up, kStages, kMost>(a, at, shared, stream, pairs, &stage);
+        product<Up, kStages, kMost>(a, at, shared, stream, pairs, st);
     }
     {
-        Stream<Down, kStages> stream(a, pairs, smem_addr(shared + own), smem_addr(shared + stage), range_of<Down>(a, head));
+        Stream<Down, kStages> stream(a, pairs, codes, words, st.full, st.next, range_of<Down>(a, head));
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) stream.ask();
         meet(a, 1);
-        product<Down, kStages, kMost>(a, at, shared, stream, pairs, &stage);
+        product<Down, kStages, kMost>(a, at, shared, stream, pairs, st);
     }
-    copies_wait<0>();
+    if (*static_cast<volatile int*>(&head->abort) != 0 && lane_id() == 0)   // copies that a wait gave up on may be on their way
+        for (int i = 0; i < kStages; ++i) {
+            mbar_wait_quiet(st.full + 8 * st.next, st.phase, kWaitLimitNs / 16);
+            if (++st.next == kStages) st.next = 0, st.phase ^= 1u;
+        }
     meet(a, 2);
     join(a, weights);
     if (threadIdx.x == 0 && atomicAdd(&a.sync->left, 1u) == gridDim.x - 1u) {   // nobody looks at them any more
@@ -835,6 +864,14 @@ int shape(ExpertsArgs* a) {
 }
 
 cudaError_t launch(ExpertsArgs a, int sms, cudaStream_t stream) {
+    const auto map = [&](CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t k, uint32_t box) {
+        const uint64_t bytes = static_cast<uint64_t>((k + kSlice - 1) / kSlice * (kSlice / 2));
+        return encode_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, bytes, static_cast<uint64_t>(rows), bytes, kSlice / 2, box,
+                             CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    if (!map(&a.up_map, a.up_q, int64_t{2} * a.experts * a.inner, a.dim, kUnitRows / 2) ||
+        !map(&a.down_map, a.down_q, int64_t{1} * a.experts * a.dim, a.inner, kUnitRows))
+        return cudaErrorInvalidValue;
     using K = void (*)(ExpertsArgs);
     static const K kernels[2][3] = {{experts_kernel<2, 1>, experts_kernel<3, 1>, experts_kernel<4, 1>},
                                     {experts_kernel<2, 2>, experts_kernel<3, 2>, experts_kernel<4, 2>}};

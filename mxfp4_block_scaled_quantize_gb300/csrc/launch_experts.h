@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "mxfp4.h"
@@ -16,6 +17,8 @@ struct ExpertsSync {
 };
 
 struct ExpertsArgs {
+    CUtensorMap up_map;        // the codes as [rows of all experts, bytes of a row], boxes of 64 bytes of 16 rows
+    CUtensorMap down_map;      // (W2: 32 rows), 64-byte swizzle, zero fill
     const uint16_t* x;         // bf16 [tokens, dim], row pitch ldx
     int64_t ldx;
     const void* logits;        // [tokens, experts], row pitch ldl
