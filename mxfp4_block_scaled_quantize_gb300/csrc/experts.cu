@@ -22,13 +22,12 @@
 //
 // Work of phases 2 and 3.  A unit is 32 rows of an expert's weights (16 of g and the same 16 of u) against a pass of its routed
 // rows.  A CTA takes a range of consecutive units, so it stages an expert's activations in shared memory once.  Its 16 warps
-// take 16 units of one expert at a time, a whole unit each, and meet nobody; of the n < 16 that are left they take 8, 4, 2 and
-// 1, as n has them, with 2, 4, 8 and 16 warps to a unit, each with its part of the row's length: so all warps do the same
-// whatever n is.  (All units dealt out in slices of 128 elements to 16 warps, which met after each one, took 1.9 times the
-// instructions.)  Each warp has several slices (2 KB of codes) on their way to shared memory by asynchronous copies of
+// take 16 units of one expert at a time, a whole unit each, and meet nobody; the n < 16 that are left they share, each with
+// 1 / 16 of all their slices of 128 elements, which are of two units at most: a unit's first warp adds what the others found.
+// (All units dealt out slice by slice to 16 warps, which met after each one, took 1.9 times the instructions; the rest in
+// rounds of 8, 4, 2 and 1 units 9 us more in some CTAs than in others, of 50.)  Each warp has several slices (2 KB of codes) on
+// their way to shared memory by copies of
 // its own, across the ends of its units and, to the second product's weights, across the barrier.
-//   Rows of a unit: 32 q + i for q = 0 .. 3 and a few consecutive i of a group of 128, so that their scales (16 bytes for the
-//   four q of one i in the scale layout) are consecutive too.
 //   The order of all additions is fixed by the call's routing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -86,7 +85,7 @@ struct Layout {
         list_size = (experts < choices ? experts : choices) + choices / pass_rows;
         acts = list + align16(4 * list_size);
         sums = acts + (up > down ? up : down);
-        scales = sums + kWarps / 2 * kUnitRows * pass_rows * 4 * (pass_rows > 8 ? 1 : 2);
+        scales = sums + kWarps * kUnitRows * pass_rows * 4;
         words = scales + kWarps * kUnitRows * 16;
         codes = (words + kWarps * stage_count * kWordBytes + 511) & ~511;
         total = codes + kWarps * stage_count * kSliceBytes;
@@ -412,33 +411,52 @@ struct Down {
     }
 };
 
-// A warp's way through the CTA's units, round by round: 16 units of one expert and pass with a warp each, or the 8, 4, 2 or 1
-// that are left with more warps to each.
-struct Rounds {
+// A warp's way through the CTA's units, one segment (slices of one unit) after the other.  Rounds of 16 units of one expert and
+// pass have one for each warp, a whole unit.  A round of the n < 16 that are left has two: the warp's share of the n units'
+// slices, first what it has of a unit that another warp begins, then what it begins itself; either may be empty.
+struct Segments {
+    enum Kind { kWhole, kGoOn, kBegin };
     int end, tiles, slices, warp;
-    int base;              // first unit of the round
-    int next;              // and of the one after it
-    int pair;              // the round's place in the list of (expert, pass)
-    int parts;             // warps of a unit
-    int unit, part;        // this warp's
-    int slice, last;       // its slices: from, to
+    int base, next;        // the round's first unit, and the next round's
+    int pair;              // its place in the list of (expert, pass)
+    int left;              // its units
+    int kind;
+    int unit;              // the segment's,
+    int slice, last;       // and its slices: from, to
 
-    // Before the first round.
-    __device__ __forceinline__ Rounds(int from, int to, int tiles_, int slices_)
-        : end(to), tiles(tiles_), slices(slices_), warp(threadIdx.x >> 5), base(from), next(from), pair(-1), parts(1), unit(0), part(0),
+    // Before the first segment.
+    __device__ __forceinline__ Segments(int from, int to, int tiles_, int slices_)
+        : end(to), tiles(tiles_), slices(slices_), warp(threadIdx.x >> 5), base(from), next(from), pair(-1), left(0), kind(kWhole), unit(0),
           slice(0), last(0) {}
+    // Where the share of warp w starts among the slices of the round's units.
+    __device__ __forceinline__ int share(int w) const { return left * slices * w / kWarps; }
     __device__ __forceinline__ bool advance() {
+        if (kind == kGoOn) {   // the same round
+            kind = kBegin;
+            const int from = share(warp), to = share(warp + 1), u = (from + slices - 1) / slices;
+            unit = base + u;
+            slice = 0;
+            last = max(to - u * slices, 0);
+            return true;
+        }
         if (next >= end) return false;
         base = next;
         pair = base / tiles;
-        const int left = min(end, (pair + 1) * tiles) - base;
-        const int shift = left >= kWarps ? 0 : __clz(left) - (31 - 4);   // kWarps = 2^4
-        parts = 1 << shift;
-        unit = base + (warp >> shift);
-        part = warp & (parts - 1);
-        slice = (slices * part) >> shift;
-        last = (slices * (part + 1)) >> shift;
-        next = base + (kWarps >> shift);
+        left = min(end, (pair + 1) * tiles) - base;
+        if (left >= kWarps) {
+            kind = kWhole;
+            left = kWarps;
+            unit = base + warp;
+            slice = 0;
+            last = slices;
+        } else {
+            kind = kGoOn;
+            const int from = share(warp), to = share(warp + 1), u = from / slices;
+            unit = base + u;
+            slice = from - u * slices;
+            last = slice == 0 ? 0 : min(slices, slice + to - from);
+        }
+        next = base + left;
         return true;
     }
 };
@@ -453,17 +471,17 @@ struct Stream {
     Pairs list;
     uint32_t codes, words, full;   // the warp's stages and their barriers
     int stage;                     // the next one to be filled
-    Rounds r;
+    Segments r;
     bool more;
     int first, tile;               // of the unit: its expert's first row, and its place there
     const uint8_t* s;              // this lane's row's scales,
     int bytes;                     // to copy of them: none where there is no row
 
-    __device__ __forceinline__ Stream(const ExpertsArgs& args, const Pairs& l, uint32_t c, uint32_t w, uint32_t f, int next, const Rounds& rounds)
-        : a(args), list(l), codes(c), words(w), full(f), stage(next), r(rounds) {
+    __device__ __forceinline__ Stream(const ExpertsArgs& args, const Pairs& l, uint32_t c, uint32_t w, uint32_t f, int next, const Segments& segments)
+        : a(args), list(l), codes(c), words(w), full(f), stage(next), r(segments) {
         advance();
     }
-    // To the next round with slices for this warp.
+    // To the next segment with slices.
     __device__ __forceinline__ void advance() {
         do more = r.advance();
         while (more && r.slice >= r.last);
@@ -704,9 +722,9 @@ __device__ __forceinline__ int range_start(const Head* head, int tiles, uint32_t
 }
 
 template <typename Product>
-__device__ __forceinline__ Rounds range_of(const ExpertsArgs& a, const Head* head) {
+__device__ __forceinline__ Segments range_of(const ExpertsArgs& a, const Head* head) {
     const int tiles = Product::tiles(a);
-    return Rounds(range_start(head, tiles, blockIdx.x), range_start(head, tiles, blockIdx.x + 1), tiles, (Product::k(a) + kSlice - 1) / kSlice);
+    return Segments(range_start(head, tiles, blockIdx.x), range_start(head, tiles, blockIdx.x + 1), tiles, (Product::k(a) + kSlice - 1) / kSlice);
 }
 
 // A warp's stages.
@@ -725,12 +743,14 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
     const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
     const int scales = at.scales + warp * kUnitRows * 16;
     const int pitch = Layout::pitch(Product::k(a)), low = a.passes_rows * pitch;
+    float* const sums = reinterpret_cast<float*>(shared + at.sums) + lane;   // 32 lanes' values side by side, warp by warp
+    constexpr int kValues = 8 * kMost;
     int pair = -1;
-    Rounds round = range_of<Product>(a, head);
+    Segments seg = range_of<Product>(a, head);
 #pragma unroll 1
-    while (round.advance()) {
-        if (round.pair != pair) {
-            pair = round.pair;
+    while (seg.advance()) {
+        if (seg.pair != pair) {
+            pair = seg.pair;
             stage_rows<Product>(a, head, shared + at.acts, reinterpret_cast<const unsigned long long*>(shared + at.masks),
                                 reinterpret_cast<const float*>(shared + at.weights), reinterpret_cast<const uint16_t*>(shared + at.ids), pairs[pair]);
         }
@@ -742,9 +762,9 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
             for (int n = 0; n < kMost; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-        int x = at.acts + g * pitch + t * 16 + round.slice * (kSlice * 2);
+        int x = at.acts + g * pitch + t * 16 + seg.slice * (kSlice * 2);
 #pragma unroll 1
-        for (int i = round.slice; i < round.last; ++i) {
+        for (int i = seg.slice; i < seg.last; ++i) {
             mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort);
             const int codes = st.codes + st.next * kSliceBytes, words = st.words + st.next * kWordBytes;
             if (wide) multiply<kMost, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
@@ -758,34 +778,34 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
             }
         }
         const int cols = wide ? kMost : 1;
-        // A unit's first warp gets what the others have: at once, or in halves where 16 columns leave room for 8 warps' sums.
-        float* const sums = reinterpret_cast<float*>(shared + at.sums) + lane;
-#pragma unroll 1
-        for (int span = round.parts; span > 1;) {
-            const int keep = wide ? span / 2 : 1, first = (warp / round.parts) * (span - keep);
-            __syncthreads();   // what was here before has been added up
-            if (round.part >= keep && round.part < span)
+        if (seg.kind == Segments::kGoOn) {   // the sums of a unit that another warp began, for that warp
+            if (seg.slice < seg.last)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int n = 0; n < kMost; ++n)
                         if (n < cols)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) sums[(((first + round.part - keep) * cols + n) * 8 + m * 4 + i) * 32] = acc[m][n][i];
-            __syncthreads();
-            if (round.part < keep)
-#pragma unroll 1
-                for (int p = round.part + keep; p < span; p += keep)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int n = 0; n < kMost; ++n)
-                            if (n < cols)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) acc[m][n][i] += sums[(((first + p - keep) * cols + n) * 8 + m * 4 + i) * 32];
-            span = keep;
+                            for (int i = 0; i < 4; ++i) sums[(warp * kValues + (n * 2 + m) * 4 + i) * 32] = acc[m][n][i];
+            continue;
         }
-        if (round.part == 0) finish<kMost>(Product(), a, head, round.unit - round.pair * round.tiles, cols, acc);
+        if (seg.kind == Segments::kBegin) {
+            __syncthreads();   // the next write to the sums is behind a barrier of stage_rows or of the grid
+            const int behind = (seg.unit - seg.base + 1) * seg.slices;
+            if (seg.last == 0) continue;
+#pragma unroll 1
+            for (int w = warp + 1; w < kWarps && seg.share(w) < behind; ++w) {
+                if (seg.share(w) == seg.share(w + 1)) continue;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < kMost; ++n)
+                        if (n < cols)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[m][n][i] += sums[(w * kValues + (n * 2 + m) * 4 + i) * 32];
+            }
+        }
+        finish<kMost>(Product(), a, head, seg.unit - seg.pair * seg.tiles, cols, acc);
     }
 }
 
