@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "launch.h"
 #include "launch_experts.h"
 #include "ptx.cuh"
@@ -898,8 +900,17 @@ cudaError_t launch(ExpertsArgs a, int sms, cudaStream_t stream) {
     const int smem = shape(&a);
     if (smem == 0) return cudaErrorInvalidValue;
     const K kernel = kernels[a.passes_rows > 8][a.stages - 2];
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+    static std::atomic<uint64_t> known[2][3];   // the devices that have the attribute: the call costs the host as much as a launch
+    std::atomic<uint64_t>& devices = known[a.passes_rows > 8][a.stages - 2];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(devices.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+        if (e != cudaSuccess) return e;
+        devices.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;

@@ -9,6 +9,8 @@
 // inputs give the same bits.  A sample that is one CTA's needs no second kernel.  Rows come as in the
 // forward pass, x and dy side by side in a slot of the ring.  Bound by the memory: x and dy in, dx
 // out; the partial rows are 4 / chunk_rows of x and dy in bf16.
+#include <atomic>
+
 #include "norm_row.cuh"
 
 namespace mxfp4 {
@@ -211,9 +213,17 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
     constexpr int kBudget = 208 * 1024 / kCtas;
     const int slot_bytes = 2 * static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStages ? kBudget / slot_bytes : kNormStages;
-    if (kMode == kRingRow) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
+    if (kMode == kRingRow) {   // once a device: the call costs the host as much as a launch
+        static std::atomic<uint64_t> known{0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        const uint64_t bit = uint64_t{1} << (dev & 63);
+        if (!(known.load(std::memory_order_relaxed) & bit)) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
+            if (e != cudaSuccess) return e;
+            known.fetch_or(bit, std::memory_order_relaxed);
+        }
     }
     return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), threads, a.stages * slot_bytes, stream);
 }

@@ -28,8 +28,7 @@ class MXFP4Experts:
             raise ValueError(f"top_k from 1 to {min(experts, abi.MXFP4_EXPERTS_MAX_TOP_K)}, not {top_k}")
         self.experts, self.dim, self.inner, self.top_k = experts, dim, inner, top_k
         self.max_tokens, self.normalize = max_tokens, normalize
-        # every number of tokens has to fit, not the largest alone
-        size = max(abi.mxfp4_experts_workspace_bytes(t, experts, top_k, dim, inner) for t in range(1, max_tokens + 1))
+        size = abi.mxfp4_experts_workspace_bytes(max_tokens, experts, top_k, dim, inner)   # fewer tokens need less of everything
         self._workspace = torch.zeros(size, dtype=torch.uint8, device=device)
         self.y = torch.empty((max_tokens, dim), dtype=torch.bfloat16, device=device)
         self._gpu = self.y.get_device() if self.y.is_cuda else None   # no tensor's get_device() is None

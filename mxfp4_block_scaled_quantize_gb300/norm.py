@@ -40,6 +40,7 @@ class LayerNorm:
             self.mean, self.rstd = buf(max_rows), buf(max_rows)
             self.dw, self.db = buf(max_samples, dim), buf(max_samples, dim)
             self._workspace = buf(abi.mxfp4_layer_norm_workspace_bytes(dim), dtype=torch.uint8)
+            self._vectors = {}   # views of dw and db by the shape of the vectors, each made once
         self._last = None   # rows, and shapes and type of the last forward's vectors; None: no backward can follow
 
     def _check_rows(self, x, what):
@@ -106,7 +107,8 @@ class LayerNorm:
         abi.mxfp4_layer_norm_backward(dy, pitch, x, rows, self.dim, ldx, weight, samples, flags, self.mean, self.rstd, self.dx,
                                       self.dim, dw, db, self._workspace, self._workspace.numel(), stream)
 
-        def like(v):
-            return None if v is None else v[:samples].view(kind[1])
-
-        return self.dx if rows == self.max_rows else self.dx[:rows], like(dw), like(db)
+        if kind is not None and kind[1] not in self._vectors:
+            self._vectors[kind[1]] = self.dw[:samples].view(kind[1]), self.db[:samples].view(kind[1])
+        views = (None, None) if kind is None else self._vectors[kind[1]]
+        return (self.dx if rows == self.max_rows else self.dx[:rows], views[0] if has_weight else None,
+                views[1] if has_bias else None)
