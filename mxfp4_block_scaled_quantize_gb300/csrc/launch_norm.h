@@ -9,7 +9,10 @@
 namespace mxfp4 {
 
 constexpr int kNormWarpRowDim = 512;     // rows of up to this many elements are one warp's, longer ones a CTA's
-constexpr int kNormStages = 8;           // rows that a CTA may have on their way to shared memory
+// Rows that a CTA has on their way to shared memory, at most.
+constexpr int kNormStagesForward = 3;
+constexpr int kNormStagesBackward = 4;
+constexpr int kNormStages = 4;
 
 // CTAs that share the rows of a backward pass, each of which leaves a partial row of dw and db: as many as
 // 152 SMs hold at a time, 512 threads each.

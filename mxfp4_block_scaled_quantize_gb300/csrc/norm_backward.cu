@@ -212,7 +212,7 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
     // The ring: as many rows as fit beside the CTAs that share the SM.
     constexpr int kBudget = 208 * 1024 / kCtas;
     const int slot_bytes = 2 * static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
-    a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStages ? kBudget / slot_bytes : kNormStages;
+    a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStagesBackward ? kBudget / slot_bytes : kNormStagesBackward;
     if (kMode == kRingRow) {   // once a device: the call costs the host as much as a launch
         static std::atomic<uint64_t> known{0};
         int dev = 0;

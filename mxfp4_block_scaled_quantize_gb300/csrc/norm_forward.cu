@@ -10,7 +10,7 @@
 // fp32; y is rounded once.  Bound by the memory, and by instructions not far below it.
 //
 // A warp takes a row of up to 512 elements, a CTA a longer one.  CTAs stay for many rows, with the
-// vectors in registers.  A CTA's rows come through a ring in shared memory, which has up to 8 of them on
+// vectors in registers.  A CTA's rows come through a ring in shared memory, which has three of them on
 // their way whatever the registers hold; a warp's are loaded into registers one row ahead.
 #include <atomic>
 
@@ -19,8 +19,8 @@
 namespace mxfp4 {
 namespace {
 
-template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_constant__ NormArgs a) {
+template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) uint8_t slots[];
     __shared__ float4 parts[2][32];   // of a row's warps: m, r, squares
     __shared__ RowRing ring;
@@ -161,17 +161,19 @@ bool wide(const NormArgs& a) {
     return (all & 15u) == 0 && a.dim % 8 == 0 && (a.rows == 1 || (a.ldx % 8 == 0 && a.ldy % 8 == 0));
 }
 
-template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads>
+// kCtas: CTAs that an SM holds at least, by registers.
+template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
 cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
-    const auto kernel = norm_forward_kernel<kF32, kWide, kGroups, kMode, kThreads>;
+    const auto kernel = norm_forward_kernel<kF32, kWide, kGroups, kMode, kThreads, kCtas>;
     const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
     const int64_t need = kMode == kWarpRow ? (a.rows + kThreads / 32 - 1) / (kThreads / 32) : a.rows;
-    // The ring: as many rows as fit beside the CTAs that share the SM.
-    constexpr int kBudget = kThreads <= 128 ? 44 * 1024 : kThreads <= 256 ? 96 * 1024 : 192 * 1024;
+    // The ring: three rows, if they fit beside the CTAs that share the SM.  More CTAs hide more than deeper rings do: 4608 rows of
+    // 5120 take 19.9 us with 3 rows, 20.5 with 4, 21.9 with 6, and 26 with 8 in rings that left room for two CTAs.
+    constexpr int kBudget = kThreads <= 128 ? 32 * 1024 : kThreads <= 256 ? 64 * 1024 : 192 * 1024;
     const int row_bytes = static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
-    a.stages = kMode != kRingRow ? 0 : kBudget / row_bytes < kNormStages ? kBudget / row_bytes : kNormStages;
+    a.stages = kMode != kRingRow ? 0 : kBudget / row_bytes < kNormStagesForward ? kBudget / row_bytes : kNormStagesForward;
     const int smem = a.stages * row_bytes;
-    // resident CTAs an SM, by device and warps of the CTA (with the largest ring)
+    // CTAs that an SM holds, by device and warps of the CTA: by registers and threads, and then by the rings
     static std::atomic<int> per_sm[64][kThreads / 32 + 1];
     int dev = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -179,14 +181,14 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
     std::atomic<int>& known = per_sm[dev & 63][threads / 32];
     n = known.load(std::memory_order_relaxed);
     if (n == 0) {
-        const int most = kMode == kRingRow ? kBudget : 0;
-        if (most > 0) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, most);
+        if (kMode == kRingRow) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
         if (e != cudaSuccess) return e;
         if (n < 1) n = 1;
         known.store(n, std::memory_order_relaxed);
     }
-    const int64_t most = static_cast<int64_t>(n) * sms;
+    const int by_rings = kMode == kRingRow ? 227 * 1024 / (smem + 3 * 1024) : n;   // with what a CTA has besides
+    const int64_t most = static_cast<int64_t>(n < by_rings ? n : by_rings) * sms;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -201,22 +203,23 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
 }
 
 // Elements a thread: 32 where rows come in 16-byte accesses, for the join of a row's warps costs each warp as much as
-// some 16 elements (8 a thread: 2.9 TB/s at 1024 elements, 16: 3.6 TB/s at 2048 and 4.4 at 4096, 32: 5.2 at 4096 and
-// 6.2 at 8192); 16 where they do not, which the registers of the single accesses' addresses fill.
+// some 16 elements (8192 rows of 4096: 33 us with 16, 26 with 32; 16384 of 8192: 149 and 88); 16 where they do not, which the
+// registers of the single accesses' addresses fill.  A warp's row wins up to 1024 elements: 32768 rows of 1024 take 26 us, 46 as
+// a CTA's.  Now 5.3 TB/s at 4096, 6.1 at 8192, 4.7 for 4608 rows of 5120.
 template <bool kF32, bool kWide>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
-    if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256>(a, sms, stream);
-    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256>(a, sms, stream);
+    if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256, 1>(a, sms, stream);
+    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256, 1>(a, sms, stream);
     if (kWide) {
-        if (a.dim <= 1024) return launch<kF32, true, 4, kWarpRow, 128>(a, sms, stream);
-        if (a.dim <= 4096) return launch<kF32, true, 4, kRingRow, 128>(a, sms, stream);
-        if (a.dim <= 8192) return launch<kF32, true, 4, kRingRow, 256>(a, sms, stream);
-        return launch<kF32, true, 4, kRingRow, 512>(a, sms, stream);
+        if (a.dim <= 1024) return launch<kF32, true, 4, kWarpRow, 128, 4>(a, sms, stream);
+        if (a.dim <= 4096) return launch<kF32, true, 4, kRingRow, 128, 4>(a, sms, stream);
+        if (a.dim <= 8192) return launch<kF32, true, 4, kRingRow, 256, 2>(a, sms, stream);
+        return launch<kF32, true, 4, kRingRow, 512, 1>(a, sms, stream);
     }
-    if (a.dim <= 2048) return launch<kF32, false, 2, kRingRow, 128>(a, sms, stream);
-    if (a.dim <= 4096) return launch<kF32, false, 2, kRingRow, 256>(a, sms, stream);
-    if (a.dim <= 8192) return launch<kF32, false, 2, kRingRow, 512>(a, sms, stream);
-    return launch<kF32, false, 2, kRingRow, 1024>(a, sms, stream);
+    if (a.dim <= 2048) return launch<kF32, false, 2, kRingRow, 128, 1>(a, sms, stream);
+    if (a.dim <= 4096) return launch<kF32, false, 2, kRingRow, 256, 1>(a, sms, stream);
+    if (a.dim <= 8192) return launch<kF32, false, 2, kRingRow, 512, 1>(a, sms, stream);
+    return launch<kF32, false, 2, kRingRow, 1024, 1>(a, sms, stream);
 }
 
 }  // namespace
