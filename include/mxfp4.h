@@ -510,7 +510,7 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const voi
  *              `inner` rows of g, then its `inner` rows of u; 16-byte aligned
  *   down_q, down_s  W2's, [experts * dim, inner] in equal groups
  *   sizes      experts 1 .. MXFP4_MAX_GROUPS, top_k 1 .. min(experts, MXFP4_EXPERTS_MAX_TOP_K); dim and inner as far as the
- *              activations of 8 routed rows fit the shared memory: up to 7168 and 3584 whatever the rest
+ *              activations of 8 routed rows fit the shared memory: up to 7040 and 3456 whatever the rest
  *              (mxfp4_experts_workspace_bytes tells: it refuses what the call refuses)
  *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned; its first 256 bytes are zero before the first use
  *              (a call leaves them zero); calls that share one are ordered one after the other, as are replays of

@@ -269,6 +269,21 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+_current_device = None
+
+
+def is_current(gpu) -> bool:
+    """Is GPU number gpu the current device, on whose stream a call without a stream is enqueued and whose kernels it
+    launches?  True in a process that has no CUDA context, where no tensor can be on a GPU."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        if not torch.cuda.is_initialized():
+            return True
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # the first takes 0.5 us less
+    return _current_device() == gpu
+
+
 def _check(status: int, what: str) -> None:
     if status != MXFP4_OK:
         raise Mxfp4Error(status, what)

@@ -18,7 +18,7 @@
 //   1. CTA t: token t's choices, and its row of x in fp16.
 //   2. The first product, with silu(g) u.   3. The second product.   4. The sums over the experts, in the tokens' order.
 // (As two kernels that each routed and staged for themselves, and with the sums left to whichever CTA came last for 32
-// columns: 137 us where this takes ##, of which 60 passed before the first and after the last weights.)
+// columns: 137 us where one kernel then took 115, of which 60 passed before the first and after the last weights.)
 //
 // Work of phases 2 and 3.  A unit is 32 rows of an expert's weights (16 of g and the same 16 of u) against a pass of its routed
 // rows.  A CTA takes a range of consecutive units, so it stages an expert's activations in shared memory once.  Its 16 warps
@@ -29,6 +29,13 @@
 // their way to shared memory by copies of
 // its own, across the ends of its units and, to the second product's weights, across the barrier.
 //   The order of all additions is fixed by the call's routing.
+//   (The two fp16 of an activation between the products cost a second set of matrix instructions: 17 us of the 209 for 64 tokens
+// below.  Up to 4 rows have them side by side as 8 columns, which costs none: 8 tokens 59 us, 65 without that.)
+//
+// Measured (experts dim x inner; 1, 8 and 32 tokens of 8 of 64, 2048 x 1408; 64 of 6 of 64, 4096 x 2048): 28, 59, 85 and 205 us,
+// where the weights' bytes take 5.4, 28.5, 42.8 and 126.  One token: 3.3 us to the first barrier, 3 to the first weights asked
+// for, 7 for the first product, 5 for the second, 5 for the other two barriers and the sums; much of it is code that runs once
+// and comes from memory.  64 tokens: the first product at 20 bytes a clock and SM (of 23), the second at 16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -50,8 +57,10 @@ constexpr int kWordBytes = 4 * kUnitRows;                // and a word of four s
 constexpr int kMaxStages = 4;
 constexpr int kMaxPass = 16;                             // routed rows of a pass
 constexpr int kSharedMost = 227 * 1024;
-// A unit of a pass of more than 8 rows takes 1.6 times as long as one of up to 8.
-constexpr uint32_t kNarrowCost = 5, kWideCost = 8;
+// A unit of a pass of more than 8 rows takes 1.6 times as long as one of up to 8, and coming to another expert or pass as long as
+// kStagingSlices slices of a unit (32 tokens, 8 of 64: 88 us without counting that, 84.6 with 32 slices, 83.3 with 64, 82.2 with 96;
+// 8 tokens: 64.9, 60.8, 61.4, 63.1).
+constexpr uint32_t kNarrowCost = 5, kWideCost = 8, kStagingSlices = 64;
 
 struct Row {           // of a pass
     int32_t slot;      // token * top_k + place among the token's choices; -1: no row
@@ -60,28 +69,31 @@ struct Row {           // of a pass
     uint32_t from;     // its activations' row
 };
 
-// Shared memory: this head, then [experts] masks, [tokens * top_k] weights and experts, the list of (expert, pass),
+// Shared memory: this head, then [experts] masks, [tokens * top_k] weights, what undoes the activations' powers of two (of a
+// token, then of a choice) and experts, the list of (expert, pass),
 // the activations, the units' sums, the warps' scales, their words and (at a multiple of 512 bytes) their codes.
 struct Head {
     Row rows[kMaxPass];
     int32_t narrow;    // (expert, pass) pairs of up to 8 rows,
     int32_t pairs;     // and all of them
-    int32_t wide;      // the pass has more than 8 rows
+    int32_t wide;      // the pass has more than 8 rows,
+    int32_t slim;      // up to 4: the second product then has its activations' low parts beside the high ones, as columns 4 to 7
     uint32_t top;      // largest magnitude of a row of x, as bits
     int32_t abort;     // a wait has run out
-    int32_t pad[3];
+    int32_t pad[2];
     uint64_t full[kWarps][kMaxStages];
 };
 
 __host__ __device__ inline int align16(int n) { return (n + 15) & ~15; }
 
 struct Layout {
-    int masks, weights, ids, list, list_size, acts, sums, scales, words, codes, total;
+    int masks, weights, backs, ids, list, list_size, acts, sums, scales, words, codes, total;
     __host__ __device__ Layout(int experts, int tokens, int top_k, int dim, int inner, int pass_rows, int stage_count) {
         const int choices = tokens * top_k, up = pass_rows * pitch(dim), down = 2 * pass_rows * pitch(inner);
         masks = align16(sizeof(Head));
         weights = masks + align16(8 * experts);
-        ids = weights + align16(4 * choices);
+        backs = weights + align16(4 * choices);
+        ids = backs + align16(4 * choices);
         list = ids + align16(2 * choices);
         // an expert's passes: one, and one more for every further pass_rows of its tokens
         list_size = (experts < choices ? experts : choices) + choices / pass_rows;
@@ -327,7 +339,7 @@ __device__ __forceinline__ void meet(const ExpertsArgs& a, int which) {
 // Each expert's tokens, and the list of (expert, pass) pairs that have any: those of up to 8 rows from its front on, the
 // others from its back on.
 __device__ __forceinline__ void list_pairs(const ExpertsArgs& a, Head* head, unsigned long long* masks, float* weights, uint16_t* ids, uint32_t* list,
-                                           int list_size) {
+                                           int list_size, float* backs) {
 #pragma unroll 1
     for (int e = threadIdx.x; e < a.experts; e += kThreads) masks[e] = 0ull;
     __syncthreads();
@@ -339,6 +351,7 @@ __device__ __forceinline__ void list_pairs(const ExpertsArgs& a, Head* head, uns
         ids[i] = static_cast<uint16_t>(e);
         if (w != 0.0f) atomicOr(&masks[e], 1ull << (i / a.top_k));   // not where it changes nothing
     }
+    if (threadIdx.x < a.tokens) backs[threadIdx.x] = __ldcg(a.backs + threadIdx.x);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = static_cast<int>(lane_id());
@@ -466,7 +479,7 @@ struct Segments {
 // A warp's slices on their way to shared memory, in the order in which it takes them: the codes as boxes of a tensor copy, whose
 // 64-byte swizzle turns a row's four 16-byte pieces by (row / 2) % 4, the scales as a word for each lane's row; a barrier for each
 // stage counts both.  (All of it by 16-byte asynchronous copies from the lanes: 15 clocks of the load pipe for 512 bytes, 2.6 us
-// for the first four slices of 16 warps, ## us where this takes ##.)
+// for the first four slices of 16 warps, and 101 us for 32 tokens where this took 93.)
 template <typename Product, int kStages>
 struct Stream {
     const ExpertsArgs& a;
@@ -576,7 +589,7 @@ __device__ __forceinline__ void multiply(uint8_t* shared, int stage_codes, int s
 // The rows of a pass, and their activations: x's lowered rows as they are, the rows of h as two fp16.
 template <typename Product>
 __device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, const unsigned long long* masks,
-                                           const float* weights, const uint16_t* ids, uint32_t pair) {
+                                           const float* weights, const float* backs, const uint16_t* ids, uint32_t pair) {
     const int e = static_cast<int>(pair & 0xFFFFu), skip = static_cast<int>(pair >> 16) * a.passes_rows;
     const int pitch = Layout::pitch(Product::k(a)), groups = (pitch - 64) / 16;
     const unsigned long long mask = masks[e];
@@ -594,11 +607,13 @@ __device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uin
                 if (ids[token * a.top_k + j] == e) row.slot = token * a.top_k + j;
             row.weight = weights[row.slot];
             row.from = static_cast<uint32_t>(Product::kPairs ? row.slot : token);
-            if (Product::kPairs) lift(__uint_as_float(__ldcg(a.tops + row.slot)), &row.back);
-            else row.back = __ldcg(a.backs + token);
+            row.back = backs[row.from];
         }
         head->rows[threadIdx.x] = row;
-        if (threadIdx.x == 0) head->wide = rows > 8;
+        if (threadIdx.x == 0) {
+            head->wide = rows > 8;
+            head->slim = rows <= 4;
+        }
     }
     __syncthreads();
     if (!Product::kPairs) {
@@ -638,7 +653,7 @@ __device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uin
             }
             uint4* const to = reinterpret_cast<uint4*>(acts + n * pitch + 2 * c);
             *to = make_uint4(w[0], w[1], w[2], w[3]);
-            to[a.passes_rows * pitch / 16] = make_uint4(l[0], l[1], l[2], l[3]);
+            to[(rows <= 4 ? 4 : a.passes_rows) * pitch / 16] = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
     __syncthreads();
@@ -716,17 +731,27 @@ __device__ __forceinline__ void join(const ExpertsArgs& a, const float* weights)
 }
 
 // The unit at which CTA `cta` starts, so that all have the same to do.
-__device__ __forceinline__ int range_start(const Head* head, int tiles, uint32_t cta) {
-    const uint32_t narrow = static_cast<uint32_t>(head->narrow * tiles), all = static_cast<uint32_t>(head->pairs * tiles);
-    // below 2^32: at most 1200 pairs of 300 units, cost 8, on 256 SMs
-    const uint32_t at = (narrow * kNarrowCost + (all - narrow) * kWideCost) * cta / gridDim.x;
-    return static_cast<int>(at < narrow * kNarrowCost ? at / kNarrowCost : narrow + (at - narrow * kNarrowCost) / kWideCost);
+__device__ __forceinline__ int range_start(const Head* head, uint32_t tiles, uint32_t slices, uint32_t cta) {
+    const uint32_t narrow = static_cast<uint32_t>(head->narrow), wide = static_cast<uint32_t>(head->pairs) - narrow;
+    // of a unit, of a pair; all of it is below 2^30: at most 1200 pairs of 300 units of 74 slices
+    const uint32_t unit_n = kNarrowCost * slices, unit_w = kWideCost * slices, staging = kNarrowCost * kStagingSlices;
+    const uint32_t pair_n = tiles * unit_n + staging, pair_w = tiles * unit_w + staging;
+    const uint32_t all = narrow * pair_n + wide * pair_w, share = all / gridDim.x;
+    uint32_t at = share * cta + (all - share * gridDim.x) * cta / gridDim.x, first = 0, pair = pair_n, unit = unit_n;
+    if (at >= narrow * pair_n) {
+        at -= narrow * pair_n;
+        first = narrow;
+        pair = pair_w;
+        unit = unit_w;
+    }
+    const uint32_t p = at / pair, in = at - p * pair;
+    return static_cast<int>((first + p) * tiles + (in <= staging ? 0 : (in - staging) / unit));
 }
 
 template <typename Product>
 __device__ __forceinline__ Segments range_of(const ExpertsArgs& a, const Head* head) {
-    const int tiles = Product::tiles(a);
-    return Segments(range_start(head, tiles, blockIdx.x), range_start(head, tiles, blockIdx.x + 1), tiles, (Product::k(a) + kSlice - 1) / kSlice);
+    const int tiles = Product::tiles(a), slices = (Product::k(a) + kSlice - 1) / kSlice;
+    return Segments(range_start(head, tiles, slices, blockIdx.x), range_start(head, tiles, slices, blockIdx.x + 1), tiles, slices);
 }
 
 // A warp's stages.
@@ -754,9 +779,10 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
         if (seg.pair != pair) {
             pair = seg.pair;
             stage_rows<Product>(a, head, shared + at.acts, reinterpret_cast<const unsigned long long*>(shared + at.masks),
-                                reinterpret_cast<const float*>(shared + at.weights), reinterpret_cast<const uint16_t*>(shared + at.ids), pairs[pair]);
+                                reinterpret_cast<const float*>(shared + at.weights), reinterpret_cast<const float*>(shared + at.backs),
+                                reinterpret_cast<const uint16_t*>(shared + at.ids), pairs[pair]);
         }
-        const bool wide = kMost > 1 && head->wide != 0;
+        const bool wide = kMost > 1 && head->wide != 0, slim = Product::kPairs && head->slim != 0;
         float acc[2][kMost][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -770,6 +796,7 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
             mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort);
             const int codes = st.codes + st.next * kSliceBytes, words = st.words + st.next * kWordBytes;
             if (wide) multiply<kMost, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
+            else if (slim) multiply<1, false>(shared, codes, words, scales, x, pitch, low, acc);
             else multiply<1, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
             __syncwarp();
             stream.ask();
@@ -807,6 +834,11 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
                             for (int i = 0; i < 4; ++i) acc[m][n][i] += sums[(w * kValues + (n * 2 + m) * 4 + i) * 32];
             }
         }
+        if (slim)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[m][0][i], 2);   // columns 4 away
         finish<kMost>(Product(), a, head, seg.unit - seg.pair * seg.tiles, cols, acc);
     }
 }
@@ -841,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
     meet(a, 0);
     list_pairs(a, head, reinterpret_cast<unsigned long long*>(shared + at.masks), weights, reinterpret_cast<uint16_t*>(shared + at.ids), list,
-               at.list_size);
+               at.list_size, reinterpret_cast<float*>(shared + at.backs));
     const Pairs pairs{list, at.list_size, head->narrow};
     Stages st{at.codes + warp * kStages * kSliceBytes, at.words + warp * kStages * kWordBytes, smem_addr(head->full[warp]), 0, 0u};
     const uint32_t codes = smem_addr(shared + st.codes), words = smem_addr(shared + st.words);
@@ -856,6 +888,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) stream.ask();
         meet(a, 1);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads)   // a barrier of stage_rows is ahead of their use
+            lift(__uint_as_float(__ldcg(a.tops + i)), reinterpret_cast<float*>(shared + at.backs) + i);
         product<Down, kStages, kMost>(a, at, shared, stream, pairs, st);
     }
     if (*static_cast<volatile int*>(&head->abort) != 0 && lane_id() == 0)   // copies that a wait gave up on may be on their way
@@ -874,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 // Sets the rows of a pass and the stages, and gives the shared memory, or 0 where it does not fit.
 int shape(ExpertsArgs* a) {
     // 16 rows where an expert has 8 on average, else 8: an expert with more than 8 is read twice then, but the others' stages
-    // have the room (64 tokens, 6 of 64, 4096 x 2048: ## us with 16, ## with 8; 2 of 8: ## and ##).
+    // have the room (32 tokens, 8 of 64, 2048 x 1408: 93 us with 16, 85 with 8; 64 tokens, 2 of 8, 4096 x 2048: 74.5 and 77).
     for (int cols = a->tokens > 8 && a->tokens * a->top_k >= 8 * a->experts ? 2 : 1; cols >= 1; --cols) {
         a->passes_rows = 8 * cols;
         for (a->stages = 4; a->stages >= 2; --a->stages) {

@@ -61,6 +61,8 @@ class MXFP4Experts:
         """Y [T, dim] in bf16 for bf16 x [T, dim] and logits [T, experts] in fp32 or bf16."""
         if x.dtype is not torch.bfloat16:
             raise ValueError(f"x: bf16, not {x.dtype}")
+        if not abi.is_current(self._gpu):
+            raise ValueError("the layer's GPU is not the current device")
         flags = self._flags
         if logits.dtype is torch.float32:
             flags |= abi.MXFP4_EXPERTS_LOGITS_F32

@@ -70,6 +70,8 @@ class LayerNorm:
 
     def forward(self, x, weight=None, bias=None, stream=None):
         """Y [R, dim] in the type of the rows."""
+        if not abi.is_current(self._gpu):
+            raise ValueError("the layer's GPU is not the current device")
         rows, pitch = self._check_rows(x, "x")
         samples, flags, kind = 1, self._flags, None
         for v, what in ((weight, "weight"), (bias, "bias")):
@@ -93,6 +95,8 @@ class LayerNorm:
             raise ValueError("backward needs the statistics of a training layer")
         if self._last is None:
             raise ValueError("no forward before")
+        if not abi.is_current(self._gpu):
+            raise ValueError("the layer's GPU is not the current device")
         rows, samples, flags, kind, has_weight, has_bias = self._last
         (n, pitch), (nx, ldx) = self._check_rows(dy, "dy"), self._check_rows(x, "x")
         if n != rows or nx != rows:

@@ -70,6 +70,8 @@ class GradNorm:
     def _run(self, addresses, dtype, max_norm, flags, stream):
         if not max_norm > 0:
             raise ValueError(f"a largest norm above 0, not {max_norm}")
+        if not abi.is_current(self._gpu):
+            raise ValueError("the parameters' GPU is not the current device")
         self._grads[:] = addresses
         if dtype is torch.float32:
             flags |= abi.MXFP4_GRAD_F32
@@ -168,23 +170,28 @@ class AdamW:
                     [-(-n // abi.MXFP4_ADAMW_BLOCK) for n in self._numel])
         self._table["n"] = self._numel
 
-    def step(self, grads, step=None, lr=None, grad_scale=1.0, dynamic=None, stream=None, max_norm=None):
+    def step(self, grads, step=None, lr=None, grad_scale=1.0, dynamic=None, stream=None, max_norm=None,
+             grad_factor=None):
         """One update with the gradients (contiguous, all fp32 or all bf16, in the order of the
         parameters).  step: this step's number (default: counted from 1); grad_scale: a factor on
         every gradient; dynamic: a CUDA fp32 tensor [lr, 1 - beta1^step, 1 - beta2^step, grad_scale]
         (with a seed, and step) that takes their place, for steps captured in a graph.  max_norm: the
         gradients, as they are given, are scaled down to that norm where theirs is larger; their
-        norm and the factor are then in `grad_norm.out`."""
+        norm and the factor are then in `grad_norm.out`.  grad_factor: one CUDA fp32 that grad_scale is
+        multiplied by, the factor of a GradNorm over more parameters than these (`out[1:]`)."""
         dtype = _check_grads(grads, self._numel, self._gpu)
         if dynamic is not None and (dynamic.dtype != torch.float32 or dynamic.numel() != self._dynamic or
                                     not dynamic.is_contiguous() or dynamic.get_device() != self._gpu):
             raise ValueError(f"dynamic: {self._dynamic} consecutive fp32 on the parameters' GPU")
+        if grad_factor is not None and (max_norm is not None or grad_factor.dtype != torch.float32 or
+                                        grad_factor.numel() != 1 or grad_factor.get_device() != self._gpu):
+            raise ValueError("grad_factor: one fp32 on the parameters' GPU, and no max_norm beside it")
         if step is None:
             step = self.steps + 1
         addresses = list(map(_address, grads))
         self._grads[:] = addresses
         flags = self._flags | (abi.MXFP4_ADAMW_G_F32 if dtype == torch.float32 else 0)
-        factor = None
+        factor = None if grad_factor is None else grad_factor.data_ptr()
         if max_norm is not None:
             if self.grad_norm is None:
                 raise ValueError(f"max_norm: for up to {abi.MXFP4_GRAD_MAX_TENSORS} parameters")

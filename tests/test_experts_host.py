@@ -42,7 +42,7 @@ def test_misaligned_addresses_are_refused(bad):
 def test_workspace_tells_what_fits():
     for t in (0, 1, 8, 9, 64):
         for experts, top_k in ((1, 1), (64, 8), (1024, 16)):
-            assert abi.mxfp4_experts_workspace_bytes(t, experts, top_k, 7168, 3584) >= 4 * t * top_k * 10752
+            assert abi.mxfp4_experts_workspace_bytes(t, experts, top_k, 7040, 3456) >= 4 * t * top_k * 10496
     for bad in (dict(dim=12000), dict(inner=6000), dict(tokens=65), dict(top_k=9), dict(experts=0)):
         with pytest.raises(abi.Mxfp4Error):
             abi.mxfp4_experts_workspace_bytes(**{**SIZES, **bad})
@@ -86,6 +86,13 @@ def test_x_is_checked(layer, x):
 def test_logits_are_checked(layer, logits):
     with pytest.raises(ValueError):
         layer.forward(gpu(4, 256), logits, *layer.blobs)
+    assert not layer.made
+
+
+def test_another_current_device_is_refused(layer, monkeypatch):
+    monkeypatch.setattr(abi, "is_current", lambda gpu: gpu != 0)
+    with pytest.raises(ValueError, match="current device"):
+        layer.forward(gpu(4, 256), gpu(4, 8), *layer.blobs)
     assert not layer.made
 
 

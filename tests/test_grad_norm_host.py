@@ -76,6 +76,30 @@ def test_gradients_are_checked(calls):
     assert first[2:4] == (abi.MXFP4_GRAD_F32, math.inf) and second[2:4] == (abi.MXFP4_GRAD_SCALE, 2.0)
 
 
+def test_another_current_device_is_refused(calls, monkeypatch):
+    norm, opt = optim.GradNorm(tensors()), optim.AdamW(tensors())
+    monkeypatch.setattr(abi, "is_current", lambda gpu: gpu != 0)
+    for f in (norm.measure, lambda g, m: opt.step(g, max_norm=m)):
+        with pytest.raises(ValueError, match="current device"):
+            f(tensors(), 1.0)
+    assert not calls and opt.steps == 0
+
+
+def test_a_factor_from_outside_is_checked(calls):
+    opt = optim.AdamW(tensors())
+    from test_adamw_calls_host import OnTheGpu
+    good = torch.ones(1).as_subclass(OnTheGpu)
+    for bad in (torch.ones(1), torch.ones(2).as_subclass(OnTheGpu), torch.ones(1, dtype=torch.float64).as_subclass(OnTheGpu),
+                torch.ones(1).as_subclass(OnAnotherGpu)):
+        with pytest.raises(ValueError, match="grad_factor"):
+            opt.step(tensors(), grad_factor=bad)
+    with pytest.raises(ValueError, match="grad_factor"):
+        opt.step(tensors(), grad_factor=good, max_norm=1.0)
+    assert not calls and opt.steps == 0
+    opt.step(tensors(), grad_factor=good)
+    assert calls[0][1][3].grad_factor == good.data_ptr()
+
+
 def test_a_step_takes_the_factor_from_the_norm(calls):
     opt = optim.AdamW(tensors())
     grads = tensors()

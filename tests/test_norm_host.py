@@ -126,6 +126,16 @@ def test_vectors_of_two_kinds_are_refused(layer):
     assert not layer.made
 
 
+def test_another_current_device_is_refused(layer, monkeypatch):
+    layer.forward(gpu(4, 64))
+    layer.made.clear()
+    monkeypatch.setattr(abi, "is_current", lambda gpu: gpu != 0)
+    for f in (lambda: layer.forward(gpu(4, 64)), lambda: layer.backward(gpu(4, 64), gpu(4, 64))):
+        with pytest.raises(ValueError, match="current device"):
+            f()
+    assert not layer.made
+
+
 def test_backward_goes_with_the_last_forward(layer):
     x, w = gpu(4, 64), gpu(2, 64)
     with pytest.raises(ValueError, match="no forward"):
