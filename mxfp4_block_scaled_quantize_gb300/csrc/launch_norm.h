@@ -22,6 +22,9 @@ inline int norm_chunks(int64_t dim) {
 inline int64_t norm_slots(int64_t dim) { return 2 * norm_chunks(dim); }
 constexpr int64_t kNormLeastRows = 4;    // of a CTA, where there are few: a partial row costs as much as two rows of x
 
+// How rows are read and written: norm_row.cuh.
+enum NormAccess { kNormSingle, kNormWide, kNormShifted };
+
 struct NormArgs {
     const void* x;
     const void* dy;          // backward
@@ -35,11 +38,14 @@ struct NormArgs {
     int64_t ldx, lddy, ldy;
     int64_t rows;
     int64_t sample_rows;     // rows of a sample
-    int64_t chunk_rows;      // backward: rows of a CTA, all of one sample
-    int32_t chunks;          // backward: of a sample
+    int64_t chunk_rows;      // backward: rows of a CTA, all of one sample, every period-th from its first on
+    int32_t chunks;          // backward: CTAs of a sample, of which the first `period` start at its first rows
+    int32_t period;          // rows from one to the next that is shifted alike: 1 but for kNormShifted
+    NormAccess access;
     int32_t dim;
     float eps;
     int32_t w_f32;
+    int32_t w_wide;          // weight and bias start at multiples of 16 bytes
     int32_t add_one;
     int32_t stages;          // rows on their way to shared memory (its ring), where rows are copied there
     uint32_t* err;

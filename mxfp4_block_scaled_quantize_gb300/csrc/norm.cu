@@ -20,6 +20,39 @@ bool shape_ok(int64_t rows, int64_t dim, int64_t samples) {
 // One row alone may have any pitch.
 bool pitch_ok(int64_t ld, int64_t dim, int64_t rows) { return rows <= 1 || (ld >= dim && ld <= (int64_t{1} << 40)); }
 
+// How the kernels may access these tensors of rows (null: not there), and the rows from one to the next that is shifted alike.
+// Shifted accesses cost every row some masks and a launch its edge rows; they are for bf16 rows that CTAs take, and, of a
+// backward pass, for many elements.  us shifted and single: forward 8192 rows of 4100 48 and 71, 16000 of 6001 126 and 161, 1111 of
+// 1001 5.2 and 6.1; backward 73 and 89, 141 and 202, 14.3 and 12.8, 5000 of 1531 24 and 27, 4000 of 777 16.6 and 15.9; fp32, 3000
+// of 2050, 13.3 and 14.0 forward, 26.5 and 23 backward; rows of 250, a warp's, 13.1 and 7.7.
+void set_access(mxfp4::NormArgs* a, bool f32, const void* const* rows, const int64_t* pitches, int count) {
+    const int64_t size = f32 ? 4 : 2;
+    uintptr_t base = 0;
+    bool wide = a->dim % 8 == 0, alike = true;
+    a->w_wide = aligned_to(a->weight, 16) && aligned_to(a->bias, 16);
+    int64_t step = 0;   // bytes from a row to the next, modulo 16; of one row alone: none
+    for (int i = 0; i < count; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(rows[i]) & 15u;
+        const int64_t by = a->rows > 1 ? (pitches[i] % 16) * size % 16 : 0;
+        if (i == 0) {
+            base = at;
+            step = by;
+        }
+        alike = alike && at == base && by == step;
+        wide = wide && at == 0 && by == 0;
+    }
+    a->period = 1;
+    if (wide) {
+        a->access = mxfp4::kNormWide;
+    } else if (alike && !f32 && a->dim > mxfp4::kNormWarpRowDim && a->dim + 7 <= MXFP4_NORM_MAX_DIM &&
+               (count == 2 || a->rows >= (int64_t{1} << 22) / a->dim)) {
+        a->access = mxfp4::kNormShifted;
+        while (step * a->period % 16 != 0) a->period *= 2;
+    } else {
+        a->access = mxfp4::kNormSingle;
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -62,6 +95,9 @@ mxfp4_status mxfp4_layer_norm(const void* x, int64_t rows, int64_t dim, int64_t 
     a.w_f32 = flags & MXFP4_NORM_W_F32 ? 1 : 0;
     a.add_one = flags & MXFP4_NORM_ADD_ONE ? 1 : 0;
     a.err = err;
+    const void* const tensors[2] = {x, y};
+    const int64_t pitches[2] = {ldx, ldy};
+    set_access(&a, flags & MXFP4_NORM_X_F32, tensors, pitches, 2);
     return mxfp4::launch_norm_forward(a, flags & MXFP4_NORM_X_F32, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MXFP4_OK
                : MXFP4_ERR_CUDA;
@@ -78,11 +114,24 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     if (!aligned_to(x, xe) || !aligned_to(dy, xe) || !aligned_to(dx, xe) || !aligned_to(weight, we) || !aligned_to(mean, 4) ||
         !aligned_to(rstd, 4) || !aligned_to(dw, 4) || !aligned_to(db, 4) || !aligned_to(workspace, 16))
         return MXFP4_ERR_MISALIGNED;
-    // Each CTA its rows of one sample, about as many for each as the whole has for norm_chunks(dim) CTAs.
+    mxfp4::NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = rows;
+    a.dim = static_cast<int32_t>(dim);
+    a.weight = weight;
+    const void* const tensors[3] = {x, dy, dx};
+    const int64_t pitches[3] = {ldx, lddy, lddx};
+    set_access(&a, flags & MXFP4_NORM_X_F32, tensors, pitches, 3);
+    // Each CTA its rows of one sample, shifted alike, about as many for each as the whole has for norm_chunks(dim) CTAs.
     const int64_t sample_rows = rows / samples;
     const int64_t even = cdiv(rows, mxfp4::norm_chunks(dim));
     const int64_t chunk_rows = even > mxfp4::kNormLeastRows ? even : mxfp4::kNormLeastRows;
-    const int64_t chunks = rows > 0 ? cdiv(sample_rows, chunk_rows) : 1;
+    int64_t chunks = rows > 0 ? a.period * cdiv(cdiv(sample_rows, a.period), chunk_rows) : 1;
+    if (a.period > 1 && samples * chunks > mxfp4::norm_slots(dim)) {   // many short samples: their partial rows would not fit
+        a.access = mxfp4::kNormSingle;
+        a.period = 1;
+        chunks = cdiv(sample_rows, chunk_rows);
+    }
     const int64_t ctas = samples * chunks;   // with several chunks a sample: at most rows / chunk_rows + samples, norm_slots(dim)
     const bool partial = chunks > 1 && (dw != nullptr || db != nullptr);
     size_t need = 0;
@@ -100,11 +149,8 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
             if (v != nullptr && cudaMemsetAsync(v, 0, bytes, s) != cudaSuccess) return MXFP4_ERR_CUDA;
         return MXFP4_OK;
     }
-    mxfp4::NormArgs a;
-    std::memset(&a, 0, sizeof(a));
     a.x = x;
     a.dy = dy;
-    a.weight = weight;
     a.y = dx;
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
@@ -114,11 +160,9 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     a.ldx = ldx;
     a.lddy = lddy;
     a.ldy = lddx;
-    a.rows = rows;
     a.sample_rows = sample_rows;
     a.chunk_rows = chunk_rows;
     a.chunks = static_cast<int32_t>(chunks);
-    a.dim = static_cast<int32_t>(dim);
     a.w_f32 = flags & MXFP4_NORM_W_F32 ? 1 : 0;
     a.add_one = flags & MXFP4_NORM_ADD_ONE ? 1 : 0;
     a.err = err;

@@ -16,10 +16,11 @@
 namespace mxfp4 {
 namespace {
 
-template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+template <bool kF32, NormAccess kAccess, int kGroups, RowMode kMode, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) uint8_t slots[];
-    using Part = RowPart<kF32, kWide, kGroups>;
+    using Part = RowPart<kF32, kAccess, kGroups>;
+    constexpr bool kWide = Part::kWide;
     constexpr int kE = Part::kElements, kP = Part::kPairs;
     constexpr int kSize = kF32 ? 4 : 2;
     constexpr int kWarps = kThreads / 32;
@@ -29,12 +30,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     __shared__ float sums[kWarp ? kWarps : 1][kWarp ? 32 * kE : 1];
     const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
     const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
-    const RowShape shape{a.dim, t, threads};
+    // rows first, first + period, ..., chunk_rows of them at most
     const int64_t sample = blockIdx.x / a.chunks;
-    const int64_t in_sample = static_cast<int64_t>(blockIdx.x % a.chunks) * a.chunk_rows;
+    const int32_t chunk = blockIdx.x % a.chunks;
+    const int64_t in_sample = chunk % a.period + static_cast<int64_t>(chunk / a.period) * a.chunk_rows * a.period;
     const int64_t first = sample * a.sample_rows + in_sample;
-    const int64_t end = sample * a.sample_rows + min(in_sample + a.chunk_rows, a.sample_rows);
-    const int64_t stride = kWarp ? kWarps : 1;
+    const int64_t end = sample * a.sample_rows + min(in_sample + a.chunk_rows * a.period, a.sample_rows);
+    const int64_t stride = (kWarp ? kWarps : 1) * static_cast<int64_t>(a.period);
+    const int skew = Part::kShifted ? static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const uint8_t*>(a.x) + first * a.ldx * kSize) & 15u) : 0;
+    const RowShape shape{a.dim, t, threads, skew / kSize};
     const float inv = 1.0f / static_cast<float>(a.dim);
     const uint8_t *const xs = static_cast<const uint8_t*>(a.x), *const ys = static_cast<const uint8_t*>(a.dy);
     const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize, part_bytes = ring_bytes<kWide>(bytes);
@@ -56,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         ring_copy<kWide>(to + part_bytes, y, bytes, bar);
     };
     if (kRing && threadIdx.x == 0)
-        for (int i = 0; i < a.stages && first + i < end; ++i) copy(first + i, i);
+        for (int i = 0; i < a.stages && first + i * stride < end; ++i) copy(first + i * stride, i);
     uint64_t g[kP], dw[kP], db[kP];
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -65,16 +69,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         db[i] = 0ull;
     }
     if (a.weight != nullptr) {
-        load_vector<kF32, kWide, kGroups>(a.weight, sample * a.dim, a.w_f32, shape, g);
+        load_vector<kF32, kAccess, kGroups>(a.weight, sample * a.dim, a.w_f32, a.w_wide, shape, g);
         if (a.add_one)
 #pragma unroll
             for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
     }
-    int64_t row = first + (kWarp ? threadIdx.x >> 5 : 0);
+    int64_t row = first + (kWarp ? static_cast<int64_t>(threadIdx.x >> 5) * a.period : 0);
     Part nx, ny;
     float nmean = 0.0f, nrstd = 0.0f;
     auto fetch = [&](int64_t r) {
-        if (!kRing) {
+        if constexpr (!kRing) {
             nx.load(xs + r * a.ldx * kSize, shape);
             ny.load(ys + r * a.lddy * kSize, shape);
         }
@@ -85,16 +89,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     int turn = 0, slot = 0;
     uint32_t phase = 0;
     for (; row < end; row += stride, turn ^= 1) {
-        if (kRing) {
+        if constexpr (kRing) {
             ring_wait(ring, slot, phase, a.err);
             const uint8_t *const x = xs + row * a.ldx * kSize, *const y = ys + row * a.lddy * kSize;
+            uint8_t* const in = slots + 2 * slot * part_bytes;
             if (ring_edge<kWide>(row, a.rows)) {
-                nx.load(x, shape);
-                ny.load(y, shape);
-            } else {
-                nx.template load<true>(slots + 2 * slot * part_bytes + ring_skew<kWide>(x), shape);
-                ny.template load<true>(slots + (2 * slot + 1) * part_bytes + ring_skew<kWide>(y), shape);
+                ring_fill<kF32>(in + ring_skew<kWide>(x), x, a.dim);
+                ring_fill<kF32>(in + part_bytes + ring_skew<kWide>(y), y, a.dim);
+                __syncthreads();
             }
+            nx.template load<true>(in + ring_skew<kWide>(x), shape);
+            ny.template load<true>(in + part_bytes + ring_skew<kWide>(y), shape);
         }
         const float mean = nmean, rstd = nrstd;
         uint64_t xh[kP], c[kP], sa = 0ull, sx = 0ull;
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         const float2 s1 = unpack2(sa), s2 = unpack2(sx);
         const float2 sum = row_sum2<kMode, kWarps>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y)), shared[turn]);
         if (kRing) {
-            if (threadIdx.x == 0 && row + a.stages < end) copy(row + a.stages, slot);
+            if (threadIdx.x == 0 && row + a.stages * stride < end) copy(row + a.stages * stride, slot);
             if (++slot == a.stages) {
                 slot = 0;
                 phase ^= 1u;
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
                 out[c] = s;
             }
         } else if (kWide && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
-            RowPart<true, true, kGroups>::store(out, v, shape);
+            RowPart<true, kNormWide, kGroups>::store(out, v, shape);
         } else {
 #pragma unroll
             for (int k = 0; k < kP; ++k) {
@@ -183,12 +188,6 @@ __global__ void __launch_bounds__(32 * kStrips) norm_reduce_kernel(const __grid_
     }
 }
 
-bool wide(const NormArgs& a) {
-    const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
-                          reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.weight);
-    return (all & 15u) == 0 && a.dim % 8 == 0 && (a.rows == 1 || (a.ldx % 8 == 0 && a.ldy % 8 == 0 && a.lddy % 8 == 0));
-}
-
 template <typename Args>
 cudaError_t launch_dependent(void (*kernel)(Args), const Args& a, dim3 grid, int threads, int smem, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
@@ -205,13 +204,13 @@ cudaError_t launch_dependent(void (*kernel)(Args), const Args& a, dim3 grid, int
 }
 
 // kCtas: CTAs that an SM holds, by registers.
-template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+template <bool kF32, NormAccess kAccess, int kGroups, RowMode kMode, int kThreads, int kCtas>
 cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
-    const auto kernel = norm_backward_kernel<kF32, kWide, kGroups, kMode, kThreads, kCtas>;
-    const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
+    const auto kernel = norm_backward_kernel<kF32, kAccess, kGroups, kMode, kThreads, kCtas>;
+    const int threads = kMode == kWarpRow ? kThreads : row_threads(columns_of(a), kGroups);
     // The ring: as many rows as fit beside the CTAs that share the SM.
     constexpr int kBudget = 208 * 1024 / kCtas;
-    const int slot_bytes = 2 * static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
+    const int slot_bytes = 2 * static_cast<int>(ring_bytes<kAccess == kNormWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStagesBackward ? kBudget / slot_bytes : kNormStagesBackward;
     if (kMode == kRingRow) {   // once a device: the call costs the host as much as a launch
         static std::atomic<uint64_t> known{0};
@@ -228,22 +227,26 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
     return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), threads, a.stages * slot_bytes, stream);
 }
 
-template <bool kF32, bool kWide>
+template <bool kF32, NormAccess kAccess>
 cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
-    if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256, 2>(a, ctas, stream);
-    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256, 2>(a, ctas, stream);
-    if (a.dim <= 1024) return launch<kF32, kWide, 2, kRingRow, 64, 8>(a, ctas, stream);
-    if (a.dim <= 2048) return launch<kF32, kWide, 2, kRingRow, 128, 4>(a, ctas, stream);
-    if (a.dim <= 4096) return launch<kF32, kWide, 2, kRingRow, 256, 2>(a, ctas, stream);
-    if (a.dim <= 8192) return launch<kF32, kWide, 2, kRingRow, 512, 1>(a, ctas, stream);
-    return launch<kF32, kWide, 2, kRingRow, 1024, 1>(a, ctas, stream);
+    const int columns = columns_of(a);
+    if constexpr (kAccess != kNormShifted) {
+        if (columns <= 256) return launch<kF32, kAccess, 1, kWarpRow, 256, 2>(a, ctas, stream);
+        if (columns <= kNormWarpRowDim) return launch<kF32, kAccess, 2, kWarpRow, 256, 2>(a, ctas, stream);
+    }
+    if (columns <= 1024) return launch<kF32, kAccess, 2, kRingRow, 64, 8>(a, ctas, stream);
+    if (columns <= 2048) return launch<kF32, kAccess, 2, kRingRow, 128, 4>(a, ctas, stream);
+    if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 2>(a, ctas, stream);
+    if (columns <= 8192) return launch<kF32, kAccess, 2, kRingRow, 512, 1>(a, ctas, stream);
+    return launch<kF32, kAccess, 2, kRingRow, 1024, 1>(a, ctas, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_backward(const NormArgs& a, bool f32, int64_t ctas, cudaStream_t stream) {
-    if (wide(a)) return f32 ? launch<true, true>(a, ctas, stream) : launch<false, true>(a, ctas, stream);
-    return f32 ? launch<true, false>(a, ctas, stream) : launch<false, false>(a, ctas, stream);
+    if (a.access == kNormWide) return f32 ? launch<true, kNormWide>(a, ctas, stream) : launch<false, kNormWide>(a, ctas, stream);
+    if (a.access == kNormShifted) return launch<false, kNormShifted>(a, ctas, stream);
+    return f32 ? launch<true, kNormSingle>(a, ctas, stream) : launch<false, kNormSingle>(a, ctas, stream);
 }
 
 cudaError_t launch_norm_reduce(const NormReduceArgs& a, cudaStream_t stream) {

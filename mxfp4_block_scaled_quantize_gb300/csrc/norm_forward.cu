@@ -19,20 +19,22 @@
 namespace mxfp4 {
 namespace {
 
-template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+template <bool kF32, NormAccess kAccess, int kGroups, RowMode kMode, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) uint8_t slots[];
     __shared__ float4 parts[2][32];   // of a row's warps: m, r, squares
     __shared__ RowRing ring;
-    using Part = RowPart<kF32, kWide, kGroups>;
-    constexpr int kP = Part::kPairs, kWarps = kThreads / 32;
+    using Part = RowPart<kF32, kAccess, kGroups>;
+    constexpr bool kWide = Part::kWide;
+    constexpr int kP = Part::kPairs, kWarps = kThreads == 320 ? 16 : kThreads / 32;   // of a row's sums: a power of two
     constexpr int kSize = kF32 ? 4 : 2;
     constexpr bool kWarp = kMode == kWarpRow, kRing = kMode == kRingRow;
     const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
     const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
-    const RowShape shape{a.dim, t, threads};
-    const int64_t stride = kWarp ? static_cast<int64_t>(gridDim.x) * (kThreads / 32) : gridDim.x;
+    const int64_t stride = kWarp ? static_cast<int64_t>(gridDim.x) * (kThreads / 32) : gridDim.x;   // whole periods, if there is a second row
     int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const int skew = Part::kShifted ? static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const uint8_t*>(a.x) + row * a.ldx * kSize) & 15u) : 0;
+    const RowShape shape{a.dim, t, threads, skew / kSize};
     const float inv = 1.0f / static_cast<float>(a.dim);
     const uint8_t* const xs = static_cast<const uint8_t*>(a.x);
     const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize, slot_bytes = ring_bytes<kWide>(bytes);
@@ -62,11 +64,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
     }
     // elements of this warp, and of the warp that this lane stands for when the warps' parts are joined
     auto elements = [&](int warp) {
-        const RowShape first{a.dim, kWarp ? 0 : 32 * warp, threads};
+        const RowShape first{a.dim, kWarp ? 0 : 32 * warp, threads, shape.shift};
         int n = 0;
 #pragma unroll
-        for (int k = 0; k < 2 * kP; k += Part::kTurn)
-            n += min(max(a.dim - Part::column(k, first), 0), 32 * Part::kTurn);
+        for (int k = 0; k < 2 * kP; k += Part::kTurn) {
+            const int c = Part::column(k, first);
+            n += max(min(a.dim, c + 32 * Part::kTurn) - max(c, 0), 0);
+        }
         return n;
     };
     const int joined = kWarp ? 0 : static_cast<int>(lane_id()) & (kWarps - 1);
@@ -79,7 +83,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
     int turn = 0;
     int64_t sample = -1;
     Part next;
-    if (!kRing && row < a.rows) next.load(xs + row * a.ldx * kSize, shape);
+    if constexpr (!kRing)
+        if (row < a.rows) next.load(xs + row * a.ldx * kSize, shape);
     int slot = 0;
     uint32_t phase = 0;
     for (; row < a.rows; row += stride) {
@@ -87,18 +92,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
         if (s != sample) {
             sample = s;
             if (a.weight != nullptr) {
-                load_vector<kF32, kWide, kGroups>(a.weight, s * a.dim, a.w_f32, shape, g);
+                load_vector<kF32, kAccess, kGroups>(a.weight, s * a.dim, a.w_f32, a.w_wide, shape, g);
                 if (a.add_one)
 #pragma unroll
                     for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
             }
-            if (a.bias != nullptr) load_vector<kF32, kWide, kGroups>(a.bias, s * a.dim, a.w_f32, shape, b);
+            if (a.bias != nullptr) load_vector<kF32, kAccess, kGroups>(a.bias, s * a.dim, a.w_f32, a.w_wide, shape, b);
         }
-        if (kRing) {
+        if constexpr (kRing) {
             ring_wait(ring, slot, phase, a.err);
             const uint8_t* const from = xs + row * a.ldx * kSize;
-            if (ring_edge<kWide>(row, a.rows)) next.load(from, shape);
-            else next.template load<true>(slots + slot * slot_bytes + ring_skew<kWide>(from), shape);
+            uint8_t* const in = slots + slot * slot_bytes + ring_skew<kWide>(from);
+            if (ring_edge<kWide>(row, a.rows)) {
+                ring_fill<kF32>(in, from, a.dim);
+                __syncthreads();
+            }
+            next.template load<true>(in, shape);
         }
         uint64_t x[kP], sum = 0ull;
 #pragma unroll
@@ -106,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
             x[i] = next.pair(i);
             sum = add2(sum, x[i]);
         }
-        if (!kRing && row + stride < a.rows) next.load(xs + (row + stride) * a.ldx * kSize, shape);
+        if constexpr (!kRing)
+            if (row + stride < a.rows) next.load(xs + (row + stride) * a.ldx * kSize, shape);
         const float2 halves = unpack2(sum);
         float mean = lanes_sum<32>(halves.x + halves.y) * inv_own;
         uint64_t square = 0ull;
@@ -155,22 +165,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
     if (kRing && threadIdx.x == 0) ring_drain(ring, a.stages, issued);
 }
 
-bool wide(const NormArgs& a) {
-    const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
-                          reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.bias);
-    return (all & 15u) == 0 && a.dim % 8 == 0 && (a.rows == 1 || (a.ldx % 8 == 0 && a.ldy % 8 == 0));
-}
-
 // kCtas: CTAs that an SM holds at least, by registers.
-template <bool kF32, bool kWide, int kGroups, RowMode kMode, int kThreads, int kCtas>
+template <bool kF32, NormAccess kAccess, int kGroups, RowMode kMode, int kThreads, int kCtas>
 cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
-    const auto kernel = norm_forward_kernel<kF32, kWide, kGroups, kMode, kThreads, kCtas>;
-    const int threads = kMode == kWarpRow ? kThreads : row_threads(a.dim, kGroups);
+    const auto kernel = norm_forward_kernel<kF32, kAccess, kGroups, kMode, kThreads, kCtas>;
+    const int threads = kMode == kWarpRow ? kThreads : row_threads(columns_of(a), kGroups);
     const int64_t need = kMode == kWarpRow ? (a.rows + kThreads / 32 - 1) / (kThreads / 32) : a.rows;
     // The ring: three rows, if they fit beside the CTAs that share the SM.  More CTAs hide more than deeper rings do: 4608 rows of
     // 5120 take 19.9 us with 3 rows, 20.5 with 4, 21.9 with 6, and 26 with 8 in rings that left room for two CTAs.
-    constexpr int kBudget = kThreads <= 128 ? 32 * 1024 : kThreads <= 256 ? 64 * 1024 : 192 * 1024;
-    const int row_bytes = static_cast<int>(ring_bytes<kWide>(a.dim * (kF32 ? 4 : 2)));
+    constexpr int kBudget = kThreads <= 128 ? 32 * 1024 : kThreads <= 320 ? 64 * 1024 : 192 * 1024;
+    const int row_bytes = static_cast<int>(ring_bytes<kAccess == kNormWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / row_bytes < kNormStagesForward ? kBudget / row_bytes : kNormStagesForward;
     const int smem = a.stages * row_bytes;
     // CTAs that an SM holds, by device and warps of the CTA: by registers and threads, and then by the rings
@@ -193,7 +197,7 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(need <= most ? need : most / a.period * a.period), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -206,27 +210,33 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
 // some 16 elements (8192 rows of 4096: 33 us with 16, 26 with 32; 16384 of 8192: 149 and 88); 16 where they do not, which the
 // registers of the single accesses' addresses fill.  A warp's row wins up to 1024 elements: 32768 rows of 1024 take 26 us, 46 as
 // a CTA's.  Now 5.3 TB/s at 4096, 6.1 at 8192, 4.7 for 4608 rows of 5120.
-template <bool kF32, bool kWide>
+template <bool kF32, NormAccess kAccess>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
-    if (a.dim <= 256) return launch<kF32, kWide, 1, kWarpRow, 256, 1>(a, sms, stream);
-    if (a.dim <= kNormWarpRowDim) return launch<kF32, kWide, 2, kWarpRow, 256, 1>(a, sms, stream);
-    if (kWide) {
-        if (a.dim <= 1024) return launch<kF32, true, 4, kWarpRow, 128, 4>(a, sms, stream);
-        if (a.dim <= 4096) return launch<kF32, true, 4, kRingRow, 128, 4>(a, sms, stream);
-        if (a.dim <= 8192) return launch<kF32, true, 4, kRingRow, 256, 2>(a, sms, stream);
-        return launch<kF32, true, 4, kRingRow, 512, 1>(a, sms, stream);
+    const int columns = columns_of(a);
+    if constexpr (kAccess != kNormShifted) {
+        if (columns <= 256) return launch<kF32, kAccess, 1, kWarpRow, 256, 1>(a, sms, stream);
+        if (columns <= kNormWarpRowDim) return launch<kF32, kAccess, 2, kWarpRow, 256, 1>(a, sms, stream);
     }
-    if (a.dim <= 2048) return launch<kF32, false, 2, kRingRow, 128, 1>(a, sms, stream);
-    if (a.dim <= 4096) return launch<kF32, false, 2, kRingRow, 256, 1>(a, sms, stream);
-    if (a.dim <= 8192) return launch<kF32, false, 2, kRingRow, 512, 1>(a, sms, stream);
-    return launch<kF32, false, 2, kRingRow, 1024, 1>(a, sms, stream);
+    if constexpr (kAccess == kNormWide) {
+        if (columns <= 1024) return launch<kF32, kAccess, 4, kWarpRow, 128, 4>(a, sms, stream);
+        if (columns <= 4096) return launch<kF32, kAccess, 4, kRingRow, 128, 4>(a, sms, stream);
+        if (columns <= 8192) return launch<kF32, kAccess, 4, kRingRow, 256, 2>(a, sms, stream);
+        return launch<kF32, kAccess, 4, kRingRow, 512, 1>(a, sms, stream);
+    } else {
+        if (columns <= 2048) return launch<kF32, kAccess, 2, kRingRow, 128, 4>(a, sms, stream);
+        if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 2>(a, sms, stream);
+        if (columns <= 5120) return launch<kF32, kAccess, 2, kRingRow, 320, 2>(a, sms, stream);
+        if (columns <= 8192) return launch<kF32, kAccess, 2, kRingRow, 512, 1>(a, sms, stream);
+        return launch<kF32, kAccess, 2, kRingRow, 1024, 1>(a, sms, stream);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_norm_forward(const NormArgs& a, bool f32, int sms, cudaStream_t stream) {
-    if (wide(a)) return f32 ? launch<true, true>(a, sms, stream) : launch<false, true>(a, sms, stream);
-    return f32 ? launch<true, false>(a, sms, stream) : launch<false, false>(a, sms, stream);
+    if (a.access == kNormWide) return f32 ? launch<true, kNormWide>(a, sms, stream) : launch<false, kNormWide>(a, sms, stream);
+    if (a.access == kNormShifted) return launch<false, kNormShifted>(a, sms, stream);
+    return f32 ? launch<true, kNormSingle>(a, sms, stream) : launch<false, kNormSingle>(a, sms, stream);
 }
 
 }  // namespace mxfp4

@@ -36,42 +36,61 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// A row, and a thread's place in it.
+// A row, and a thread's place in it.  shift: kShifted rows, elements by which a row starts behind a multiple of 16 bytes.
 struct RowShape {
-    int dim, t, threads;
+    int dim, t, threads, shift;
 };
 
-// A thread's 8 kGroups elements of a row.  kWide: groups of 8 consecutive elements, one or two 16-byte
-// accesses each (pitches and dim are multiples of 8 and every address of 16 bytes); else pairs of bf16, in one
-// access where the row starts at a multiple of 4 bytes, or single fp32.  Threads past the row hold zeros.
-template <bool kF32, bool kWide, int kGroups>
+// A thread's 8 kGroups elements of a row, zeros outside it.
+//   kWide     groups of 8 consecutive elements, one or two 16-byte accesses each: pitches and dim are multiples of 8, and
+//             every address of 16 bytes
+//   kShifted  the same at the multiples of 16 bytes around a row of bf16 that starts behind one, in its slot of the ring: a
+//             thread's columns then go by the row's shift, which is that of every a.period-th row, and which all of a CTA's
+//             rows have in common.  Groups that reach over the row's ends are masked, and stored element by element.
+//   kSingle   pairs of bf16, in one access where the row starts at a multiple of 4 bytes, or single fp32: where x, y and dy
+//             are not shifted alike
+template <bool kF32, NormAccess kAccess, int kGroups>
 struct RowPart {
+    static constexpr bool kWide = kAccess == kNormWide, kShifted = kAccess == kNormShifted;
     static constexpr int kElements = 8 * kGroups;
     static constexpr int kPairs = kElements / 2;
     static constexpr int kWords = kElements / (kF32 ? 1 : 2);
-    static constexpr int kTurn = kWide ? 8 : kF32 ? 1 : 2;   // neighbours that a thread takes together
+    static constexpr int kTurn = kWide || kShifted ? 8 : kF32 ? 1 : 2;   // neighbours that a thread takes together
     uint32_t w[kWords];
 
     __device__ __forceinline__ static int column(int k, const RowShape& s) {
-        return ((k / kTurn) * s.threads + s.t) * kTurn + k % kTurn;
+        return ((k / kTurn) * s.threads + s.t) * kTurn + k % kTurn - (kShifted ? s.shift : 0);
     }
-    __device__ __forceinline__ static bool inside(int k, const RowShape& s) { return column(k, s) < s.dim; }
+    __device__ __forceinline__ static bool inside(int k, const RowShape& s) {
+        return kShifted ? static_cast<unsigned>(column(k, s)) < static_cast<unsigned>(s.dim) : column(k, s) < s.dim;
+    }
+    // kShifted: is all of group j inside.
+    __device__ __forceinline__ static bool whole(int j, const RowShape& s) {
+        const int c = column(8 * j, s);
+        return c >= 0 && c + 8 <= s.dim;
+    }
 
-    // kPadded: the bytes behind the row may be read (its slot in shared memory).
+    // kPadded: the bytes around the row, up to multiples of 16, may be read (its slot in shared memory).
     template <bool kPadded = false>
     __device__ __forceinline__ void load(const void* row, const RowShape& s) {
+        static_assert(!kShifted || (kPadded && !kF32), "shifted rows: bf16, from the ring");
         const uint8_t* const p = static_cast<const uint8_t*>(row);
-        if (kWide) {
+        if (kWide || kShifted) {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 constexpr int kLoads = kF32 ? 2 : 1;
+                const bool some = kShifted ? column(8 * j, s) > -8 && column(8 * j, s) < s.dim : inside(8 * j, s);
 #pragma unroll
                 for (int h = 0; h < kLoads; ++h) {
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (inside(8 * j, s)) v = reinterpret_cast<const uint4*>(p + static_cast<int64_t>(column(8 * j, s)) * (kF32 ? 4 : 2))[h];
+                    if (some) v = reinterpret_cast<const uint4*>(p + static_cast<int64_t>(column(8 * j, s)) * (kF32 ? 4 : 2))[h];
                     uint32_t* const d = w + (j * kLoads + h) * 4;
                     d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
                 }
+                if (kShifted && !whole(j, s))
+#pragma unroll
+                    for (int k = 8 * j; k < 8 * j + 8; ++k)
+                        if (!inside(k, s)) w[k >> 1] &= k & 1 ? 0xFFFFu : 0xFFFF0000u;
             }
         } else if (kF32) {
 #pragma unroll
@@ -113,13 +132,22 @@ struct RowPart {
     // The pairs v, each element rounded once to the row's type, to the row's elements.
     __device__ __forceinline__ static void store(void* row, const uint64_t* v, const RowShape& s) {
         uint8_t* const p = static_cast<uint8_t*>(row);
-        if (kWide) {
+        if (kWide || kShifted) {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                if (!inside(8 * j, s)) continue;
                 float2 f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = unpack2(v[4 * j + i]);
+                if (kShifted && !whole(j, s)) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (!inside(8 * j + k, s)) continue;
+                        const float e = k & 1 ? f[k >> 1].y : f[k >> 1].x;
+                        reinterpret_cast<__nv_bfloat16*>(p)[column(8 * j + k, s)] = __float2bfloat16_rn(e);
+                    }
+                    continue;
+                }
+                if (!kShifted && !inside(8 * j, s)) continue;
                 if (kF32) {
                     float4* const d = reinterpret_cast<float4*>(p + 4 * static_cast<int64_t>(column(8 * j, s)));
                     d[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
@@ -161,17 +189,17 @@ struct RowPart {
 };
 
 // A thread's part of a vector of fp32 or bf16, as pairs in the places of Part, zero behind the row's end.
-template <bool kF32, bool kWide, int kGroups>
-__device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32, const RowShape& s, uint64_t* f) {
-    using Part = RowPart<kF32, kWide, kGroups>;
-    if (kWide) {
+template <bool kF32, NormAccess kAccess, int kGroups>
+__device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32, bool wide, const RowShape& s, uint64_t* f) {
+    using Part = RowPart<kF32, kAccess, kGroups>;
+    if (kAccess == kNormWide && wide) {
         if (f32) {
-            RowPart<true, true, kGroups> p;
+            RowPart<true, kNormWide, kGroups> p;
             p.load(static_cast<const float*>(v) + at, s);
 #pragma unroll
             for (int i = 0; i < Part::kPairs; ++i) f[i] = p.pair(i);
         } else {
-            RowPart<false, true, kGroups> p;
+            RowPart<false, kNormWide, kGroups> p;
             p.load(static_cast<const uint16_t*>(v) + at, s);
 #pragma unroll
             for (int i = 0; i < Part::kPairs; ++i) f[i] = p.pair(i);
@@ -187,8 +215,11 @@ __device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32,
     for (int i = 0; i < Part::kPairs; ++i) f[i] = pack2(make_float2(one(2 * i), one(2 * i + 1)));
 }
 
+// The columns that a row's threads have to cover: a shifted row's first group starts before it.
+inline int columns_of(const NormArgs& a) { return a.dim + (a.access == kNormShifted ? 7 : 0); }
+
 // Threads of a CTA that has a row to itself.
-inline int row_threads(int dim, int groups) { return ((dim + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
+inline int row_threads(int columns, int groups) { return ((columns + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
 
 // How a kernel takes its rows: one a warp, straight into registers; or one a CTA, through a
 // ring of rows in shared memory that bulk copies fill ahead of it.
@@ -205,7 +236,7 @@ struct RowRing {
 
 // How a row lies in its slot.  Bulk copies move whole 16 bytes: a row that does not start or end at a
 // multiple of 16 comes with what lies around it in its 16 bytes, which belongs to the rows beside it; the first and the
-// last row have no such neighbour, and are loaded directly (`edge`).
+// last row have no such neighbour, and the threads copy them (`edge`).
 template <bool kWide>
 __device__ __forceinline__ bool ring_edge(int64_t row, int64_t rows) {
     return !kWide && (row == 0 || row == rows - 1);
@@ -244,6 +275,28 @@ __device__ __forceinline__ void ring_init(RowRing& r, int stages) {
 
 __device__ __forceinline__ void ring_wait(RowRing& r, int slot, uint32_t phase, uint32_t* err) {
     mbar_wait(smem_addr(&r.full[slot]), phase, err, kErrNorm, &r.abort);
+}
+
+template <bool kF32>
+struct Element { using Type = uint16_t; };
+template <>
+struct Element<true> { using Type = uint32_t; };
+
+// An edge row into its slot; a barrier of the CTA is to follow.
+template <bool kF32>
+__device__ __forceinline__ void ring_fill(uint8_t* to, const uint8_t* row, int dim) {
+    using T = typename Element<kF32>::Type;
+    constexpr int kTogether = 16;   // loads under way
+    const T* const from = reinterpret_cast<const T*>(row);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < dim; i += kTogether * blockDim.x) {
+        T v[kTogether];
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) v[k] = from[min(i + k * static_cast<int>(blockDim.x), dim - 1)];
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k)
+            if (i + k * static_cast<int>(blockDim.x) < dim) reinterpret_cast<T*>(to)[i + k * blockDim.x] = v[k];
+    }
 }
 
 // Thread 0, before it ends: copies that a wait gave up on may still be on their way.

@@ -153,6 +153,36 @@ def test_vectors_of_samples(w_dtype, rows, dim, samples):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows, dim, samples", [(1, 1001, 1), (2, 333, 1), (3, 2501, 1), (7, 1003, 1), (8, 505, 1), (9, 4100, 1), (4200, 1003, 1), (4300, 1541, 2), (700, 8191, 7), (17, 250, 1),
+                                                (100, 8191, 1), (640, 2050, 2), (1300, 517, 5), (3000, 1005, 600), (2000, 70, 500)])
+def test_rows_that_start_anywhere(dtype, rows, dim, samples):
+    check(rows, dim, dtype, samples=None if samples == 1 else samples)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [260, 1001, 2300])
+@pytest.mark.parametrize("at_x, at_dy", [(1, 1), (3, 3), (1, 2), (0, 5), (8, 8)])
+def test_tensors_shifted_alike_and_not(dtype, dim, at_x, at_dy):
+    x, dy, w, b = make(40, dim, dtype, torch.float32, None, seed=8)
+
+    def moved(t, at):
+        store = torch.full((40 * (dim + 3) + at,), 7e4, dtype=dtype, device="cuda")
+        view = store[at:].view(40, dim + 3)[:, :dim]
+        view.copy_(t)
+        return view
+
+    layer = LayerNorm(dim, 40, dtype=dtype)
+    xv, dyv = moved(x, at_x), moved(dy, at_dy)
+    y = layer.forward(xv, w, b)
+    dx, dw, db = layer.backward(dyv, xv, w)
+    want = formulas(x, dy, w, b, 1e-5, False)
+    within(y, *want[0:2], dtype, "y")
+    within(dx, *want[2:4], dtype, "dx")
+    within(dw, *want[4:6], torch.float32, "dw")
+    within(db, *want[6:8], torch.float32, "db")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("dim", [100, 1536])
 def test_a_mean_far_above_the_deviation(dtype, dim):
     check(50, dim, dtype, mean=300.0, std=0.01 if dtype == torch.float32 else 1.0)
@@ -174,7 +204,8 @@ def test_views_inside_a_larger_tensor_and_unaligned_vectors():
         x = store[:, at:at + 256]
         w = torch.randn(257, device="cuda")[1:]
         layer, other = LayerNorm(256, 20), LayerNorm(256, 20)
-        assert torch.equal(layer.forward(x, w), other.forward(x.contiguous(), w.clone()))
+        # sums in another order, so values some 2^-20 apart before they are rounded: one step of bf16, 2^-7, at most
+        assert torch.allclose(layer.forward(x, w).float(), other.forward(x.contiguous(), w.clone()).float(), rtol=2.0 ** -7, atol=1e-5)
         dy = store[:, :256]
         for p, q in zip(layer.backward(dy, x, w)[:2], other.backward(dy.contiguous(), x.contiguous(), w.clone())[:2]):
             assert torch.allclose(p.float(), q.float(), rtol=2.0 ** -7, atol=1e-5)   # sums in another order: one rounding of bf16 apart

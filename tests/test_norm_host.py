@@ -62,14 +62,18 @@ def test_workspace_refuses_dims_out_of_range():
 
 
 def test_partial_rows_fit_the_workspace():
-    # the C entry's sharing out, restated: CTAs with partial rows, over samples and rows
+    # the C entry's sharing out, restated: CTAs with partial rows, over samples and rows, and over the rows from one to the next that
+    # starts as far behind a multiple of 16 bytes
     slots = abi.mxfp4_layer_norm_workspace_bytes(1) // 8
     for samples in list(range(1, 320)) + [600, 1000]:
         for each in list(range(1, 40)) + [303, 304, 305, 1000, 4097]:
             rows = samples * each
             chunk = max(-(-rows // 608), 4)
-            chunks = -(-each // chunk)
-            assert chunks == 1 or samples * chunks <= slots
+            for period in (1, 2, 4, 8):
+                chunks = period * -(-(-(-each // period)) // chunk)
+                if period > 1 and samples * chunks > slots:
+                    chunks = -(-each // chunk)
+                assert chunks == 1 or samples * chunks <= slots
 
 
 @pytest.fixture
