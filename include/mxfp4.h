@@ -633,7 +633,8 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
  * elements of every finite size; an infinite one gives norm inf and factor 0, a NaN makes both NaN.
  * The same gradients give the same bits.
  *   tensors    count of them (0 .. MXFP4_GRAD_MAX_TENSORS), n elements each (n == 0: skipped; at most
- *              2^40 in all), dense, aligned to their element; no two overlap
+ *              2^40 in all), dense, aligned to their element; with MXFP4_GRAD_SCALE
+ *              two that overlap are refused, else what they share counts twice
  *   max_norm   above 0; may be infinite
  *   workspace  mxfp4_grad_norm_workspace_bytes(count) bytes, 256-byte aligned, all zero before its
  *              first use (a call leaves its first 256 bytes zero); calls that share one are ordered

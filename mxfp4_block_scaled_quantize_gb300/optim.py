@@ -63,7 +63,7 @@ class GradNorm:
         return self._run(list(map(_address, grads)), _check_grads(grads, self._numel, self._gpu), max_norm, 0, stream)
 
     def clip_(self, grads, max_norm, stream=None):
-        """The same, and the gradients multiplied by the factor in place."""
+        """The same, and the gradients multiplied by the factor in place: no two share an element."""
         return self._run(list(map(_address, grads)), _check_grads(grads, self._numel, self._gpu), max_norm,
                          abi.MXFP4_GRAD_SCALE, stream)
 

@@ -49,6 +49,23 @@ def test_misaligned_addresses_are_refused(bad):
     assert call(**bad) == abi.MXFP4_ERR_MISALIGNED
 
 
+@pytest.mark.parametrize("table, apart", [
+    ([(0x1000, 8), (0x1010, 8)], True), ([(0x1010, 8), (0x1000, 8)], True), ([(0x1000, 8), (0x1000, 8)], False),
+    ([(0x1000, 9), (0x1010, 8)], False), ([(0x1010, 8), (0x1000, 9)], False), ([(0x2000, 8), (0x1000, 8), (0x1800, 8)], True),
+    ([(0x2000, 8), (0x1000, 8), (0x1800, 0x401)], False), ([(0x2000, 8), (0x1000, 0x1000), (0x1800, 4)], False),
+    ([(0x1000, 8), (0, 0), (0, 0), (0x1010, 8)], True), ([(0x1000, 8), (0x1004, 0), (0x1010, 8)], True)])
+def test_gradients_that_overlap_are_not_scaled(table, apart):
+    # the workspace's address is refused after everything else, so that none of the calls launches anything
+    arr = (ctypes.c_uint64 * (2 * len(table)))(*[v for pair in table for v in pair])
+    need = abi.mxfp4_grad_norm_workspace_bytes(len(table))
+
+    def status(flags):
+        return abi.load().mxfp4_grad_norm(len(table), ctypes.addressof(arr), flags, 1.0, 0x1000, 0x1010, need, None)
+
+    assert status(abi.MXFP4_GRAD_SCALE) == (abi.MXFP4_ERR_MISALIGNED if apart else abi.MXFP4_ERR_INVALID_ARG)
+    assert status(0) == abi.MXFP4_ERR_MISALIGNED
+
+
 def test_workspace_grows_with_the_launches():
     sizes = [abi.mxfp4_grad_norm_workspace_bytes(n) for n in (0, 1, 1279, 1280, 2560, abi.MXFP4_GRAD_MAX_TENSORS)]
     assert sizes == sorted(sizes) and sizes[0] > 256 and sizes[2] == sizes[1] and sizes[4] > sizes[3] > sizes[2]
