@@ -346,7 +346,7 @@ __device__ __forceinline__ void list_pairs(const ExpertsArgs& a, Head* head, uns
 #pragma unroll 1
     for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads) {
         const float w = __ldcg(a.weights + i);
-        const int e = __ldcg(a.ids + i);
+        const int e = min(static_cast<int>(__ldcg(a.ids + i)), a.experts - 1);   // a barrier that gave up may have left anything there
         weights[i] = w;
         ids[i] = static_cast<uint16_t>(e);
         if (w != 0.0f) atomicOr(&masks[e], 1ull << (i / a.top_k));   // not where it changes nothing
@@ -793,7 +793,7 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
         int x = at.acts + g * pitch + t * 16 + seg.slice * (kSlice * 2);
 #pragma unroll 1
         for (int i = seg.slice; i < seg.last; ++i) {
-            mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort);
+            if (!mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort)) stream.more = false;   // no copies over copies
             const int codes = st.codes + st.next * kSliceBytes, words = st.words + st.next * kWordBytes;
             if (wide) multiply<kMost, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
             else if (slim) multiply<1, false>(shared, codes, words, scales, x, pitch, low, acc);

@@ -8,7 +8,7 @@
 
 namespace mxfp4 {
 
-constexpr int kNormWarpRowDim = 512;     // rows of up to this many elements are one warp's, longer ones a CTA's
+constexpr int kNormWarpRowDim = 512;     // rows of up to this many elements are one warp's in either pass
 // Rows that a CTA has on their way to shared memory, at most.
 constexpr int kNormStagesForward = 3;
 constexpr int kNormStagesBackward = 4;

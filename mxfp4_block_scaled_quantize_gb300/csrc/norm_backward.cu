@@ -9,6 +9,11 @@
 // inputs give the same bits.  A sample that is one CTA's needs no second kernel.  Rows come as in the
 // forward pass, x and dy side by side in a slot of the ring.  Bound by the memory: x and dy in, dx
 // out; the partial rows are 4 / chunk_rows of x and dy in bf16.
+//
+// 16 elements a thread, for dw, db and the gain in registers leave room for no more at 512 threads an SM (8 a thread and 1024
+// threads: 16384 rows of 8192 in 156 us, 129 with 16; 24 warps at 85 registers each spill: 8192 of 4096 in 58 us, 39 with 16 warps).
+// Now 6.2 TB/s for 16384 rows of 8192, 5.2 for 8192 of 4096; of 39 us there the second kernel takes 4.  Rows of more than 8192
+// elements have 64 registers a thread, and spill: 4096 rows of 16384 take 187 us, 2.2 TB/s.
 #include <atomic>
 
 #include "norm_row.cuh"

@@ -9,7 +9,7 @@
 // squares are the warps' and n_w (d_w - D)^2.  So nothing is lost where |mu| is far above the deviation.  All of it in
 // fp32; y is rounded once.  Bound by the memory, and by instructions not far below it.
 //
-// A warp takes a row of up to 512 elements, a CTA a longer one.  CTAs stay for many rows, with the
+// A warp takes a short row, a CTA a longer one (launch() below says where).  CTAs stay for many rows, with the
 // vectors in registers.  A CTA's rows come through a ring in shared memory, which has three of them on
 // their way whatever the registers hold; a warp's are loaded into registers one row ahead.
 #include <atomic>

@@ -320,18 +320,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// A sum (two sums) over the row's threads, in all of them and in the same order in each.  A row of several warps, of
+// Two sums over the row's threads, in all of them and in the same order in each.  A row of several warps, of
 // kWarps at most, goes through `shared`, which two calls in a row do not share: one barrier a call.
-template <RowMode kMode, int kWarps>
-__device__ __forceinline__ float row_sum(float v, float* shared) {
-    v = lanes_sum<32>(v);
-    if (kMode == kWarpRow) return v;
-    if (lane_id() == 0) shared[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int i = static_cast<int>(lane_id()) & (kWarps - 1);
-    return lanes_sum<kWarps>(i < static_cast<int>(blockDim.x >> 5) ? shared[i] : 0.0f);
-}
-
 template <RowMode kMode, int kWarps>
 __device__ __forceinline__ float2 row_sum2(uint64_t v, uint64_t* shared) {
     v = lanes_sum2<32>(v);
