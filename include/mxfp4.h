@@ -512,8 +512,8 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const voi
  *   sizes      experts 1 .. MXFP4_MAX_GROUPS, top_k 1 .. min(experts, MXFP4_EXPERTS_MAX_TOP_K); dim and inner as far as the
  *              activations of 8 routed rows fit the shared memory: up to 7040 and 3456 whatever the rest
  *              (mxfp4_experts_workspace_bytes tells: it refuses what the call refuses)
- *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned; its first 256 bytes are zero before the first use
- *              (a call leaves them zero); calls that share one are ordered one after the other, as are replays of
+ *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned, all zero before its first use (a call leaves zero
+ *              what the next one needs so); calls that share one are ordered one after the other, as are replays of
  *              graphs that hold them
  * x, the weights and the sums are not rounded on the way: the products are those of the values that the blobs stand for, in
  * fp32, and the activations between the two keep 22 bits.  y is rounded once.  The same inputs give the same bits. */

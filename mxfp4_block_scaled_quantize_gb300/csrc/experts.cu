@@ -15,7 +15,7 @@
 // multiplied by its scale in fp32, as all sums are.  y is rounded once.
 //
 // Four phases, with the grid meeting in between (a cooperative launch, one CTA an SM; a barrier takes 1 to 2 us):
-//   1. CTA t: token t's choices, and its row of x in fp16.
+//   1. CTA t: token t's choices, and its row of x in fp16.  (Up to kFew tokens: every CTA, all of them, and no barrier.)
 //   2. The first product, with silu(g) u.   3. The second product.   4. The sums over the experts, in the tokens' order.
 // (As two kernels that each routed and staged for themselves, and with the sums left to whichever CTA came last for 32
 // columns: 137 us where one kernel then took 115, of which 60 passed before the first and after the last weights.)
@@ -26,16 +26,17 @@
 // 1 / 16 of all their slices of 128 elements, which are of two units at most: a unit's first warp adds what the others found.
 // (All units dealt out slice by slice to 16 warps, which met after each one, took 1.9 times the instructions; the rest in
 // rounds of 8, 4, 2 and 1 units 9 us more in some CTAs than in others, of 50.)  Each warp has several slices (2 KB of codes) on
-// their way to shared memory by copies of
-// its own, across the ends of its units and, to the second product's weights, across the barrier.
+// their way to shared memory by copies of its own, across the ends of its units and, to the second product's weights, across the barrier.
 //   The order of all additions is fixed by the call's routing.
 //   (The two fp16 of an activation between the products cost a second set of matrix instructions: 17 us of the 209 for 64 tokens
 // below.  Up to 4 rows have them side by side as 8 columns, which costs none: 8 tokens 59 us, 65 without that.)
 //
-// Measured (experts dim x inner; 1, 8 and 32 tokens of 8 of 64, 2048 x 1408; 64 of 6 of 64, 4096 x 2048): 28, 59, 85 and 205 us,
-// where the weights' bytes take 5.4, 28.5, 42.8 and 126.  One token: 3.3 us to the first barrier, 3 to the first weights asked
-// for, 7 for the first product, 5 for the second, 5 for the other two barriers and the sums; much of it is code that runs once
-// and comes from memory.  64 tokens: the first product at 20 bytes a clock and SM (of 23), the second at 16.
+// Both products go through the same code.  (Written out for each, with what a product multiplies as constants, it took as long.)
+//
+// Measured (experts dim x inner; 1, 8 and 32 tokens of 8 of 64, 2048 x 1408; 64 of 6 of 64, 4096 x 2048): 26, 59, 85 and 206 us,
+// where the weights' bytes take 5.4, 28.5, 42.8 and 126.  One token: 2 us for the choices, 1.5 for the lists, 1.7 until the first weights
+// are asked for, 6.2 for the first product, 4.8 for the second, 5 for the two barriers and the sums, and 4 before and after.
+// 64 tokens: the first product at 20 bytes a clock and SM (of 23), the second at 16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -56,6 +57,9 @@ constexpr int kSliceBytes = kUnitRows * kSlice / 2;      // codes
 constexpr int kWordBytes = 4 * kUnitRows;                // and a word of four scales for each row
 constexpr int kMaxStages = 4;
 constexpr int kMaxPass = 16;                             // routed rows of a pass
+// Up to kFew tokens, every CTA chooses for all of them and stages them by itself, and needs no barrier for it: one token 26 us, 28
+// with the barrier; 4 take 46 either way, and 8 a little more without it, for a warp then has a row to itself.
+constexpr int kFew = 4;
 constexpr int kSharedMost = 227 * 1024;
 // A unit of a pass of more than 8 rows takes 1.6 times as long as one of up to 8, and coming to another expert or pass as long as
 // kStagingSlices slices of a unit (32 tokens, 8 of 64: 88 us without counting that, 84.6 with 32 slices, 83.3 with 64, 82.2 with 96;
@@ -74,17 +78,19 @@ struct Row {           // of a pass
 // the activations, the units' sums, the warps' scales, their words and (at a multiple of 512 bytes) their codes.
 struct Head {
     Row rows[kMaxPass];
-    int32_t narrow;    // (expert, pass) pairs of up to 8 rows,
-    int32_t pairs;     // and all of them
+    int32_t range[4];  // the CTA's units of the first product: from, to; of the second
+    int32_t narrow;    // (expert, pass) pairs of up to 8 rows
     int32_t wide;      // the pass has more than 8 rows,
     int32_t slim;      // up to 4: the second product then has its activations' low parts beside the high ones, as columns 4 to 7
-    uint32_t top;      // largest magnitude of a row of x, as bits
     int32_t abort;     // a wait has run out
-    int32_t pad[2];
+    uint32_t tops[kFew];   // largest magnitudes of rows of x, as bits
     uint64_t full[kWarps][kMaxStages];
 };
 
 __host__ __device__ inline int align16(int n) { return (n + 15) & ~15; }
+
+// n / d for n d < 2^32, by = 2^32 / d rounded up, or 0 for d = 1.  (A division is 30 instructions, most of them waiting for one another.)
+__device__ __forceinline__ int divide(int n, uint32_t by) { return by == 0u ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), by)); }
 
 struct Layout {
     int masks, weights, backs, ids, list, list_size, acts, sums, scales, words, codes, total;
@@ -186,7 +192,7 @@ __device__ __forceinline__ float logit_of(const ExpertsArgs& a, int64_t t, int e
 // Phase 1 for one token, by one warp: its choices and their weights.  kPer: 32 kPer experts at most.  Order: value, then lowest
 // index; a NaN is above all values, as in a sort.
 template <int kPer>
-__device__ __forceinline__ void choose(const ExpertsArgs& a, int t) {
+__device__ __forceinline__ void choose(const ExpertsArgs& a, int t, float* weights, uint16_t* ids) {
     const int lane = static_cast<int>(lane_id());
     const float none = __int_as_float(0xFF800000);
     float v[kPer];
@@ -240,10 +246,14 @@ __device__ __forceinline__ void choose(const ExpertsArgs& a, int t) {
     }
     sum = sum_all(sum);
     if (lane < a.top_k) {
-        a.weights[t * a.top_k + lane] = sum == 0.0f ? 0.0f : p / sum;   // 0: every logit is -inf
-        a.ids[t * a.top_k + lane] = static_cast<uint16_t>(id);
-        a.tops[t * a.top_k + lane] = 0u;
+        weights[t * a.top_k + lane] = sum == 0.0f ? 0.0f : p / sum;   // 0: every logit is -inf
+        ids[t * a.top_k + lane] = static_cast<uint16_t>(id);
     }
+}
+__device__ __forceinline__ void choose(const ExpertsArgs& a, int t, float* weights, uint16_t* ids) {
+    if (a.experts <= 64) choose<2>(a, t, weights, ids);
+    else if (a.experts <= 256) choose<8>(a, t, weights, ids);
+    else choose<32>(a, t, weights, ids);
 }
 
 // 2^k that brings `top` to 2^14 .. 2^15 (k <= 126), and 2^-k.
@@ -280,29 +290,48 @@ __device__ __forceinline__ void x8(const ExpertsArgs& a, const uint16_t* row, in
     for (int i = 0; i < 8; ++i) f[i] = c + i < a.dim ? __uint_as_float(static_cast<uint32_t>(row[c + i]) << 16) : 0.0f;
 }
 
-// Phase 1 for one token, by the warps from 1 on: its row of x in fp16, zeros behind its end.
-__device__ __forceinline__ void lower_row(const ExpertsArgs& a, Head* head, int t) {
-    constexpr int kOthers = kThreads - 32;
+// Token t's row of x in fp16, zeros behind its end, by `threads` threads (whole warps) of which this is number `first`; to: its
+// place, back: that of what undoes the row's power of two.  `barrier` is theirs, or also others' who come to it as often.
+__device__ __forceinline__ void lower_row(const ExpertsArgs& a, int t, int first, int threads, uint32_t* head_top, uint32_t barrier_threads, uint4* to,
+                                          float* back_to) {
     const uint16_t* const row = a.x + t * a.ldx;
     const bool wide = a.dim % 8 == 0 && (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
-    const int groups = (Layout::pitch(a.dim) - 64) / 16, first = static_cast<int>(threadIdx.x) - 32;
-    float f[8], top = 0.0f;
+    const int groups = (Layout::pitch(a.dim) - 64) / 16;
+    float top = 0.0f;
 #pragma unroll 1
-    for (int i = first; i < groups; i += kOthers) {
-        x8(a, row, 8 * i, wide, f);
+    for (int i = first; wide && i < groups; i += 8 * threads) {
+        uint4 u[8];   // on their way together
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = 8 * (i + j * threads);
+            u[j] = c < a.dim ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(finite_or_zero(__uint_as_float(w[k] << 16)), finite_or_zero(__uint_as_float(w[k] & 0xFFFF0000u))));
+#pragma unroll
+            for (int k = 0; k < 7; ++k) u[k] = u[k + 1];
+        }
+    }
+#pragma unroll 1
+    for (int i = first; !wide && i < groups; i += threads) {
+        float f[8];
+        x8(a, row, 8 * i, false, f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_or_zero(f[j]));
     }
     const uint32_t most = max_all(__float_as_uint(top));
-    if (lane_id() == 0) atomicMax(&head->top, most);   // the order does not matter
-    named_barrier(1, kOthers);
+    if (lane_id() == 0) atomicMax(head_top, most);   // the order does not matter
+    named_barrier(1, barrier_threads);
     float back;
-    const float up = lift(__uint_as_float(head->top), &back);
-    if (first == 0) a.backs[t] = back;
-    uint4* const to = reinterpret_cast<uint4*>(a.lowered + static_cast<int64_t>(t) * 8 * groups);
+    const float up = lift(__uint_as_float(*head_top), &back);
+    if (first == 0) *back_to = back;
 #pragma unroll 1
-    for (int i = first; i < groups; i += kOthers) {
-        if (i != first || groups > kOthers) x8(a, row, 8 * i, wide, f);   // else they are still there
+    for (int i = first; i < groups; i += threads) {
+        float f[8];
+        x8(a, row, 8 * i, wide, f);
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = half2_of(f[2 * j] * up, f[2 * j + 1] * up);
@@ -315,8 +344,7 @@ __device__ __forceinline__ void lower_row(const ExpertsArgs& a, Head* head, int 
 __device__ __forceinline__ void meet(const ExpertsArgs& a, int which) {
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(&a.sync->arrived[which], 1u);
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(&a.sync->arrived[which]) : "memory");   // the CTA's writes before
         const uint64_t t0 = globaltimer();
         for (;;) {
             uint32_t n = 0;
@@ -331,27 +359,48 @@ __device__ __forceinline__ void meet(const ExpertsArgs& a, int which) {
                 break;
             }
         }
-        __threadfence();
     }
     __syncthreads();
 }
 
+// The unit at which CTA `cta` starts, so that all have the same to do.
+__device__ __forceinline__ int range_start(const ExpertsSide& side, uint32_t narrow, uint32_t wide, uint32_t cta) {
+    const uint32_t tiles = static_cast<uint32_t>(side.tiles), slices = static_cast<uint32_t>(side.slices);
+    // of a unit, of a pair; all of it is below 2^30: at most 1200 pairs of 300 units of 74 slices
+    const uint32_t unit_n = kNarrowCost * slices, unit_w = kWideCost * slices;
+    const uint32_t staging = kNarrowCost * kStagingSlices;
+    const uint32_t pair_n = tiles * unit_n + staging, pair_w = tiles * unit_w + staging;
+    const uint32_t all = narrow * pair_n + wide * pair_w, share = all / gridDim.x;
+    uint32_t at = share * cta + (all - share * gridDim.x) * cta / gridDim.x, first = 0, pair = pair_n, unit = unit_n;
+    if (at >= narrow * pair_n) {
+        at -= narrow * pair_n;
+        first = narrow;
+        pair = pair_w;
+        unit = unit_w;
+    }
+    const uint32_t p = at / pair, in = at - p * pair;
+    return static_cast<int>((first + p) * tiles + (in <= staging ? 0 : (in - staging) / unit));
+}
+
 // Each expert's tokens, and the list of (expert, pass) pairs that have any: those of up to 8 rows from its front on, the
-// others from its back on.
+// others from its back on.  The masks are zero before.
 __device__ __forceinline__ void list_pairs(const ExpertsArgs& a, Head* head, unsigned long long* masks, float* weights, uint16_t* ids, uint32_t* list,
                                            int list_size, float* backs) {
-#pragma unroll 1
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) masks[e] = 0ull;
-    __syncthreads();
+    const bool here = a.tokens <= kFew;   // this CTA's own choices are there already
 #pragma unroll 1
     for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads) {
-        const float w = __ldcg(a.weights + i);
-        const int e = min(static_cast<int>(__ldcg(a.ids + i)), a.experts - 1);   // a barrier that gave up may have left anything there
-        weights[i] = w;
-        ids[i] = static_cast<uint16_t>(e);
+        float w;
+        int e;
+        if (here) {
+            w = weights[i];
+            e = ids[i];
+        } else {
+            weights[i] = w = __ldcg(a.weights + i);
+            ids[i] = static_cast<uint16_t>(e = min(static_cast<int>(__ldcg(a.ids + i)), a.experts - 1));   // a barrier that gave up may have left anything there
+        }
         if (w != 0.0f) atomicOr(&masks[e], 1ull << (i / a.top_k));   // not where it changes nothing
     }
-    if (threadIdx.x < a.tokens) backs[threadIdx.x] = __ldcg(a.backs + threadIdx.x);
+    if (!here && threadIdx.x < a.tokens) backs[threadIdx.x] = __ldcg(a.backs + threadIdx.x);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = static_cast<int>(lane_id());
@@ -378,10 +427,9 @@ __device__ __forceinline__ void list_pairs(const ExpertsArgs& a, Head* head, uns
             }
             before += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
-        if (lane == 0) {
-            head->narrow = before & 0xFFFF;
-            head->pairs = (before & 0xFFFF) + (before >> 16);
-        }
+        const uint32_t narrow = static_cast<uint32_t>(before & 0xFFFF), wide = static_cast<uint32_t>(before >> 16);
+        if (lane == 0) head->narrow = static_cast<int32_t>(narrow);
+        if (lane < 4) head->range[lane] = range_start(a.side[lane >> 1], narrow, wide, blockIdx.x + (lane & 1));
     }
     __syncthreads();
 }
@@ -393,45 +441,12 @@ struct Pairs {
     __device__ __forceinline__ uint32_t operator[](int p) const { return list[p < narrow ? p : size - 1 - (p - narrow)]; }
 };
 
-// What the two products multiply: `rows` rows of k elements for each expert, `tiles` units.
-struct Up {
-    static constexpr bool kPairs = false;
-    static __device__ __forceinline__ const uint8_t* scales(const ExpertsArgs& a) { return a.up_s; }
-    static __device__ __forceinline__ int rows(const ExpertsArgs& a) { return 2 * a.inner; }
-    static __device__ __forceinline__ int k(const ExpertsArgs& a) { return a.dim; }
-    static __device__ __forceinline__ int tiles(const ExpertsArgs& a) { return (a.inner + 15) / 16; }
-    // The weights' row for row lr of tile `tile`; -1: none.
-    static __device__ __forceinline__ int row(const ExpertsArgs& a, int tile, int lr) {
-        const int r = 16 * tile + (lr & 15);
-        return r < a.inner ? (lr < 16 ? r : a.inner + r) : -1;
-    }
-    // The codes of a slice of a unit: 16 rows of g and 16 of u; what lies behind either's end is of no use, and does no harm.
-    static __device__ __forceinline__ void load(const ExpertsArgs& a, uint32_t to, int x, int first, int tile, uint32_t bar) {
-        tma_load_2d(to, &a.up_map, x, first + 16 * tile, bar);
-        tma_load_2d(to + kSliceBytes / 2, &a.up_map, x, first + a.inner + 16 * tile, bar);
-    }
-};
-struct Down {
-    static constexpr bool kPairs = true;
-    static __device__ __forceinline__ const uint8_t* scales(const ExpertsArgs& a) { return a.down_s; }
-    static __device__ __forceinline__ int rows(const ExpertsArgs& a) { return a.dim; }
-    static __device__ __forceinline__ int k(const ExpertsArgs& a) { return a.inner; }
-    static __device__ __forceinline__ int tiles(const ExpertsArgs& a) { return (a.dim + 31) / 32; }
-    static __device__ __forceinline__ int row(const ExpertsArgs& a, int tile, int lr) {
-        const int r = 32 * tile + lr;
-        return r < a.dim ? r : -1;
-    }
-    static __device__ __forceinline__ void load(const ExpertsArgs& a, uint32_t to, int x, int first, int tile, uint32_t bar) {
-        tma_load_2d(to, &a.down_map, x, first + 32 * tile, bar);
-    }
-};
-
 // A warp's way through the CTA's units, one segment (slices of one unit) after the other.  Rounds of 16 units of one expert and
 // pass have one for each warp, a whole unit.  A round of the n < 16 that are left has two: the warp's share of the n units'
 // slices, first what it has of a unit that another warp begins, then what it begins itself; either may be empty.
 struct Segments {
     enum Kind { kWhole, kGoOn, kBegin };
-    int end, tiles, slices, warp;
+    int end, warp;
     int base, next;        // the round's first unit, and the next round's
     int pair;              // its place in the list of (expert, pass)
     int left;              // its units
@@ -440,15 +455,15 @@ struct Segments {
     int slice, last;       // and its slices: from, to
 
     // Before the first segment.
-    __device__ __forceinline__ Segments(int from, int to, int tiles_, int slices_)
-        : end(to), tiles(tiles_), slices(slices_), warp(threadIdx.x >> 5), base(from), next(from), pair(-1), left(0), kind(kWhole), unit(0),
-          slice(0), last(0) {}
+    __device__ __forceinline__ Segments(int from, int to)
+        : end(to), warp(threadIdx.x >> 5), base(from), next(from), pair(-1), left(0), kind(kWhole), unit(0), slice(0), last(0) {}
     // Where the share of warp w starts among the slices of the round's units.
-    __device__ __forceinline__ int share(int w) const { return left * slices * w / kWarps; }
-    __device__ __forceinline__ bool advance() {
+    __device__ __forceinline__ int share(const ExpertsSide& side, int w) const { return left * side.slices * w / kWarps; }
+    __device__ __forceinline__ bool advance(const ExpertsSide& side) {
+        const int tiles = side.tiles, slices = side.slices;
         if (kind == kGoOn) {   // the same round
             kind = kBegin;
-            const int from = share(warp), to = share(warp + 1), u = (from + slices - 1) / slices;
+            const int from = share(side, warp), to = share(side, warp + 1), u = divide(from + slices - 1, side.by_slices);
             unit = base + u;
             slice = 0;
             last = max(to - u * slices, 0);
@@ -456,7 +471,7 @@ struct Segments {
         }
         if (next >= end) return false;
         base = next;
-        pair = base / tiles;
+        pair = divide(base, side.by_tiles);
         left = min(end, (pair + 1) * tiles) - base;
         if (left >= kWarps) {
             kind = kWhole;
@@ -466,7 +481,7 @@ struct Segments {
             last = slices;
         } else {
             kind = kGoOn;
-            const int from = share(warp), to = share(warp + 1), u = from / slices;
+            const int from = share(side, warp), to = share(side, warp + 1), u = divide(from, side.by_slices);
             unit = base + u;
             slice = from - u * slices;
             last = slice == 0 ? 0 : min(slices, slice + to - from);
@@ -480,36 +495,37 @@ struct Segments {
 // 64-byte swizzle turns a row's four 16-byte pieces by (row / 2) % 4, the scales as a word for each lane's row; a barrier for each
 // stage counts both.  (All of it by 16-byte asynchronous copies from the lanes: 15 clocks of the load pipe for 512 bytes, 2.6 us
 // for the first four slices of 16 warps, and 101 us for 32 tokens where this took 93.)
-template <typename Product, int kStages>
+template <int kStages>
 struct Stream {
-    const ExpertsArgs& a;
+    const ExpertsSide& side;
     Pairs list;
     uint32_t codes, words, full;   // the warp's stages and their barriers
     int stage;                     // the next one to be filled
     Segments r;
     bool more;
-    int first, tile;               // of the unit: its expert's first row, and its place there
+    int first;                     // of the unit: its first row of all experts'
     const uint8_t* s;              // this lane's row's scales,
     int bytes;                     // to copy of them: none where there is no row
 
-    __device__ __forceinline__ Stream(const ExpertsArgs& args, const Pairs& l, uint32_t c, uint32_t w, uint32_t f, int next, const Segments& segments)
-        : a(args), list(l), codes(c), words(w), full(f), stage(next), r(segments) {
+    __device__ __forceinline__ Stream(const ExpertsSide& sides, const Pairs& l, uint32_t c, uint32_t w, uint32_t f, int next, const Segments& segments)
+        : side(sides), list(l), codes(c), words(w), full(f), stage(next), r(segments) {
         advance();
     }
     // To the next segment with slices.
     __device__ __forceinline__ void advance() {
-        do more = r.advance();
+        do more = r.advance(side);
         while (more && r.slice >= r.last);
         if (!more) return;
         const int e = static_cast<int>(list[r.pair] & 0xFFFFu);
-        tile = r.unit - r.pair * r.tiles;
-        first = e * Product::rows(a);
-        const int row = Product::row(a, tile, static_cast<int>(lane_id()));
-        bytes = row < 0 ? 0 : 4;
-        s = Product::scales(a);
-        if (row >= 0) {
-            const int64_t group = static_cast<int64_t>(e) * ((Product::rows(a) + 127) / 128) + row / 128;
-            s += (group * r.slices + r.slice) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
+        const int tile = r.unit - r.pair * side.tiles;
+        first = e * side.rows + side.step * tile;
+        const int lane = static_cast<int>(lane_id()), row = side.step * tile + (lane & 15) + (lane < 16 ? 0 : side.apart);
+        const bool there = row < (lane < 16 ? side.half : side.rows);
+        bytes = there ? 4 : 0;
+        s = side.scales;
+        if (there) {
+            const int64_t group = static_cast<int64_t>(e) * ((side.rows + 127) / 128) + row / 128;
+            s += (group * side.slices + r.slice) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
         }
     }
     // Asks for the next slice, if there is one.
@@ -521,7 +537,10 @@ struct Stream {
         s += 512;
         if (lane_id() == 0) {
             mbar_arrive_expect_tx(bar, kSliceBytes);
-            Product::load(a, codes + stage * kSliceBytes, r.slice * (kSlice / 2), first, tile, bar);
+            // what lies behind the end of either half is of no use, and does no harm
+            const uint32_t to = codes + stage * kSliceBytes;
+            tma_load_2d(to, &side.map, r.slice * (kSlice / 2), first, bar);
+            tma_load_2d(to + kSliceBytes / 2, &side.map, r.slice * (kSlice / 2), first + side.apart, bar);
         }
         if (++stage == kStages) stage = 0;
         if (++r.slice == r.last) advance();
@@ -587,26 +606,27 @@ __device__ __forceinline__ void multiply(uint8_t* shared, int stage_codes, int s
 }
 
 // The rows of a pass, and their activations: x's lowered rows as they are, the rows of h as two fp16.
-template <typename Product>
-__device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uint8_t* acts, const unsigned long long* masks,
+__device__ __forceinline__ void stage_rows(const ExpertsArgs& a, const ExpertsSide& side, Head* head, uint8_t* acts, const unsigned long long* masks,
                                            const float* weights, const float* backs, const uint16_t* ids, uint32_t pair) {
     const int e = static_cast<int>(pair & 0xFFFFu), skip = static_cast<int>(pair >> 16) * a.passes_rows;
-    const int pitch = Layout::pitch(Product::k(a)), groups = (pitch - 64) / 16;
+    const int pitch = side.pitch, groups = side.groups;
     const unsigned long long mask = masks[e];
     const int rows = min(a.passes_rows, __popcll(mask) - skip);
+    const bool here = !side.down && a.tokens <= kFew;
     __syncthreads();   // the rows before are done with
     if (threadIdx.x < kMaxPass) {
         Row row{-1, 0.0f, 0.0f, 0u};
-        if (static_cast<int>(threadIdx.x) < rows) {
+        // a few tokens are their own columns of the first product, whatever they chose
+        if (here ? (mask >> threadIdx.x & 1) != 0 : static_cast<int>(threadIdx.x) < rows) {
             unsigned long long m = mask;
 #pragma unroll 1
-            for (int i = skip + static_cast<int>(threadIdx.x); i > 0; --i) m &= m - 1;
-            const int token = __ffsll(static_cast<long long>(m)) - 1;
+            for (int i = here ? 0 : skip + static_cast<int>(threadIdx.x); i > 0; --i) m &= m - 1;
+            const int token = here ? static_cast<int>(threadIdx.x) : __ffsll(static_cast<long long>(m)) - 1;
 #pragma unroll 1
             for (int j = 0; j < a.top_k; ++j)   // an expert is among a token's choices once
                 if (ids[token * a.top_k + j] == e) row.slot = token * a.top_k + j;
             row.weight = weights[row.slot];
-            row.from = static_cast<uint32_t>(Product::kPairs ? row.slot : token);
+            row.from = static_cast<uint32_t>(side.down ? row.slot : token);
             row.back = backs[row.from];
         }
         head->rows[threadIdx.x] = row;
@@ -616,10 +636,11 @@ __device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uin
         }
     }
     __syncthreads();
-    if (!Product::kPairs) {
+    if (here) return;   // the activations are there
+    if (!side.down) {
 #pragma unroll 1
         for (int i = threadIdx.x; i < rows * groups; i += kThreads) {
-            const int n = i / groups, c = i - n * groups;
+            const int n = divide(i, side.by_groups), c = i - n * groups;
             copy16(smem_addr(acts + n * pitch + 16 * c), a.lowered + (static_cast<int64_t>(head->rows[n].from) * groups + c) * 8, 16);
         }
         copies_commit();
@@ -628,7 +649,7 @@ __device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uin
         const bool wide = a.inner % 8 == 0;
 #pragma unroll 2
         for (int i = threadIdx.x; i < rows * groups; i += kThreads) {
-            const int n = i / groups, c = 8 * (i - n * groups);
+            const int n = divide(i, side.by_groups), c = 8 * (i - n * groups);
             const float* const p = a.h + static_cast<int64_t>(head->rows[n].from) * a.inner + c;
             float f[8];
             if (wide) {
@@ -662,7 +683,7 @@ __device__ __forceinline__ void stage_rows(const ExpertsArgs& a, Head* head, uin
 // What becomes of a unit's sums, in the registers of one warp: element (row 16 m + 8 h + g, column 8 n + 2 t + c) of the
 // unit in acc[m][n][2 h + c].
 template <int kMost>
-__device__ __forceinline__ void finish(Up, const ExpertsArgs& a, const Head* head, int tile, int cols, const float (*acc)[kMost][4]) {
+__device__ __forceinline__ void finish_up(const ExpertsArgs& a, const Head* head, int tile, int cols, const float (*acc)[kMost][4]) {
     const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
 #pragma unroll
     for (int n = 0; n < kMost; ++n) {
@@ -690,7 +711,7 @@ __device__ __forceinline__ void finish(Up, const ExpertsArgs& a, const Head* hea
 }
 
 template <int kMost>
-__device__ __forceinline__ void finish(Down, const ExpertsArgs& a, const Head* head, int tile, int cols, const float (*acc)[kMost][4]) {
+__device__ __forceinline__ void finish_down(const ExpertsArgs& a, const Head* head, int tile, int cols, const float (*acc)[kMost][4]) {
     const int g = static_cast<int>(lane_id()) >> 2, t = static_cast<int>(lane_id()) & 3;
 #pragma unroll
     for (int n = 0; n < kMost; ++n) {
@@ -701,8 +722,8 @@ __device__ __forceinline__ void finish(Down, const ExpertsArgs& a, const Head* h
             if (row.slot < 0) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = Down::row(a, tile, 8 * i + g);
-                if (r >= 0) a.part[static_cast<int64_t>(row.slot) * a.dim + r] = acc[i >> 1][n][2 * (i & 1) + c] * row.back * row.weight;
+                const int r = 32 * tile + 8 * i + g;
+                if (r < a.dim) a.part[static_cast<int64_t>(row.slot) * a.dim + r] = acc[i >> 1][n][2 * (i & 1) + c] * row.back * row.weight;
             }
         }
     }
@@ -730,30 +751,6 @@ __device__ __forceinline__ void join(const ExpertsArgs& a, const float* weights)
     }
 }
 
-// The unit at which CTA `cta` starts, so that all have the same to do.
-__device__ __forceinline__ int range_start(const Head* head, uint32_t tiles, uint32_t slices, uint32_t cta) {
-    const uint32_t narrow = static_cast<uint32_t>(head->narrow), wide = static_cast<uint32_t>(head->pairs) - narrow;
-    // of a unit, of a pair; all of it is below 2^30: at most 1200 pairs of 300 units of 74 slices
-    const uint32_t unit_n = kNarrowCost * slices, unit_w = kWideCost * slices, staging = kNarrowCost * kStagingSlices;
-    const uint32_t pair_n = tiles * unit_n + staging, pair_w = tiles * unit_w + staging;
-    const uint32_t all = narrow * pair_n + wide * pair_w, share = all / gridDim.x;
-    uint32_t at = share * cta + (all - share * gridDim.x) * cta / gridDim.x, first = 0, pair = pair_n, unit = unit_n;
-    if (at >= narrow * pair_n) {
-        at -= narrow * pair_n;
-        first = narrow;
-        pair = pair_w;
-        unit = unit_w;
-    }
-    const uint32_t p = at / pair, in = at - p * pair;
-    return static_cast<int>((first + p) * tiles + (in <= staging ? 0 : (in - staging) / unit));
-}
-
-template <typename Product>
-__device__ __forceinline__ Segments range_of(const ExpertsArgs& a, const Head* head) {
-    const int tiles = Product::tiles(a), slices = (Product::k(a) + kSlice - 1) / kSlice;
-    return Segments(range_start(head, tiles, slices, blockIdx.x), range_start(head, tiles, slices, blockIdx.x + 1), tiles, slices);
-}
-
 // A warp's stages.
 struct Stages {
     int codes, words;     // their places in shared memory
@@ -763,26 +760,25 @@ struct Stages {
 };
 
 // A product over the CTA's range.
-template <typename Product, int kStages, int kMost>
-__device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, uint8_t* shared, Stream<Product, kStages>& stream, const Pairs& pairs,
-                                        Stages& st) {
+template <int kStages, int kMost>
+__device__ __forceinline__ void product(const ExpertsArgs& a, const ExpertsSide& side, const Layout& at, uint8_t* shared, Segments seg,
+                                        Stream<kStages>& stream, const Pairs& pairs, Stages& st) {
     Head* const head = reinterpret_cast<Head*>(shared);
     const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
     const int scales = at.scales + warp * kUnitRows * 16;
-    const int pitch = Layout::pitch(Product::k(a)), low = a.passes_rows * pitch;
+    const int pitch = side.pitch, low = a.passes_rows * pitch;
     float* const sums = reinterpret_cast<float*>(shared + at.sums) + lane;   // 32 lanes' values side by side, warp by warp
     constexpr int kValues = 8 * kMost;
     int pair = -1;
-    Segments seg = range_of<Product>(a, head);
 #pragma unroll 1
-    while (seg.advance()) {
+    while (seg.advance(side)) {
         if (seg.pair != pair) {
             pair = seg.pair;
-            stage_rows<Product>(a, head, shared + at.acts, reinterpret_cast<const unsigned long long*>(shared + at.masks),
+            stage_rows(a, side, head, shared + at.acts, reinterpret_cast<const unsigned long long*>(shared + at.masks),
                                 reinterpret_cast<const float*>(shared + at.weights), reinterpret_cast<const float*>(shared + at.backs),
                                 reinterpret_cast<const uint16_t*>(shared + at.ids), pairs[pair]);
         }
-        const bool wide = kMost > 1 && head->wide != 0, slim = Product::kPairs && head->slim != 0;
+        const bool down = side.down != 0, wide = kMost > 1 && head->wide != 0, slim = down && head->slim != 0;
         float acc[2][kMost][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -795,9 +791,14 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
         for (int i = seg.slice; i < seg.last; ++i) {
             if (!mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort)) stream.more = false;   // no copies over copies
             const int codes = st.codes + st.next * kSliceBytes, words = st.words + st.next * kWordBytes;
-            if (wide) multiply<kMost, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
-            else if (slim) multiply<1, false>(shared, codes, words, scales, x, pitch, low, acc);
-            else multiply<1, Product::kPairs>(shared, codes, words, scales, x, pitch, low, acc);
+            if (kMost > 1 && wide) {
+                if (down) multiply<kMost, true>(shared, codes, words, scales, x, pitch, low, acc);
+                else multiply<kMost, false>(shared, codes, words, scales, x, pitch, low, acc);
+            } else if (down && !slim) {
+                multiply<1, true>(shared, codes, words, scales, x, pitch, low, acc);
+            } else {
+                multiply<1, false>(shared, codes, words, scales, x, pitch, low, acc);
+            }
             __syncwarp();
             stream.ask();
             x += kSlice * 2;
@@ -820,11 +821,11 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
         }
         if (seg.kind == Segments::kBegin) {
             __syncthreads();   // the next write to the sums is behind a barrier of stage_rows or of the grid
-            const int behind = (seg.unit - seg.base + 1) * seg.slices;
+            const int behind = (seg.unit - seg.base + 1) * side.slices;
             if (seg.last == 0) continue;
 #pragma unroll 1
-            for (int w = warp + 1; w < kWarps && seg.share(w) < behind; ++w) {
-                if (seg.share(w) == seg.share(w + 1)) continue;
+            for (int w = warp + 1; w < kWarps && seg.share(side, w) < behind; ++w) {
+                if (seg.share(side, w) == seg.share(side, w + 1)) continue;
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -839,7 +840,9 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const Layout& at, 
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[m][0][i], 2);   // columns 4 away
-        finish<kMost>(Product(), a, head, seg.unit - seg.pair * seg.tiles, cols, acc);
+        const int tile = seg.unit - seg.pair * side.tiles;
+        if (down) finish_down<kMost>(a, head, tile, cols, acc);
+        else finish_up<kMost>(a, head, tile, cols, acc);
     }
 }
 
@@ -850,48 +853,65 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const Layout at(a.experts, a.tokens, a.top_k, a.dim, a.inner, a.passes_rows, kStages);
     Head* const head = reinterpret_cast<Head*>(shared);
     float* const weights = reinterpret_cast<float*>(shared + at.weights);
+    float* const backs = reinterpret_cast<float*>(shared + at.backs);
+    uint16_t* const ids = reinterpret_cast<uint16_t*>(shared + at.ids);
+    unsigned long long* const masks = reinterpret_cast<unsigned long long*>(shared + at.masks);
     uint32_t* const list = reinterpret_cast<uint32_t*>(shared + at.list);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         head->abort = 0;
-        prefetch_tensormap(&a.up_map);
-        prefetch_tensormap(&a.down_map);
+        prefetch_tensormap(&a.side[0].map);
+        prefetch_tensormap(&a.side[1].map);
     }
     if (threadIdx.x < kWarps * kStages)   // 32 lanes' words, and the codes
         mbar_init(smem_addr(&head->full[threadIdx.x / kStages][threadIdx.x % kStages]), 33);
     fence_barrier_init();
 
 #pragma unroll 1
-    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        if (threadIdx.x == 0) head->top = 0u;
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) masks[e] = 0ull;
+    if (threadIdx.x < kFew) head->tops[threadIdx.x] = 0u;
+    __syncthreads();
+    if (a.tokens <= kFew) {
+        const int each = (kWarps - a.tokens) / a.tokens, mine = warp - a.tokens;   // warps of a row
+        if (mine < 0) {
+            choose(a, warp, weights, ids);
+        } else if (mine < each * a.tokens) {
+            const int t = mine / each;
+            lower_row(a, t, 32 * (mine - t * each) + static_cast<int>(lane_id()), 32 * each, &head->tops[t], 32 * each * a.tokens,
+                      reinterpret_cast<uint4*>(shared + at.acts + t * Layout::pitch(a.dim)), backs + t);
+        }
         __syncthreads();
-        if (warp > 0) lower_row(a, head, t);
-        else if (a.experts <= 64) choose<2>(a, t);
-        else if (a.experts <= 256) choose<8>(a, t);
-        else choose<32>(a, t);
-        __syncthreads();
+    } else {
+#pragma unroll 1
+        for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+            if (warp > 0)
+                lower_row(a, t, static_cast<int>(threadIdx.x) - 32, kThreads - 32, &head->tops[0], kThreads - 32,
+                          reinterpret_cast<uint4*>(a.lowered + static_cast<int64_t>(t) * ((Layout::pitch(a.dim) - 64) / 2)), a.backs + t);
+            else choose(a, t, a.weights, a.ids);
+            __syncthreads();
+            if (threadIdx.x == 0) head->tops[0] = 0u;   // the next one's
+            __syncthreads();
+        }
+        meet(a, 0);
     }
-    meet(a, 0);
-    list_pairs(a, head, reinterpret_cast<unsigned long long*>(shared + at.masks), weights, reinterpret_cast<uint16_t*>(shared + at.ids), list,
-               at.list_size, reinterpret_cast<float*>(shared + at.backs));
+    list_pairs(a, head, masks, weights, ids, list, at.list_size, backs);
     const Pairs pairs{list, at.list_size, head->narrow};
     Stages st{at.codes + warp * kStages * kSliceBytes, at.words + warp * kStages * kWordBytes, smem_addr(head->full[warp]), 0, 0u};
     const uint32_t codes = smem_addr(shared + st.codes), words = smem_addr(shared + st.words);
-    {
-        Stream<Up, kStages> stream(a, pairs, codes, words, st.full, st.next, range_of<Up>(a, head));
+#pragma unroll 1
+    for (int p = 0; p < 2; ++p) {
+        const ExpertsSide& side = a.side[p];
+        const Segments seg(head->range[2 * p], head->range[2 * p + 1]);
+        Stream<kStages> stream(side, pairs, codes, words, st.full, st.next, seg);
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) stream.ask();
-        product<Up, kStages, kMost>(a, at, shared, stream, pairs, st);
-    }
-    {
-        Stream<Down, kStages> stream(a, pairs, codes, words, st.full, st.next, range_of<Down>(a, head));
+        if (p != 0) {
+            meet(a, 1);
 #pragma unroll 1
-        for (int i = 0; i < kStages; ++i) stream.ask();
-        meet(a, 1);
-#pragma unroll 1
-        for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads)   // a barrier of stage_rows is ahead of their use
-            lift(__uint_as_float(__ldcg(a.tops + i)), reinterpret_cast<float*>(shared + at.backs) + i);
-        product<Down, kStages, kMost>(a, at, shared, stream, pairs, st);
+            for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads)   // a barrier of stage_rows is ahead of their use
+                lift(__uint_as_float(__ldcg(a.tops + i)), backs + i);
+        }
+        product<kStages, kMost>(a, side, at, shared, seg, stream, pairs, st);
     }
     if (*static_cast<volatile int*>(&head->abort) != 0 && lane_id() == 0)   // copies that a wait gave up on may be on their way
         for (int i = 0; i < kStages; ++i) {
@@ -899,6 +919,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             if (++st.next == kStages) st.next = 0, st.phase ^= 1u;
         }
     meet(a, 2);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads) a.tops[i] = 0u;   // for the next call
     join(a, weights);
     if (threadIdx.x == 0 && atomicAdd(&a.sync->left, 1u) == gridDim.x - 1u) {   // nobody looks at them any more
         a.sync->arrived[0] = a.sync->arrived[1] = a.sync->arrived[2] = 0u;
@@ -921,14 +943,18 @@ int shape(ExpertsArgs* a) {
 }
 
 cudaError_t launch(ExpertsArgs a, int sms, cudaStream_t stream) {
-    const auto map = [&](CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t k, uint32_t box) {
-        const uint64_t bytes = static_cast<uint64_t>((k + kSlice - 1) / kSlice * (kSlice / 2));
-        return encode_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, bytes, static_cast<uint64_t>(rows), bytes, kSlice / 2, box,
-                             CU_TENSOR_MAP_SWIZZLE_64B);
-    };
-    if (!map(&a.up_map, a.up_q, int64_t{2} * a.experts * a.inner, a.dim, kUnitRows / 2) ||
-        !map(&a.down_map, a.down_q, int64_t{1} * a.experts * a.dim, a.inner, kUnitRows))
-        return cudaErrorInvalidValue;
+    const auto by = [](int32_t d) { return d == 1 ? 0u : static_cast<uint32_t>(((uint64_t{1} << 32) + d - 1) / d); };
+    for (ExpertsSide& s : a.side) {
+        const uint64_t bytes = static_cast<uint64_t>(s.slices) * (kSlice / 2);
+        s.pitch = Layout::pitch(s.k);
+        s.groups = s.slices * (kSlice / 8);
+        s.by_tiles = by(s.tiles);
+        s.by_slices = by(s.slices);
+        s.by_groups = by(s.groups);
+        if (!encode_map_2d(&s.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, s.codes, bytes, static_cast<uint64_t>(s.rows) * a.experts, bytes, kSlice / 2,
+                           kUnitRows / 2, CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
+    }
     using K = void (*)(ExpertsArgs);
     static const K kernels[2][3] = {{experts_kernel<2, 1>, experts_kernel<3, 1>, experts_kernel<4, 1>},
                                     {experts_kernel<2, 2>, experts_kernel<3, 2>, experts_kernel<4, 2>}};
@@ -981,10 +1007,10 @@ struct Parts {
     int64_t weights, ids, tops, backs, lowered, h, part, total;
     Parts(int64_t tokens, int64_t top_k, int64_t dim, int64_t inner) {
         const int64_t choices = tokens * top_k;
-        weights = align256(sizeof(ExpertsSync));
+        tops = align256(sizeof(ExpertsSync));   // at the same place in every call: each leaves them zero
+        weights = tops + 4 * MXFP4_EXPERTS_MAX_TOKENS * MXFP4_EXPERTS_MAX_TOP_K;
         ids = weights + align256(4 * choices);
-        tops = ids + align256(2 * choices);
-        backs = tops + align256(4 * choices);
+        backs = ids + align256(2 * choices);
         lowered = backs + align256(4 * tokens);
         h = lowered + align256(2 * tokens * ((dim + kSlice - 1) / kSlice * kSlice));
         part = h + align256(4 * choices * inner);
@@ -1047,10 +1073,21 @@ mxfp4_status mxfp4_experts_forward(const void* x, int64_t tokens, int64_t ldx, c
     a.inner = static_cast<int32_t>(inner);
     a.logits_f32 = flags & MXFP4_EXPERTS_LOGITS_F32 ? 1 : 0;
     a.normalize = flags & MXFP4_EXPERTS_NORMALIZE ? 1 : 0;
-    a.up_q = static_cast<const uint8_t*>(up_q);
-    a.up_s = static_cast<const uint8_t*>(up_s);
-    a.down_q = static_cast<const uint8_t*>(down_q);
-    a.down_s = static_cast<const uint8_t*>(down_s);
+    const int32_t d = a.dim, n = a.inner;
+    const auto set = [&](mxfp4::ExpertsSide& s, const void* q, const void* scales, int32_t rows, int32_t k, int32_t step, int32_t apart, int32_t half) {
+        s.codes = static_cast<const uint8_t*>(q);
+        s.scales = static_cast<const uint8_t*>(scales);
+        s.rows = rows;
+        s.k = k;
+        s.step = step;
+        s.apart = apart;
+        s.half = half;
+        s.tiles = (half + step - 1) / step;
+        s.slices = (k + mxfp4::kSlice - 1) / mxfp4::kSlice;
+    };
+    set(a.side[0], up_q, up_s, 2 * n, d, 16, n, n);
+    set(a.side[1], down_q, down_s, d, n, 32, 16, d);
+    a.side[1].down = 1;
     return mxfp4::launch(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
 }
 
