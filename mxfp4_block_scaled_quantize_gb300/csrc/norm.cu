@@ -22,8 +22,8 @@ bool pitch_ok(int64_t ld, int64_t dim, int64_t rows) { return rows <= 1 || (ld >
 
 // How the kernels may access these tensors of rows (null: not there), and the rows from one to the next that is shifted alike.
 // Shifted accesses cost every row some masks and a launch its edge rows; they are for bf16 rows that CTAs take, and, of a
-// backward pass, for many elements.  us shifted and single: forward 8192 rows of 4100 48 and 71, 16000 of 6001 126 and 161, 1111 of
-// 1001 5.2 and 6.1; backward 73 and 89, 141 and 202, 14.3 and 12.8, 5000 of 1531 24 and 27, 4000 of 777 16.6 and 15.9; fp32, 3000
+// backward pass, for many elements.  us shifted and single: forward 8192 rows of 4100 39 and 71, 16000 of 6001 87 and 161, 1111 of
+// 1001 4.9 and 6.1; backward 68 and 89, 130 and 202, 14.3 and 12.8, 5000 of 1531 24 and 27, 4000 of 777 16.6 and 15.9; fp32, 3000
 // of 2050, 13.3 and 14.0 forward, 26.5 and 23 backward; rows of 250, a warp's, 13.1 and 7.7.
 void set_access(mxfp4::NormArgs* a, bool f32, const void* const* rows, const int64_t* pitches, int count) {
     const int64_t size = f32 ? 4 : 2;

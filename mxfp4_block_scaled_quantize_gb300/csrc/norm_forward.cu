@@ -122,8 +122,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
         uint64_t square = 0ull;
         sum = 0ull;
 #pragma unroll
+        for (int i = 0; i < kP; ++i) x[i] = add2(x[i], Part::kShifted ? both(-mean) : Part::within(-mean, i, shape));
+        if constexpr (Part::kShifted) Part::clear(x, shape);
+#pragma unroll
         for (int i = 0; i < kP; ++i) {
-            x[i] = add2(x[i], Part::within(-mean, i, shape));
             sum = add2(sum, x[i]);
             square = fma2(x[i], x[i], square);
         }
@@ -208,7 +210,8 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
 
 // Elements a thread: 32 where rows come in 16-byte accesses, for the join of a row's warps costs each warp as much as
 // some 16 elements (8192 rows of 4096: 33 us with 16, 26 with 32; 16384 of 8192: 149 and 88); 16 where they do not, which the
-// registers of the single accesses' addresses fill.  A warp's row wins up to 1024 elements: 32768 rows of 1024 take 26 us, 46 as
+// registers of the single accesses' addresses fill, and 32 again for longer shifted rows (8192 rows of 2500 25 us with 16, 27 with
+// 32; of 4001 36 and 32; of 7001 69 and 52).  A warp's row wins up to 1024 elements: 32768 rows of 1024 take 26 us, 46 as
 // a CTA's.  Now 5.3 TB/s at 4096, 6.1 at 8192, 4.7 for 4608 rows of 5120.
 template <bool kF32, NormAccess kAccess>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
@@ -224,10 +227,17 @@ cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
         return launch<kF32, kAccess, 4, kRingRow, 512, 1>(a, sms, stream);
     } else {
         if (columns <= 2048) return launch<kF32, kAccess, 2, kRingRow, 128, 4>(a, sms, stream);
-        if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 2>(a, sms, stream);
-        if (columns <= 5120) return launch<kF32, kAccess, 2, kRingRow, 320, 2>(a, sms, stream);
-        if (columns <= 8192) return launch<kF32, kAccess, 2, kRingRow, 512, 1>(a, sms, stream);
-        return launch<kF32, kAccess, 2, kRingRow, 1024, 1>(a, sms, stream);
+        if constexpr (kAccess == kNormShifted) {
+            if (columns <= 2560) return launch<kF32, kAccess, 2, kRingRow, 256, 2>(a, sms, stream);
+            if (columns <= 4096) return launch<kF32, kAccess, 4, kRingRow, 128, 4>(a, sms, stream);
+            if (columns <= 8192) return launch<kF32, kAccess, 4, kRingRow, 256, 2>(a, sms, stream);
+            return launch<kF32, kAccess, 4, kRingRow, 512, 1>(a, sms, stream);
+        } else {
+            if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 2>(a, sms, stream);
+            if (columns <= 5120) return launch<kF32, kAccess, 2, kRingRow, 320, 2>(a, sms, stream);
+            if (columns <= 8192) return launch<kF32, kAccess, 2, kRingRow, 512, 1>(a, sms, stream);
+            return launch<kF32, kAccess, 2, kRingRow, 1024, 1>(a, sms, stream);
+        }
     }
 }
 

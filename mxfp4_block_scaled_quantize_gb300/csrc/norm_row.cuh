@@ -64,6 +64,12 @@ struct RowPart {
     __device__ __forceinline__ static bool inside(int k, const RowShape& s) {
         return kShifted ? static_cast<unsigned>(column(k, s)) < static_cast<unsigned>(s.dim) : column(k, s) < s.dim;
     }
+    // kShifted: s, for masks that are worked out where a group needs them.  Those of 32 elements, kept in registers for all rows, spill:
+    // 8192 rows of 4100 forward 57 us, 39 so; 16 elements' are kept (backward 69 us so, 68 kept; 8192 of 1001 forward 12.9 and 12.7).
+    __device__ __forceinline__ static RowShape afresh(RowShape s) {
+        if (kGroups > 2) asm volatile("" : "+r"(s.t));
+        return s;
+    }
     // kShifted: is all of group j inside.
     __device__ __forceinline__ static bool whole(int j, const RowShape& s) {
         const int c = column(8 * j, s);
@@ -87,10 +93,12 @@ struct RowPart {
                     uint32_t* const d = w + (j * kLoads + h) * 4;
                     d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
                 }
-                if (kShifted && !whole(j, s))
+                if (kShifted && !whole(j, s)) {
+                    const RowShape own = afresh(s);
 #pragma unroll
                     for (int k = 8 * j; k < 8 * j + 8; ++k)
-                        if (!inside(k, s)) w[k >> 1] &= k & 1 ? 0xFFFFu : 0xFFFF0000u;
+                        if (!inside(k, own)) w[k >> 1] &= k & 1 ? 0xFFFFu : 0xFFFF0000u;
+                }
             }
         } else if (kF32) {
 #pragma unroll
@@ -129,6 +137,19 @@ struct RowPart {
         if (kWide) return both(inside(2 * i, s) ? v : 0.0f);
         return pack2(make_float2(inside(2 * i, s) ? v : 0.0f, inside(2 * i + 1, s) ? v : 0.0f));
     }
+    // kShifted: zeros outside the row.  Only groups over its ends take the masks.
+    __device__ __forceinline__ static void clear(uint64_t* v, const RowShape& s) {
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            if (whole(j, s)) continue;
+            const RowShape own = afresh(s);
+#pragma unroll
+            for (int i = 4 * j; i < 4 * j + 4; ++i) {
+                const float2 f = unpack2(v[i]);
+                v[i] = pack2(make_float2(inside(2 * i, own) ? f.x : 0.0f, inside(2 * i + 1, own) ? f.y : 0.0f));
+            }
+        }
+    }
     // The pairs v, each element rounded once to the row's type, to the row's elements.
     __device__ __forceinline__ static void store(void* row, const uint64_t* v, const RowShape& s) {
         uint8_t* const p = static_cast<uint8_t*>(row);
@@ -139,11 +160,12 @@ struct RowPart {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = unpack2(v[4 * j + i]);
                 if (kShifted && !whole(j, s)) {
+                    const RowShape own = afresh(s);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        if (!inside(8 * j + k, s)) continue;
+                        if (!inside(8 * j + k, own)) continue;
                         const float e = k & 1 ? f[k >> 1].y : f[k >> 1].x;
-                        reinterpret_cast<__nv_bfloat16*>(p)[column(8 * j + k, s)] = __float2bfloat16_rn(e);
+                        reinterpret_cast<__nv_bfloat16*>(p)[column(8 * j + k, own)] = __float2bfloat16_rn(e);
                     }
                     continue;
                 }
@@ -204,6 +226,28 @@ __device__ __forceinline__ void load_vector(const void* v, int64_t at, bool f32,
 #pragma unroll
             for (int i = 0; i < Part::kPairs; ++i) f[i] = p.pair(i);
         }
+        return;
+    }
+    if constexpr (Part::kShifted) {
+        // One branch for the type and all loads under way together: 100 rows of 5001 forward 4.8 us, 5.3 as below.  (Single accesses
+        // of fp32 lost by it: 8192 rows of 4001 99 us, 44 as below, with as many registers.)
+        const RowShape own = Part::afresh(s);
+        uint32_t w[Part::kElements];
+#pragma unroll
+        for (int k = 0; k < Part::kElements; ++k) w[k] = 0u;
+        if (f32) {
+            const uint32_t* const p = static_cast<const uint32_t*>(v) + at;
+#pragma unroll
+            for (int k = 0; k < Part::kElements; ++k)
+                if (Part::inside(k, own)) w[k] = p[Part::column(k, own)];
+        } else {
+            const uint16_t* const p = static_cast<const uint16_t*>(v) + at;
+#pragma unroll
+            for (int k = 0; k < Part::kElements; ++k)
+                if (Part::inside(k, own)) w[k] = static_cast<uint32_t>(p[Part::column(k, own)]) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < Part::kPairs; ++i) f[i] = pack2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])));
         return;
     }
     auto one = [&](int k) {
