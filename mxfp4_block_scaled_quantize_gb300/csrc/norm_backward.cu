@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
     if (kRing) ring_init(ring, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
-    int issued = 0;
-    auto copy = [&](int64_t r, int slot) {   // thread 0
+    int issued = 0;   // of thread 0: the copies so far
+    auto copy = [&](int64_t r, int slot) {   // one thread
         if (*static_cast<volatile int*>(&ring.abort) != 0) return;
         ++issued;
         const uint32_t bar = smem_addr(&ring.full[slot]), to = smem_addr(slots + 2 * slot * part_bytes);
@@ -64,8 +64,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         ring_copy<kWide>(to, x, bytes, bar);
         ring_copy<kWide>(to + part_bytes, y, bytes, bar);
     };
-    if (kRing && threadIdx.x == 0)
-        for (int i = 0; i < a.stages && first + i * stride < end; ++i) copy(first + i * stride, i);
+    if (kRing && lane_id() == 0) {   // the first rows, each by another warp: a copy costs its thread some 400 clocks
+        for (int i = static_cast<int>(threadIdx.x >> 5); i < a.stages && first + i * stride < end; i += threads >> 5) copy(first + i * stride, i);
+        issued = 0;
+        while (issued < a.stages && first + issued * stride < end) ++issued;
+    }
     uint64_t g[kP], dw[kP], db[kP];
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
