@@ -122,17 +122,22 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     const void* const tensors[3] = {x, dy, dx};
     const int64_t pitches[3] = {ldx, lddy, lddx};
     set_access(&a, flags & MXFP4_NORM_X_F32, tensors, pitches, 3);
-    // Each CTA its rows of one sample, shifted alike, about as many for each as the whole has for norm_chunks(dim) CTAs.
+    // Each CTA its rows of one sample, shifted alike; norm_chunks(dim) CTAs at most, if the samples are not more.
     const int64_t sample_rows = rows / samples;
-    const int64_t even = cdiv(rows, mxfp4::norm_chunks(dim));
-    const int64_t chunk_rows = even > mxfp4::kNormLeastRows ? even : mxfp4::kNormLeastRows;
-    int64_t chunks = rows > 0 ? a.period * cdiv(cdiv(sample_rows, a.period), chunk_rows) : 1;
+    int64_t chunk_rows = 1, chunks = 1;
+    auto split = [&] {
+        const int64_t alike = cdiv(sample_rows, a.period), most = mxfp4::norm_chunks(dim) / (samples * a.period);
+        const int64_t even = most > 1 ? cdiv(alike, most) : alike;
+        chunk_rows = even > mxfp4::kNormLeastRows ? even : mxfp4::kNormLeastRows;
+        chunks = rows > 0 ? a.period * cdiv(alike, chunk_rows) : 1;
+    };
+    split();
     if (a.period > 1 && samples * chunks > mxfp4::norm_slots(dim)) {   // many short samples: their partial rows would not fit
         a.access = mxfp4::kNormSingle;
         a.period = 1;
-        chunks = cdiv(sample_rows, chunk_rows);
+        split();
     }
-    const int64_t ctas = samples * chunks;   // with several chunks a sample: at most rows / chunk_rows + samples, norm_slots(dim)
+    const int64_t ctas = samples * chunks;
     const bool partial = chunks > 1 && (dw != nullptr || db != nullptr);
     size_t need = 0;
     if (partial && (mxfp4_layer_norm_workspace_bytes(dim, &need) != MXFP4_OK || workspace == nullptr || workspace_bytes < need))
