@@ -14,11 +14,8 @@ constexpr int kNormStagesForward = 3;
 constexpr int kNormStagesBackward = 4;
 constexpr int kNormStages = 4;
 
-// CTAs that share the rows of a backward pass, each of which leaves a partial row of dw and db: as many as
-// 152 SMs hold at a time, 512 threads each.
-inline int norm_chunks(int64_t dim) {
-    return dim <= kNormWarpRowDim ? 608 : dim <= 1024 ? 1216 : dim <= 2048 ? 608 : dim <= 4096 ? 304 : 152;
-}
+// CTAs that share the rows of a backward pass, each of which leaves a partial row of dw and db: as many as 152 SMs hold at a time.
+inline int norm_chunks(int64_t dim) { return dim <= kNormWarpRowDim ? 608 : 152; }
 inline int64_t norm_slots(int64_t dim) { return 2 * norm_chunks(dim); }
 constexpr int64_t kNormLeastRows = 4;    // of a CTA, where there are few: a partial row costs as much as two rows of x
 

@@ -11,9 +11,10 @@
 // out; the partial rows are 4 / chunk_rows of x and dy in bf16.
 //
 // 16 elements a thread, for dw, db and the gain in registers leave room for no more at 512 threads an SM (8 a thread and 1024
-// threads: 16384 rows of 8192 in 156 us, 129 with 16; 24 warps at 85 registers each spill: 8192 of 4096 in 58 us, 39 with 16 warps).
-// Now 6.2 TB/s for 16384 rows of 8192, 5.2 for 8192 of 4096; of 39 us there the second kernel takes 4.  Rows of more than 8192
-// elements have 64 registers a thread, and spill: 4096 rows of 16384 take 187 us, 2.2 TB/s.
+// threads: 16384 rows of 8192 in 156 us, 129 with 16; 24 warps at 85 registers each spill: 8192 of 4096 in 58 us, 40 with 16 warps;
+// the gain in shared memory and 20 warps instead of 10 for rows of 5120: 35 us either way).
+// Now 6.2 TB/s for 16384 rows of 8192, 5.3 for 8192 of 4096, of whose 38 us the partial rows and the second kernel take 6.  Rows of more
+// than 8192 elements have 64 registers a thread, and spill: 4096 rows of 16384 take 187 us, 2.2 TB/s.
 #include <atomic>
 
 #include "norm_row.cuh"
@@ -21,36 +22,46 @@
 namespace mxfp4 {
 namespace {
 
+// A CTA of shorter rows has teams of kThreads threads at most, 512 in all, each with a row and a ring to itself, and one partial row for
+// all of them.  (As a CTA each: 8192 rows of 4096 39.7 us, 38 so; 8192 of 1001 24.8 and 20.4; 1111 of 1001 11.9 and 9.0.)
+template <RowMode kMode, int kThreads>
+constexpr int kTeamsOf = kMode == kRingRow && kThreads < 512 ? 512 / kThreads : 1;
+
 template <bool kF32, NormAccess kAccess, int kGroups, RowMode kMode, int kThreads, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ __align__(16) uint8_t slots[];
+__global__ void __launch_bounds__(kThreads * kTeamsOf<kMode, kThreads>, kCtas) norm_backward_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
     using Part = RowPart<kF32, kAccess, kGroups>;
     constexpr bool kWide = Part::kWide;
     constexpr int kE = Part::kElements, kP = Part::kPairs;
     constexpr int kSize = kF32 ? 4 : 2;
     constexpr int kWarps = kThreads / 32;
     constexpr bool kWarp = kMode == kWarpRow, kRing = kMode == kRingRow;
-    __shared__ uint64_t shared[2][32];
-    __shared__ RowRing ring;
+    constexpr int kTeams = kTeamsOf<kMode, kThreads>;
+    __shared__ uint64_t team_sums[kTeams][2][kWarps];
+    __shared__ RowRing rings[kTeams];
     __shared__ float sums[kWarp ? kWarps : 1][kWarp ? 32 * kE : 1];
-    const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
-    const int threads = kWarp ? 32 : static_cast<int>(blockDim.x);
+    const int threads = kWarp ? 32 : static_cast<int>(blockDim.x) / kTeams;
+    const int team = kTeams > 1 ? static_cast<int>(threadIdx.x) / threads : 0;
+    const int t = kWarp ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x) - team * threads;
+    RowRing& ring = rings[team];
     // rows first, first + period, ..., chunk_rows of them at most
     const int64_t sample = blockIdx.x / a.chunks;
     const int32_t chunk = blockIdx.x % a.chunks;
     const int64_t in_sample = chunk % a.period + static_cast<int64_t>(chunk / a.period) * a.chunk_rows * a.period;
     const int64_t first = sample * a.sample_rows + in_sample;
     const int64_t end = sample * a.sample_rows + min(in_sample + a.chunk_rows * a.period, a.sample_rows);
-    const int64_t stride = (kWarp ? kWarps : 1) * static_cast<int64_t>(a.period);
+    const int64_t stride = (kWarp ? kWarps : kTeams) * static_cast<int64_t>(a.period);
     const int skew = Part::kShifted ? static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const uint8_t*>(a.x) + first * a.ldx * kSize) & 15u) : 0;
     const RowShape shape{a.dim, t, threads, skew / kSize};
     const float inv = 1.0f / static_cast<float>(a.dim);
     const uint8_t *const xs = static_cast<const uint8_t*>(a.x), *const ys = static_cast<const uint8_t*>(a.dy);
     const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize, part_bytes = ring_bytes<kWide>(bytes);
-    if (kRing) ring_init(ring, a.stages);
+    uint8_t* const slots = shared_bytes + (kRing ? 2 * team * a.stages * part_bytes : 0u);
+    if (kRing) ring_init(rings, kTeams, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
-    int issued = 0;   // of thread 0: the copies so far
+    int64_t row = first + (kWarp ? static_cast<int64_t>(threadIdx.x >> 5) : static_cast<int64_t>(team)) * a.period;
+    int issued = 0;   // of a team's thread 0: the copies so far
     auto copy = [&](int64_t r, int slot) {   // one thread
         if (*static_cast<volatile int*>(&ring.abort) != 0) return;
         ++issued;
@@ -65,9 +76,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         ring_copy<kWide>(to + part_bytes, y, bytes, bar);
     };
     if (kRing && lane_id() == 0) {   // the first rows, each by another warp: a copy costs its thread some 400 clocks
-        for (int i = static_cast<int>(threadIdx.x >> 5); i < a.stages && first + i * stride < end; i += threads >> 5) copy(first + i * stride, i);
+        for (int i = t >> 5; i < a.stages && row + i * stride < end; i += threads >> 5) copy(row + i * stride, i);
         issued = 0;
-        while (issued < a.stages && first + issued * stride < end) ++issued;
+        while (issued < a.stages && row + issued * stride < end) ++issued;
     }
     uint64_t g[kP], dw[kP], db[kP];
 #pragma unroll
@@ -82,7 +93,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
 #pragma unroll
             for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
     }
-    int64_t row = first + (kWarp ? static_cast<int64_t>(threadIdx.x >> 5) * a.period : 0);
     Part nx, ny;
     float nmean = 0.0f, nrstd = 0.0f;
     auto fetch = [&](int64_t r) {
@@ -102,9 +112,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
             const uint8_t *const x = xs + row * a.ldx * kSize, *const y = ys + row * a.lddy * kSize;
             uint8_t* const in = slots + 2 * slot * part_bytes;
             if (ring_edge<kWide>(row, a.rows)) {
-                ring_fill<kF32>(in + ring_skew<kWide>(x), x, a.dim);
-                ring_fill<kF32>(in + part_bytes + ring_skew<kWide>(y), y, a.dim);
-                __syncthreads();
+                ring_fill<kF32>(in + ring_skew<kWide>(x), x, a.dim, t, threads);
+                ring_fill<kF32>(in + part_bytes + ring_skew<kWide>(y), y, a.dim, t, threads);
+                row_meet<(kTeams > 1)>(team, threads);
             }
             nx.template load<true>(in + ring_skew<kWide>(x), shape);
             ny.template load<true>(in + part_bytes + ring_skew<kWide>(y), shape);
@@ -123,9 +133,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         }
         if (row + stride < end) fetch(row + stride);
         const float2 s1 = unpack2(sa), s2 = unpack2(sx);
-        const float2 sum = row_sum2<kMode, kWarps>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y)), shared[turn]);
+        const float2 sum = row_sum2<kMode, kWarps, (kTeams > 1)>(pack2(make_float2(s1.x + s1.y, s2.x + s2.y)), team_sums[team][turn], t, team, threads);
         if (kRing) {
-            if (threadIdx.x == 0 && row + a.stages * stride < end) copy(row + a.stages * stride, slot);
+            if (t == 0 && row + a.stages * stride < end) copy(row + a.stages * stride, slot);
             if (++slot == a.stages) {
                 slot = 0;
                 phase ^= 1u;
@@ -136,7 +146,40 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_backward_kernel(const __
         for (int i = 0; i < kP; ++i) c[i] = mul2(add2(fma2(xh[i], m2, c[i]), m1), both(rstd));
         Part::store(static_cast<uint8_t*>(a.y) + row * a.ldy * kSize, c, shape);
     }
-    if (kRing && threadIdx.x == 0) ring_drain(ring, a.stages, issued);
+    if (kRing && t == 0) ring_drain(ring, a.stages, issued);
+    if constexpr (kTeams > 1) {
+        if (a.partial_w == nullptr && a.partial_b == nullptr) return;
+        // The teams' rows in the rings' place: 2 kTeams of fp32, where each team had room for two rows of fp32 or four of bf16 at least.
+        float* const rows = reinterpret_cast<float*>(shared_bytes);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float* const out = rows + (i * kTeams + team) * a.dim;
+            const uint64_t* const v = i == 0 ? dw : db;
+            if constexpr (kWide) {
+                RowPart<true, kNormWide, kGroups>::store(out, v, shape);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kP; ++k) {
+                    const float2 f = unpack2(v[k]);
+                    if (Part::inside(2 * k, shape)) out[Part::column(2 * k, shape)] = f.x;
+                    if (Part::inside(2 * k + 1, shape)) out[Part::column(2 * k + 1, shape)] = f.y;
+                }
+            }
+        }
+        __syncthreads();
+        for (int i = 0; i < 2; ++i) {
+            float* const to = i == 0 ? a.partial_w : a.partial_b;
+            if (to == nullptr) continue;
+            for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kTeams; ++j) s += rows[(i * kTeams + j) * a.dim + c];
+                to[static_cast<int64_t>(blockIdx.x) * a.dim + c] = s;
+            }
+        }
+        return;
+    }
     float* const to[2] = {a.partial_w, a.partial_b};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -217,7 +260,7 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
     const auto kernel = norm_backward_kernel<kF32, kAccess, kGroups, kMode, kThreads, kCtas>;
     const int threads = kMode == kWarpRow ? kThreads : row_threads(columns_of(a), kGroups);
     // The ring: as many rows as fit beside the CTAs that share the SM.
-    constexpr int kBudget = 208 * 1024 / kCtas;
+    constexpr int kTeams = kTeamsOf<kMode, kThreads>, kBudget = 208 * 1024 / kTeams;   // of a team: what is left is for the rest
     const int slot_bytes = 2 * static_cast<int>(ring_bytes<kAccess == kNormWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStagesBackward ? kBudget / slot_bytes : kNormStagesBackward;
     if (kMode == kRingRow) {   // once a device: the call costs the host as much as a launch
@@ -227,12 +270,12 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         const uint64_t bit = uint64_t{1} << (dev & 63);
         if (!(known.load(std::memory_order_relaxed) & bit)) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTeams * kBudget);
             if (e != cudaSuccess) return e;
             known.fetch_or(bit, std::memory_order_relaxed);
         }
     }
-    return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), threads, a.stages * slot_bytes, stream);
+    return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), kTeams * threads, kTeams * a.stages * slot_bytes, stream);
 }
 
 template <bool kF32, NormAccess kAccess>
@@ -242,9 +285,9 @@ cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
         if (columns <= 256) return launch<kF32, kAccess, 1, kWarpRow, 256, 2>(a, ctas, stream);
         if (columns <= kNormWarpRowDim) return launch<kF32, kAccess, 2, kWarpRow, 256, 2>(a, ctas, stream);
     }
-    if (columns <= 1024) return launch<kF32, kAccess, 2, kRingRow, 64, 8>(a, ctas, stream);
-    if (columns <= 2048) return launch<kF32, kAccess, 2, kRingRow, 128, 4>(a, ctas, stream);
-    if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 2>(a, ctas, stream);
+    if (columns <= 1024) return launch<kF32, kAccess, 2, kRingRow, 64, 1>(a, ctas, stream);
+    if (columns <= 2048) return launch<kF32, kAccess, 2, kRingRow, 128, 1>(a, ctas, stream);
+    if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 1>(a, ctas, stream);
     if (columns <= 8192) return launch<kF32, kAccess, 2, kRingRow, 512, 1>(a, ctas, stream);
     return launch<kF32, kAccess, 2, kRingRow, 1024, 1>(a, ctas, stream);
 }

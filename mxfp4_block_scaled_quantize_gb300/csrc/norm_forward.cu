@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
     const float inv = 1.0f / static_cast<float>(a.dim);
     const uint8_t* const xs = static_cast<const uint8_t*>(a.x);
     const uint32_t bytes = static_cast<uint32_t>(a.dim) * kSize, slot_bytes = ring_bytes<kWide>(bytes);
-    if (kRing) ring_init(ring, a.stages);
+    if (kRing) ring_init(&ring, 1, a.stages);
     grid_wait_prerequisites();
     grid_launch_dependents();
     int issued = 0;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_forward_kernel(const __g
             const uint8_t* const from = xs + row * a.ldx * kSize;
             uint8_t* const in = slots + slot * slot_bytes + ring_skew<kWide>(from);
             if (ring_edge<kWide>(row, a.rows)) {
-                ring_fill<kF32>(in, from, a.dim);
+                ring_fill<kF32>(in, from, a.dim, t, threads);
                 __syncthreads();
             }
             next.template load<true>(in, shape);

@@ -308,13 +308,20 @@ __device__ __forceinline__ void ring_copy(uint32_t to, const uint8_t* row, uint3
     bulk_load(to, row - ring_skew<kWide>(row), ring_moved<kWide>(row, bytes), bar);
 }
 
-__device__ __forceinline__ void ring_init(RowRing& r, int stages) {
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) mbar_init(smem_addr(&r.full[i]), 1);
-        r.abort = 0;
+__device__ __forceinline__ void ring_init(RowRing* r, int count, int stages) {
+    if (static_cast<int>(threadIdx.x) < count) {
+        for (int i = 0; i < stages; ++i) mbar_init(smem_addr(&r[threadIdx.x].full[i]), 1);
+        r[threadIdx.x].abort = 0;
         fence_barrier_init();
     }
     __syncthreads();
+}
+
+// A row's threads meet: all of a CTA's, or one of its teams' of `threads`.
+template <bool kTeams>
+__device__ __forceinline__ void row_meet(int team, int threads) {
+    if (kTeams) named_barrier(1 + team, threads);
+    else __syncthreads();
 }
 
 __device__ __forceinline__ void ring_wait(RowRing& r, int slot, uint32_t phase, uint32_t* err) {
@@ -326,20 +333,20 @@ struct Element { using Type = uint16_t; };
 template <>
 struct Element<true> { using Type = uint32_t; };
 
-// An edge row into its slot; a barrier of the CTA is to follow.
+// An edge row into its slot, by thread t of `threads`; a barrier of theirs is to follow.
 template <bool kF32>
-__device__ __forceinline__ void ring_fill(uint8_t* to, const uint8_t* row, int dim) {
+__device__ __forceinline__ void ring_fill(uint8_t* to, const uint8_t* row, int dim, int t, int threads) {
     using T = typename Element<kF32>::Type;
     constexpr int kTogether = 16;   // loads under way
     const T* const from = reinterpret_cast<const T*>(row);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < dim; i += kTogether * blockDim.x) {
+    for (int i = t; i < dim; i += kTogether * threads) {
         T v[kTogether];
 #pragma unroll
-        for (int k = 0; k < kTogether; ++k) v[k] = from[min(i + k * static_cast<int>(blockDim.x), dim - 1)];
+        for (int k = 0; k < kTogether; ++k) v[k] = from[min(i + k * threads, dim - 1)];
 #pragma unroll
         for (int k = 0; k < kTogether; ++k)
-            if (i + k * static_cast<int>(blockDim.x) < dim) reinterpret_cast<T*>(to)[i + k * blockDim.x] = v[k];
+            if (i + k * threads < dim) reinterpret_cast<T*>(to)[i + k * threads] = v[k];
     }
 }
 
@@ -366,14 +373,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // Two sums over the row's threads, in all of them and in the same order in each.  A row of several warps, of
 // kWarps at most, goes through `shared`, which two calls in a row do not share: one barrier a call.
-template <RowMode kMode, int kWarps>
-__device__ __forceinline__ float2 row_sum2(uint64_t v, uint64_t* shared) {
+template <RowMode kMode, int kWarps, bool kTeams>
+__device__ __forceinline__ float2 row_sum2(uint64_t v, uint64_t* shared, int t, int team, int threads) {
     v = lanes_sum2<32>(v);
     if (kMode == kWarpRow) return unpack2(v);
-    if (lane_id() == 0) shared[threadIdx.x >> 5] = v;
-    __syncthreads();
+    if (lane_id() == 0) shared[t >> 5] = v;
+    row_meet<kTeams>(team, threads);
     const int i = static_cast<int>(lane_id()) & (kWarps - 1);
-    return unpack2(lanes_sum2<kWarps>(i < static_cast<int>(blockDim.x >> 5) ? shared[i] : 0ull));
+    return unpack2(lanes_sum2<kWarps>(i < threads >> 5 ? shared[i] : 0ull));
 }
 
 }  // namespace mxfp4
