@@ -23,8 +23,9 @@ bool pitch_ok(int64_t ld, int64_t dim, int64_t rows) { return rows <= 1 || (ld >
 // How the kernels may access these tensors of rows (null: not there), and the rows from one to the next that is shifted alike.
 // Shifted accesses cost every row some masks and a launch its edge rows; they are for bf16 rows that CTAs take, and, of a
 // backward pass, for many elements.  us shifted and single: forward 8192 rows of 4100 39 and 71, 16000 of 6001 87 and 161, 1111 of
-// 1001 4.9 and 6.1; backward 68 and 89, 130 and 202, 14.3 and 12.8, 5000 of 1531 24 and 27, 4000 of 777 16.6 and 15.9; fp32, 3000
-// of 2050, 13.3 and 14.0 forward, 26.5 and 23 backward; rows of 250, a warp's, 13.1 and 7.7.
+// 1001 4.9 and 6.1; backward 1111 of 1001 10.2 and 9.0, 4000 of 777 13.9 and 14.9, 2000 of 2001 15.2 and 15.8, 8192 of 1001 20.3 and
+// 22.8, 100 of 5001 13.4 and 12.0, 600 of 7001 24.1 and 20.3, 8192 of 4100 68 and 84, 16000 of 6001 131 and 175; fp32, 3000 of 2050,
+// 13.3 and 14.0 forward, 26.5 and 23 backward; rows of 250, a warp's, 13.1 and 7.7.
 void set_access(mxfp4::NormArgs* a, bool f32, const void* const* rows, const int64_t* pitches, int count) {
     const int64_t size = f32 ? 4 : 2;
     uintptr_t base = 0;
@@ -45,7 +46,7 @@ void set_access(mxfp4::NormArgs* a, bool f32, const void* const* rows, const int
     if (wide) {
         a->access = mxfp4::kNormWide;
     } else if (alike && !f32 && a->dim > mxfp4::kNormWarpRowDim && a->dim + 7 <= MXFP4_NORM_MAX_DIM &&
-               (count == 2 || a->rows >= (int64_t{1} << 22) / a->dim)) {
+               (count == 2 || a->rows >= (int64_t{1} << (a->dim <= 4096 ? 21 : 23)) / a->dim)) {
         a->access = mxfp4::kNormShifted;
         while (step * a->period % 16 != 0) a->period *= 2;
     } else {
