@@ -12,7 +12,7 @@
 //
 // 16 elements a thread, for dw, db and the gain in registers leave room for no more at 512 threads an SM (8 a thread and 1024
 // threads: 16384 rows of 8192 in 156 us, 129 with 16; 24 warps at 85 registers each spill: 8192 of 4096 in 58 us, 40 with 16 warps;
-// the gain in shared memory and 20 warps instead of 10 for rows of 5120: 35 us either way).
+// two teams of rows of 5120 have it in shared memory).
 // Now 6.2 TB/s for 16384 rows of 8192, 5.3 for 8192 of 4096, of whose 38 us the partial rows and the second kernel take 6.  Rows of more
 // than 8192 elements have 64 registers a thread, and spill: 4096 rows of 16384 take 187 us, 2.2 TB/s.
 #include <atomic>
@@ -25,7 +25,11 @@ namespace {
 // A CTA of shorter rows has teams of kThreads threads at most, 512 in all, each with a row and a ring to itself, and one partial row for
 // all of them.  (As a CTA each: 8192 rows of 4096 39.7 us, 38 so; 8192 of 1001 24.8 and 20.4; 1111 of 1001 11.9 and 9.0.)
 template <RowMode kMode, int kThreads>
-constexpr int kTeamsOf = kMode == kRingRow && kThreads < 512 ? 512 / kThreads : 1;
+constexpr int kTeamsOf = kMode != kRingRow ? 1 : kThreads == 320 ? 2 : kThreads < 512 ? 512 / kThreads : 1;
+
+// Two teams of 320 threads have 96 registers each: their gains are in shared memory, where each thread finds its own.
+template <int kThreads>
+constexpr bool kGainsStored = kThreads == 320;
 
 template <bool kF32, NormAccess kAccess, int kGroups, RowMode kMode, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads * kTeamsOf<kMode, kThreads>, kCtas) norm_backward_kernel(const __grid_constant__ NormArgs a) {
@@ -34,7 +38,7 @@ __global__ void __launch_bounds__(kThreads * kTeamsOf<kMode, kThreads>, kCtas) n
     constexpr bool kWide = Part::kWide;
     constexpr int kE = Part::kElements, kP = Part::kPairs;
     constexpr int kSize = kF32 ? 4 : 2;
-    constexpr int kWarps = kThreads / 32;
+    constexpr int kWarps = kThreads == 320 ? 16 : kThreads / 32;   // of a row's sums: a power of two
     constexpr bool kWarp = kMode == kWarpRow, kRing = kMode == kRingRow;
     constexpr int kTeams = kTeamsOf<kMode, kThreads>;
     __shared__ uint64_t team_sums[kTeams][2][kWarps];
@@ -81,6 +85,7 @@ __global__ void __launch_bounds__(kThreads * kTeamsOf<kMode, kThreads>, kCtas) n
         while (issued < a.stages && row + issued * stride < end) ++issued;
     }
     uint64_t g[kP], dw[kP], db[kP];
+    ulonglong2* const gains = reinterpret_cast<ulonglong2*>(shared_bytes + (kRing ? 2 * kTeams * a.stages * part_bytes : 0u)) + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
         g[i] = both(1.0f);
@@ -93,6 +98,9 @@ __global__ void __launch_bounds__(kThreads * kTeamsOf<kMode, kThreads>, kCtas) n
 #pragma unroll
             for (int i = 0; i < kP; ++i) g[i] = add2(g[i], both(1.0f));
     }
+    if constexpr (kGainsStored<kThreads>)
+#pragma unroll
+        for (int i = 0; i < kP; i += 2) gains[i / 2 * kTeams * kThreads] = make_ulonglong2(g[i], g[i + 1]);
     Part nx, ny;
     float nmean = 0.0f, nrstd = 0.0f;
     auto fetch = [&](int64_t r) {
@@ -123,6 +131,12 @@ __global__ void __launch_bounds__(kThreads * kTeamsOf<kMode, kThreads>, kCtas) n
         uint64_t xh[kP], c[kP], sa = 0ull, sx = 0ull;
 #pragma unroll
         for (int i = 0; i < kP; ++i) {   // dy is zero behind the row's end
+            if constexpr (kGainsStored<kThreads>)
+                if (i % 2 == 0) {
+                    const ulonglong2 v = gains[i / 2 * kTeams * kThreads];
+                    g[i] = v.x;
+                    g[i + 1] = v.y;
+                }
             const uint64_t d = ny.pair(i);
             xh[i] = mul2(add2(nx.pair(i), both(-mean)), both(rstd));
             c[i] = mul2(d, g[i]);
@@ -260,7 +274,8 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
     const auto kernel = norm_backward_kernel<kF32, kAccess, kGroups, kMode, kThreads, kCtas>;
     const int threads = kMode == kWarpRow ? kThreads : row_threads(columns_of(a), kGroups);
     // The ring: as many rows as fit beside the CTAs that share the SM.
-    constexpr int kTeams = kTeamsOf<kMode, kThreads>, kBudget = 208 * 1024 / kTeams;   // of a team: what is left is for the rest
+    constexpr int kTeams = kTeamsOf<kMode, kThreads>, kGainBytes = kGainsStored<kThreads> ? 32 * kGroups * kTeams * kThreads : 0;
+    constexpr int kBudget = (208 * 1024 - kGainBytes) / kTeams;   // of a team: what is left is for the rest
     const int slot_bytes = 2 * static_cast<int>(ring_bytes<kAccess == kNormWide>(a.dim * (kF32 ? 4 : 2)));
     a.stages = kMode != kRingRow ? 0 : kBudget / slot_bytes < kNormStagesBackward ? kBudget / slot_bytes : kNormStagesBackward;
     if (kMode == kRingRow) {   // once a device: the call costs the host as much as a launch
@@ -270,14 +285,17 @@ cudaError_t launch(NormArgs a, int64_t ctas, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         const uint64_t bit = uint64_t{1} << (dev & 63);
         if (!(known.load(std::memory_order_relaxed) & bit)) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTeams * kBudget);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTeams * kBudget + kGainBytes);
             if (e != cudaSuccess) return e;
             known.fetch_or(bit, std::memory_order_relaxed);
         }
     }
-    return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), kTeams * threads, kTeams * a.stages * slot_bytes, stream);
+    return launch_dependent(kernel, a, dim3(static_cast<unsigned>(ctas), 1, 1), kTeams * threads, kTeams * a.stages * slot_bytes + kGainBytes, stream);
 }
 
+// Two teams for rows of 4097 to 5120 elements, in place of one that leaves a third of the SM's registers, pay where a CTA has many
+// rows: 16384 rows of 4608 84 us, 96 with one; 9000 of 4200 50 and 56; 16384 of 5120 93 and 98; 8192 of 5120 in fp32 90 and 93; but 4608 of
+// 5120 35.7 and 35.4, 2048 of 5120 22.4 and 21.5, 4096 of 4608 in fp32 44.6 and 42.0.
 template <bool kF32, NormAccess kAccess>
 cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
     const int columns = columns_of(a);
@@ -288,6 +306,8 @@ cudaError_t launch(const NormArgs& a, int64_t ctas, cudaStream_t stream) {
     if (columns <= 1024) return launch<kF32, kAccess, 2, kRingRow, 64, 1>(a, ctas, stream);
     if (columns <= 2048) return launch<kF32, kAccess, 2, kRingRow, 128, 1>(a, ctas, stream);
     if (columns <= 4096) return launch<kF32, kAccess, 2, kRingRow, 256, 1>(a, ctas, stream);
+    if constexpr (kAccess == kNormWide)
+        if (columns <= 5120 && a.chunk_rows >= 32) return launch<kF32, kAccess, 2, kRingRow, 320, 1>(a, ctas, stream);
     if (columns <= 8192) return launch<kF32, kAccess, 2, kRingRow, 512, 1>(a, ctas, stream);
     return launch<kF32, kAccess, 2, kRingRow, 1024, 1>(a, ctas, stream);
 }

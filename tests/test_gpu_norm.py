@@ -138,6 +138,11 @@ def test_every_number_of_rows(rows, dim):
     check(rows, dim)
 
 
+@pytest.mark.parametrize("rows, dim, samples, dtype", [(4900, 4104, 1, torch.bfloat16), (2574, 4608, 78, torch.bfloat16), (2541, 5120, 77, torch.float32)])
+def test_many_rows_of_a_cta(rows, dim, samples, dtype):
+    check(rows, dim, dtype, torch.float32, samples)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("w_dtype", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("dim, pitch", [(256, 8), (256, 3), (1100, 0), (1104, 16), (2304, 1)])
