@@ -348,6 +348,7 @@ __device__ __forceinline__ void ring_fill(uint8_t* to, const uint8_t* row, int d
         for (int k = 0; k < kTogether; ++k)
             if (i + k * threads < dim) reinterpret_cast<T*>(to)[i + k * threads] = v[k];
     }
+    fence_proxy_async_smem();   // a copy writes the slot next
 }
 
 // Thread 0, before it ends: copies that a wait gave up on may still be on their way.
