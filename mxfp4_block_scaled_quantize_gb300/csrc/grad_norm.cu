@@ -304,13 +304,14 @@ inline int64_t units_of(const mxfp4_grad_tensor& t, int esize) {
     return (t.n + skew + unit - 1) / unit;
 }
 
-// The tensors from t[j] on that one launch takes, and the index behind them; none are left: count 0.
+// The tensors from t[j] on that one launch takes, and the index behind them and the empty ones that follow; none are left: count 0.
 template <int kCap>
 int32_t fill(GradArgs<kCap>* a, int32_t count, const mxfp4_grad_tensor* t, int32_t j, int esize) {
     int64_t units = 0;   // below 2^29: check() bounds the elements of a call
     a->count = 0;
-    for (; j < count && a->count < kCap; ++j) {
+    for (; j < count; ++j) {
         if (t[j].n == 0) continue;
+        if (a->count == kCap) break;
         units += units_of(t[j], esize);
         a->t[a->count] = t[j];
         a->end[a->count++] = static_cast<int32_t>(units);
