@@ -630,7 +630,8 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
  * where max_norm is infinite, into out[0] and out[1] (device memory).  With MXFP4_GRAD_SCALE the
  * gradients are then multiplied by the factor in place, each product rounded once to its type; else
  * they are only read, and mxfp4_adamw takes the factor as its grad_factor.  The norm holds for
- * elements of every finite size; an infinite one gives norm inf and factor 0, a NaN makes both NaN.
+ * elements of every finite size; an infinite one gives norm inf and factor 0 (1 where max_norm is
+ * infinite too), a NaN makes both NaN whatever max_norm is.
  * The same gradients give the same bits.
  *   tensors    count of them (0 .. MXFP4_GRAD_MAX_TENSORS), n elements each (n == 0: skipped; at most
  *              2^40 in all), dense, aligned to their element; with MXFP4_GRAD_SCALE

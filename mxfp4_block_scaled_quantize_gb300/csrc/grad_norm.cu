@@ -242,11 +242,9 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_norm_kernel
     sum = block_sum(sum, shared);
     if (threadIdx.x == 0) {
         const double norm = sqrt(sum);
-        double factor = 1.0;
-        if (!isinf(a.max_norm)) {
-            factor = a.max_norm / (norm + 1e-6);
-            if (factor > 1.0) factor = 1.0;   // a NaN stays
-        }
+        double factor = a.max_norm / (norm + 1e-6);
+        if (factor > 1.0 || isinf(a.max_norm)) factor = 1.0;
+        if (isnan(norm)) factor = norm;   // whatever max_norm is
         a.out[0] = static_cast<float>(norm);
         a.out[1] = static_cast<float>(factor);
         a.head->done = 0;

@@ -37,7 +37,7 @@ def _check_grads(grads, numel, gpu):
 class GradNorm:
     """The norm of all gradients of `params` (CUDA tensors: their sizes and GPU are taken).
 
-    Its results are `out`, fp32 [norm, factor] on the GPU, factor = min(1, max_norm / (norm + 1e-6)).
+    Its results are `out`, fp32 [norm, factor] on the GPU, factor = min(1, max_norm / (norm + 1e-6)); a NaN makes both NaN.
     They live until the next call, and calls of one GradNorm, or replays of graphs that hold them, come
     one after the other: give each of two that may overlap a GradNorm of its own."""
 
