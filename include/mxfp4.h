@@ -556,6 +556,7 @@ mxfp4_status mxfp4_experts_forward(const void* x, int64_t tokens, int64_t ldx, c
 #define MXFP4_ADAMW_G_F32 2          /* gradients fp32 (else bf16)                             */
 #define MXFP4_ADAMW_STATE_E4M3 4     /* moments in 8 bits (else fp32)                          */
 #define MXFP4_ADAMW_STOCHASTIC 8     /* 8-bit moments rounded stochastically (with STATE_E4M3)  */
+#define MXFP4_ADAMW_GRAD_FACTOR 32   /* the parameters hold a grad_factor                       */
 #define MXFP4_ADAMW_BLOCK 128
 
 /* One tensor of n elements (n == 0: skipped), dense, every buffer aligned to its element; all
@@ -577,8 +578,9 @@ typedef struct {
  * four fp32 in device memory read instead of the host's values, so that a captured graph can
  * go on: lr, 1 - beta1^step, 1 - beta2^step, grad_scale; with MXFP4_ADAMW_STOCHASTIC five, the
  * fifth the step's number (exact up to 2^24).  seed: read with MXFP4_ADAMW_STOCHASTIC only.
- * grad_factor: NULL, or an fp32 in device memory that grad_scale is multiplied by (in fp32): the
- * factor of mxfp4_grad_norm. */
+ * grad_factor: read with MXFP4_ADAMW_GRAD_FACTOR only, so that a program built before it was there
+ * may pass a structure that ends at seed; NULL, or an fp32 in device memory that grad_scale is
+ * multiplied by (in fp32): the factor of mxfp4_grad_norm. */
 typedef struct {
     double lr;
     double beta1;

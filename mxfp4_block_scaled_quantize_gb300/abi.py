@@ -42,6 +42,7 @@ MXFP4_ADAMW_P_F32 = 1
 MXFP4_ADAMW_G_F32 = 2
 MXFP4_ADAMW_STATE_E4M3 = 4
 MXFP4_ADAMW_STOCHASTIC = 8
+MXFP4_ADAMW_GRAD_FACTOR = 32
 MXFP4_ADAMW_BLOCK = 128
 
 MXFP4_EXPERTS_LOGITS_F32 = 1

@@ -361,14 +361,16 @@ cudaError_t launch(const AdamwArgs<kCap>& a, int flags, cudaStream_t stream) {
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 mxfp4_status check(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, const mxfp4_adamw_params* h) {
-    if (count < 0 || (count > 0 && t == nullptr) || h == nullptr || (flags & ~15)) return MXFP4_ERR_INVALID_ARG;
+    if (count < 0 || (count > 0 && t == nullptr) || h == nullptr || (flags & ~(15 | MXFP4_ADAMW_GRAD_FACTOR)))
+        return MXFP4_ERR_INVALID_ARG;
     if ((flags & MXFP4_ADAMW_STOCHASTIC) && !(flags & MXFP4_ADAMW_STATE_E4M3)) return MXFP4_ERR_INVALID_ARG;
     // the fp32 values that the kernel uses have to lie in the ranges too
     const float b1 = static_cast<float>(h->beta1), b2 = static_cast<float>(h->beta2), eps = static_cast<float>(h->eps);
     if (!(h->beta1 >= 0.0 && b1 < 1.0f) || !(h->beta2 >= 0.0 && b2 < 1.0f) || !(h->eps >= 0.0) || h->step < 1 ||
         !std::isfinite(eps) || (h->eps > 0.0 && eps < kMinScale) || !std::isfinite(h->lr) || !std::isfinite(h->weight_decay))
         return MXFP4_ERR_INVALID_ARG;
-    if (!aligned_to(h->dynamic, 4) || !aligned_to(h->grad_factor, 4)) return MXFP4_ERR_MISALIGNED;
+    // without the flag the caller's structure may end before grad_factor
+    if (!aligned_to(h->dynamic, 4) || ((flags & MXFP4_ADAMW_GRAD_FACTOR) && !aligned_to(h->grad_factor, 4))) return MXFP4_ERR_MISALIGNED;
     const bool p_f32 = flags & MXFP4_ADAMW_P_F32, g_f32 = flags & MXFP4_ADAMW_G_F32, s8 = flags & MXFP4_ADAMW_STATE_E4M3;
     for (int32_t j = 0; j < count; ++j) {
         const mxfp4_adamw_tensor& x = t[j];
@@ -400,7 +402,7 @@ mxfp4_status step(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, con
     a.c2 = static_cast<float>(1.0 - std::pow(h.beta2, static_cast<double>(h.step)));
     a.grad_scale = static_cast<float>(h.grad_scale);
     a.dynamic = h.dynamic;
-    a.grad_factor = h.grad_factor;
+    a.grad_factor = flags & MXFP4_ADAMW_GRAD_FACTOR ? h.grad_factor : nullptr;
     a.first = 0;
     a.step = static_cast<uint32_t>(h.step);
     a.seed = flags & MXFP4_ADAMW_STOCHASTIC ? h.seed : 0;
@@ -419,7 +421,7 @@ mxfp4_status step(int32_t count, const mxfp4_adamw_tensor* t, int32_t flags, con
             a.t[a.count] = t[j++];
             a.end[a.count++] = static_cast<int32_t>(units);
         }
-        if (a.count > 0 && launch<kCap>(a, flags, stream) != cudaSuccess) return MXFP4_ERR_CUDA;
+        if (a.count > 0 && launch<kCap>(a, flags & 15, stream) != cudaSuccess) return MXFP4_ERR_CUDA;
         a.first += a.count;
     }
     return MXFP4_OK;

@@ -197,6 +197,8 @@ class AdamW:
                 raise ValueError(f"max_norm: for up to {abi.MXFP4_GRAD_MAX_TENSORS} parameters")
             self.grad_norm._run(addresses, dtype, max_norm, 0, stream)
             factor = self.grad_norm.out.data_ptr() + 4
+        if factor is not None:
+            flags |= abi.MXFP4_ADAMW_GRAD_FACTOR
         h = abi.AdamwParams(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                             grad_scale, step, None if dynamic is None else dynamic.data_ptr(), self.seed, factor)
         abi.mxfp4_adamw(len(self.params), self._address, flags, h, stream)
