@@ -83,6 +83,7 @@ struct Head {
     int32_t wide;      // the pass has more than 8 rows,
     int32_t slim;      // up to 4: the second product then has its activations' low parts beside the high ones, as columns 4 to 7
     int32_t abort;     // a wait has run out
+    int32_t lost[kWarps];  // of a warp whose first lane gave a wait up: 1 + 2 times the stage + 256 times the parity that it waited for; else 0
     uint32_t tops[kFew];   // largest magnitudes of rows of x, as bits
     uint64_t full[kWarps][kMaxStages];
 };
@@ -789,7 +790,12 @@ __device__ __forceinline__ void product(const ExpertsArgs& a, const ExpertsSide&
         int x = at.acts + g * pitch + t * 16 + seg.slice * (kSlice * 2);
 #pragma unroll 1
         for (int i = seg.slice; i < seg.last; ++i) {
-            if (!mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort)) stream.more = false;   // no copies over copies
+            if (!mbar_wait(st.full + 8 * st.next, st.phase, a.err, kErrExperts, &head->abort)) {
+                // No copies over copies, in this product or the next.  (A lane that gives up alone, for others ran out, leaves the
+                // stage's next phase without its arrival: the others give up there.)
+                stream.more = false;
+                if (lane == 0 && head->lost[warp] == 0) head->lost[warp] = 1 + 2 * st.next + 256 * static_cast<int>(st.phase);
+            }
             const int codes = st.codes + st.next * kSliceBytes, words = st.words + st.next * kWordBytes;
             if (kMost > 1 && wide) {
                 if (down) multiply<kMost, true>(shared, codes, words, scales, x, pitch, low, acc);
@@ -860,6 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         head->abort = 0;
+        for (int w = 0; w < kWarps; ++w) head->lost[w] = 0;
         prefetch_tensormap(&a.side[0].map);
         prefetch_tensormap(&a.side[1].map);
     }
@@ -903,6 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         const ExpertsSide& side = a.side[p];
         const Segments seg(head->range[2 * p], head->range[2 * p + 1]);
         Stream<kStages> stream(side, pairs, codes, words, st.full, st.next, seg);
+        __syncwarp();
+        if (*static_cast<volatile int*>(&head->lost[warp]) != 0) stream.more = false;
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) stream.ask();
         if (p != 0) {
@@ -913,11 +922,14 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         }
         product<kStages, kMost>(a, side, at, shared, seg, stream, pairs, st);
     }
-    if (*static_cast<volatile int*>(&head->abort) != 0 && lane_id() == 0)   // copies that a wait gave up on may be on their way
+    if (head->lost[warp] != 0 && lane_id() == 0) {   // copies from there on, which no wait has seen, may be on their way
+        st.next = (head->lost[warp] & 255) / 2;
+        st.phase = static_cast<uint32_t>(head->lost[warp] / 256);
         for (int i = 0; i < kStages; ++i) {
             mbar_wait_quiet(st.full + 8 * st.next, st.phase, kWaitLimitNs / 16);
             if (++st.next == kStages) st.next = 0, st.phase ^= 1u;
         }
+    }
     meet(a, 2);
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads) a.tops[i] = 0u;   // for the next call
