@@ -515,8 +515,11 @@ mxfp4_status mxfp4_grouped_backward(const mxfp4_grouped_linear* layer, const voi
  *   workspace  mxfp4_experts_workspace_bytes, 256-byte aligned, all zero before its first use (a call leaves zero
  *              what the next one needs so); calls that share one are ordered one after the other, as are replays of
  *              graphs that hold them
- * x, the weights and the sums are not rounded on the way: the products are those of the values that the blobs stand for, in
- * fp32, and the activations between the two keep 22 bits.  y is rounded once.  The same inputs give the same bits. */
+ * The weights are the values that the blobs stand for, sums are fp32, and y is rounded once.  x enters in fp16, times a power of
+ * two for each row: an element is exact from 2^-31 of its row's largest on, and off by 2^-39 of that at most below.  The
+ * activations between the products keep 22 bits, and are off by 2^-38 of their row's largest at most.  The powers of two are undone after a row's sums: with
+ * scales up to 2^96 (byte 223) no sum leaves fp32's range that is not outside it by its value; beyond that a small x may meet
+ * an infinity.  The same inputs give the same bits. */
 #define MXFP4_EXPERTS_LOGITS_F32 1
 #define MXFP4_EXPERTS_NORMALIZE 2
 #define MXFP4_EXPERTS_MAX_TOKENS 64

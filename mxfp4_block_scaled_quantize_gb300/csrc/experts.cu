@@ -10,9 +10,11 @@
 // expert and 4-bit or 8-bit activations) and up to 16 routed rows as its columns.
 //
 // Numbers.  A code is exact in fp16.  x is bf16 times a power of two that brings its row's largest value to 2^14 .. 2^15: exact
-// in fp16 but for what lies 2^-29 and more below that.  The activations between the products are fp32, and the second
-// product takes them as the sum of two fp16 (22 bits).  A block of 32 is summed by the matrix instruction in fp32 and then
-// multiplied by its scale in fp32, as all sums are.  y is rounded once.
+// in fp16 but for what lies more than 2^-31 below it, which is off by 2^-39 of it at most (half of fp16's smallest step).  The activations
+// between the products are fp32, and the second product takes them as the sum of two fp16 (22 bits).  A block of 32 is summed by
+// the matrix instruction in fp32 and then multiplied by its scale in fp32, as all sums are; the power of two is undone after
+// them: k elements of codes up to 6 stay below k 6 2^15 times the scale, in fp32's range up to a scale of 2^96 for every k that
+// fits the shared memory.  y is rounded once.
 //
 // Four phases, with the grid meeting in between (a cooperative launch, one CTA an SM; a barrier takes 1 to 2 us):
 //   1. CTA t: token t's choices, and its row of x in fp16.  (Up to kFew tokens: every CTA, all of them, and no barrier.)
