@@ -605,9 +605,9 @@ mxfp4_status mxfp4_adamw(int32_t count, const mxfp4_adamw_tensor* tensors, int32
  * g the weight, or 1 + weight with MXFP4_NORM_ADD_ONE (modulation), 1 where weight is NULL; b the
  * bias, 0 where it is NULL.  All in fp32, y rounded once.
  *   x, y          bf16, or fp32 with MXFP4_NORM_X_F32; row pitches ldx, ldy elements (>= dim; one row alone: any),
- *                 aligned to the element.  Addresses of 16 bytes and dim and pitches of 8 elements are fastest.
+ *                 aligned to the element.  Addresses of 16 bytes and dim and pitches of 8 elements, in either type, are fastest.
  *   weight, bias  [samples, dim] dense, bf16 or (MXFP4_NORM_W_F32) fp32: one for each of `samples` equal runs of
- *                 consecutive rows; samples 1: for all of X.  rows % samples == 0.
+ *                 consecutive rows; samples 1: for all of X.  rows % samples == 0; at most 2^31 - 1 samples in the backward pass.
  *   mean, rstd    fp32[rows], mu and r for the backward pass; or both NULL
  *   dim           1 .. MXFP4_NORM_MAX_DIM;  rows == 0 does nothing
  * Backward: with a = dy g and xh = (x - mu) r, dx = r (a - mean(a) - xh mean(a xh)) in the type of x, and
@@ -633,7 +633,7 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
 /* ---- the gradients' norm ------------------------------------------------------------------
  * norm = sqrt(sum over all tensors of sum g^2) and factor = min(1, max_norm / (norm + 1e-6)), or 1
  * where max_norm is infinite, into out[0] and out[1] (device memory).  With MXFP4_GRAD_SCALE the
- * gradients are then multiplied by the factor in place, each product rounded once to its type; else
+ * gradients are then multiplied by the factor in place, each product formed in fp32 and rounded to its type; else
  * they are only read, and mxfp4_adamw takes the factor as its grad_factor.  The norm holds for
  * elements of every finite size; an infinite one gives norm inf and factor 0 (1 where max_norm is
  * infinite too), a NaN makes both NaN whatever max_norm is.

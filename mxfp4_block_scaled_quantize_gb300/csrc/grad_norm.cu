@@ -1,7 +1,7 @@
 // grad_norm.cu -- the norm of all gradients of a step, and scaling them by a factor on the device.
 //
 //   norm = sqrt(sum over all tensors of sum g^2),  factor = min(1, max_norm / (norm + 1e-6)),
-//   and, for clipping in place, g = factor g, rounded once.
+//   and, for clipping in place, g = factor g, in fp32 and rounded to its type.
 //
 // Sums.  A thread adds the squares of 32 elements (fp32: 16) in fp32 and everything above that in fp64: the
 // norm is off by a few 2^-24 at most however many elements there are, and the order is fixed, so

@@ -211,7 +211,9 @@ cudaError_t launch(NormArgs a, int sms, cudaStream_t stream) {
 // Elements a thread: 32 where rows come in 16-byte accesses, for the join of a row's warps costs each warp as much as
 // some 16 elements (8192 rows of 4096: 33 us with 16, 26 with 32; 16384 of 8192: 149 and 88); 16 where they do not, which the
 // registers of the single accesses' addresses fill, and 32 again for longer shifted rows (8192 rows of 2500 25 us with 16, 27 with
-// 32; of 4001 36 and 32; of 7001 69 and 52).  A warp's row wins up to 1024 elements: 32768 rows of 1024 take 26 us, 46 as
+// 32; of 4001 36 and 32; of 7001 69 and 52).  Single accesses of 4097 to 5120 columns: two CTAs of up to 320 threads an SM, where one of
+// the instance for 512 leaves half of it idle (8192 rows of 4100 in fp32 49 us, 69 so; of 5001 55 and 71; 300 of 4500 6.1 and 6.7; bf16
+// rows of 4500 whose y is not shifted alike 52 and 72).  A warp's row wins up to 1024 elements: 32768 rows of 1024 take 26 us, 46 as
 // a CTA's.  Now 5.3 TB/s at 4096, 6.1 at 8192, 4.7 for 4608 rows of 5120.
 template <bool kF32, NormAccess kAccess>
 cudaError_t launch(const NormArgs& a, int sms, cudaStream_t stream) {
