@@ -615,7 +615,7 @@ mxfp4_status mxfp4_adamw(int32_t count, const mxfp4_adamw_tensor* tensors, int32
  * NULL.  The same inputs give the same bits.  rows == 0 writes zeros to dw and db.
  *   workspace     mxfp4_layer_norm_workspace_bytes(dim) bytes, 16-byte aligned, scratch (NULL and 0 where dw
  *                 and db are NULL); calls that share one are ordered one after the other
- * dx must not overlap x or dy, nor y x. */
+ * y may be x, and dx may be x or dy, with their pitch; rows that overlap in any other way are refused. */
 #define MXFP4_NORM_X_F32 1
 #define MXFP4_NORM_W_F32 2
 #define MXFP4_NORM_ADD_ONE 4

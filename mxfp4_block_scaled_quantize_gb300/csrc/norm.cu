@@ -20,6 +20,18 @@ bool shape_ok(int64_t rows, int64_t dim, int64_t samples) {
 // One row alone may have any pitch.
 bool pitch_ok(int64_t ld, int64_t dim, int64_t rows) { return rows <= 1 || (ld >= dim && ld <= (int64_t{1} << 40)); }
 
+// Would a written row of `out` be another row's input in `in`?  A row is read whole before it is written, so `out` may be `in` itself; and
+// the two may lie side by side in rows of one pitch.
+bool mixed(const void* in, int64_t ldi, const void* out, int64_t ldo, int64_t rows, int64_t dim, int64_t size) {
+    if (rows == 0 || (in == out && (rows == 1 || ldi == ldo))) return false;
+    const __int128 a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out), row = dim * size;
+    const __int128 steps = rows - 1;
+    if (a + steps * ldi * size + row <= b || b + steps * ldo * size + row <= a) return false;
+    if (rows == 1 || ldi != ldo) return true;
+    const __int128 pitch = static_cast<__int128>(ldi) * size, between = ((b - a) % pitch + pitch) % pitch;
+    return between < row || pitch - between < row;
+}
+
 // How the kernels may access these tensors of rows (null: not there), and the rows from one to the next that is shifted alike.
 // Shifted accesses cost every row some masks and a launch its edge rows; they are for bf16 rows that CTAs take, and, of a
 // backward pass, for many elements.  us shifted and single: forward 8192 rows of 4100 39 and 71, 16000 of 6001 87 and 161, 1111 of
@@ -75,6 +87,7 @@ mxfp4_status mxfp4_layer_norm(const void* x, int64_t rows, int64_t dim, int64_t 
     if (!aligned_to(x, xe) || !aligned_to(y, xe) || !aligned_to(weight, we) || !aligned_to(bias, we) || !aligned_to(mean, 4) ||
         !aligned_to(rstd, 4))
         return MXFP4_ERR_MISALIGNED;
+    if (mixed(x, ldx, y, ldy, rows, dim, xe)) return MXFP4_ERR_INVALID_ARG;
     int sms = 0;
     uint32_t* err = nullptr;
     const int st = mxfp4::device_info(&sms, &err);
@@ -115,6 +128,7 @@ mxfp4_status mxfp4_layer_norm_backward(const void* dy, int64_t lddy, const void*
     if (!aligned_to(x, xe) || !aligned_to(dy, xe) || !aligned_to(dx, xe) || !aligned_to(weight, we) || !aligned_to(mean, 4) ||
         !aligned_to(rstd, 4) || !aligned_to(dw, 4) || !aligned_to(db, 4) || !aligned_to(workspace, 16))
         return MXFP4_ERR_MISALIGNED;
+    if (mixed(x, ldx, dx, lddx, rows, dim, xe) || mixed(dy, lddy, dx, lddx, rows, dim, xe)) return MXFP4_ERR_INVALID_ARG;
     mxfp4::NormArgs a;
     std::memset(&a, 0, sizeof(a));
     a.rows = rows;

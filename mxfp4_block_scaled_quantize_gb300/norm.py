@@ -15,7 +15,8 @@ from . import abi
 
 class LayerNorm:
     """Rows of `dim` elements in bf16 or fp32, at most max_rows a call, in at most max_samples samples.  The results
-    are views of the layer's own buffers and live until the next call."""
+    are views of the layer's own buffers and live until the next call; the next call may have one as its rows, whose place its
+    results then take (rows that overlap a result's in any other way are refused)."""
 
     def __init__(self, dim: int, max_rows: int, eps: float = 1e-5, dtype=torch.bfloat16, add_one: bool = False,
                  max_samples: int = 1, train: bool = True, device="cuda"):
