@@ -44,6 +44,12 @@ class LayerNorm:
             self._vectors = {}   # views of dw and db by the shape of the vectors, each made once
         self._last = None   # rows, and shapes and type of the last forward's vectors; None: no backward can follow
 
+    def __setstate__(self, state):
+        """A copy's gradients are views of its own buffers."""
+        self.__dict__.update(state)
+        if self.train:
+            self._vectors = {}
+
     def _check_rows(self, x, what):
         shape = x.shape
         if x.dtype is not self.dtype or len(shape) != 2 or shape[1] != self.dim or (x.stride(1) != 1 and self.dim > 1):
