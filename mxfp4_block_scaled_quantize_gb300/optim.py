@@ -51,11 +51,19 @@ class GradNorm:
         self._numel = [p.numel() for p in params]
         self._table = np.zeros(len(params), dtype=_GRADS)
         self._table["n"] = self._numel
-        self._grads = self._table["g"]   # a view and an address that every call uses
-        self._address = self._table.ctypes.data
+        self._find_table()
         self._workspace = torch.zeros(abi.mxfp4_grad_norm_workspace_bytes(len(params)), dtype=torch.uint8,
                                       device=params[0].device)
         self.out = torch.empty(2, dtype=torch.float32, device=params[0].device)
+
+    def _find_table(self):
+        self._grads = self._table["g"]   # a view and an address that every call uses
+        self._address = self._table.ctypes.data
+
+    def __setstate__(self, state):
+        """A copy's table is its own."""
+        self.__dict__.update(state)
+        self._find_table()
 
     def measure(self, grads, max_norm=math.inf, stream=None):
         """`out` for these gradients (contiguous, all fp32 or all bf16, in the order of the parameters), which
@@ -133,8 +141,17 @@ class AdamW:
         self._gpu = self.params[0].get_device() if self.params[0].is_cuda else None   # no tensor's get_device() is None
         self._numel = [p.numel() for p in self.params]
         self._table = np.zeros(len(self.params), dtype=_TABLE)
+        self._find_table()
+        self._fill()
+
+    def _find_table(self):
         self._grads = self._table["g"]   # a view and an address that every step uses
         self._address = self._table.ctypes.data
+
+    def __setstate__(self, state):
+        """A copy's table is its own, and of its own tensors."""
+        self.__dict__.update(state)
+        self._find_table()
         self._fill()
 
     @staticmethod
